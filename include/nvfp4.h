@@ -18,7 +18,10 @@
  *   8. the gated MLP input projection: the fused gate+up GEMM with its SwiGLU activation in
  *      the same launch, the result optionally leaving as NVFP4 for the down projection;
  *   9. batch-1 decode of one linear layer in one launch: 1 and 2 with the token's quantization
- *      inside the GEMM kernel.
+ *      inside the GEMM kernel;
+ *  10. the attention half of the hybrid model around the key-value cache: per-head norms of
+ *      queries and keys with the position rotation, appending keys and values to a paged cache
+ *      (FP8 as in 5, or bf16), and attention of new tokens over that cache.
  *
  * Sources: the element format (E2M1 values, one E4M3 scale per 16-element block) is from
  * "NVFP4 W4A4 Quantization Compresses 27B Hybrid Models" (thevalue.engineering), section
@@ -73,7 +76,8 @@ typedef enum {
   NVFP4_ERR_HIP = 4          /* a HIP runtime call or kernel launch failed */
 } nvfp4_status;
 
-typedef enum { NVFP4_F32 = 0, NVFP4_BF16 = 1 } nvfp4_dtype;
+/* NVFP4_E4M3 (OCP E4M3FN bytes under a calibrated scale) is a type of paged caches only. */
+typedef enum { NVFP4_F32 = 0, NVFP4_BF16 = 1, NVFP4_E4M3 = 2 } nvfp4_dtype;
 
 typedef enum {
   NVFP4_SCALE_PER_TENSOR = 0, /* s_g = max|x| over the tensor / 2688, written to [1]    */
@@ -372,6 +376,144 @@ int nvfp4_fp8_kv_quantize(const void* x, int x_dtype, int64_t n, const float* sc
                           void* stream);
 int nvfp4_fp8_kv_dequantize(const uint8_t* q, int64_t n, const float* scale, void* y, int y_dtype,
                             void* stream);
+
+/*
+ * Operators of the attention layers around a paged key-value cache (the calibrated FP8 cache of
+ * the codec above, or bf16).  A cache is a pool of pages; each sequence owns the pages its row of
+ * the page table lists, in order.
+ */
+
+/* Head vectors x[t, h, 0 .. dim-1]: rows of `dim` contiguous elements at t * token_stride + h *
+ * head_stride (elements), so that q, k and v may be column ranges of one fused projection.
+ * data 16-byte aligned; both strides (of a dimension longer than one) times the element size a
+ * multiple of 16 bytes. */
+typedef struct {
+  void* data;
+  int64_t heads;
+  int64_t token_stride;
+  int64_t head_stride;
+} nvfp4_heads;
+
+/* A paged cache and the batch of sequences it serves (host struct; pointers are device pointers).
+ *   k, v         page p is [kv_heads, page_size, head_dim] contiguous at p * page_stride
+ *                elements; NVFP4_E4M3 or NVFP4_BF16; 16-byte aligned, page strides times the element
+ *                size multiples of 16 bytes (k and v may be interleaved in one allocation).
+ *   page_size    tokens per page: a power of two, 16 to 1024.
+ *   num_pages    at least 1, below 2^31.
+ *   page_table   int32 [num_seqs, table_width], row pitch table_stride: token position t of
+ *                sequence s lies in page page_table[s][t / page_size], row t % page_size.  An entry
+ *                outside [0, num_pages) stands for no page: appends to it are dropped, its keys are
+ *                attended by nobody (entries past a sequence's length are never read).
+ *   k_scale, v_scale  device fp32, the calibrated scales of an E4M3 cache (finite and > 0, value =
+ *                E4M3(byte) * scale): one, or one per key-value head (scale_count = 1 or kv_heads).
+ *                Ignored for bf16.
+ *   cu_q         int32 [num_seqs + 1]: the new tokens of sequence s are rows cu_q[s] ..
+ *                cu_q[s+1] - 1 of q, k and v (non-decreasing; rows before cu_q[0] or from
+ *                cu_q[num_seqs] on belong to nobody and their outputs are left as they were).
+ *   kv_len       int32 [num_seqs]: tokens of the sequence in the cache, new ones included, at most
+ *                table_width * page_size: new token i of n has position kv_len - n + i.
+ * cu_q, kv_len and the page table are read on the device by the kernels, so a captured graph
+ * follows their contents; a value out of range is clamped and never makes a kernel access memory
+ * outside the operands. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t num_pages;
+  int64_t k_page_stride;
+  int64_t v_page_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int32_t dtype;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_seqs;
+  int32_t table_width;
+  int32_t scale_count;
+} nvfp4_paged_kv;
+
+/* The position rotation: channel pairs of the first `dim` channels of each head are turned by the
+ * angles of the token's position, read from a table of cos (dim/2 values) then sin (dim/2) per
+ * position, fp32 [rows, dim] contiguous, 16-byte aligned:
+ *   y[a] = x[a] cos_i - x[b] sin_i,  y[b] = x[b] cos_i + x[a] sin_i,  i < dim/2,
+ * (a, b) = (i, i + dim/2), or (2i, 2i + 1) with interleaved = 1.  dim is a multiple of 16, at most
+ * the head dimension; the other channels pass through.
+ *   positions    device int32, one per token (NULL: see the entry point).  A position outside
+ *                [0, rows) has no angles: the rotated channels of that token become NaN. */
+typedef struct {
+  const float* table;
+  int64_t rows;
+  const int32_t* positions;
+  int32_t dim;
+  int32_t interleaved;
+} nvfp4_rope;
+
+/*
+ * Norms of queries and keys for each head and the position rotation, in one pass: the input side
+ * of the hybrid model's attention layers.  Per head vector, in fp32 and rounded once on the way out:
+ *   x <- x * w / sqrt(mean(x^2) + eps)   (when that tensor's weight is given)
+ *   x <- rotation of x                     (when rope is given; rope->positions required)
+ *   tokens >= 0 (0 is a no-op), head_dim a multiple of 16, 16 to 512.
+ *   q, k         inputs of x_dtype (NVFP4_BF16 or NVFP4_F32); k may be NULL.
+ *   q_weight, k_weight  device fp32 [head_dim], 16-byte aligned, or NULL; eps >= 0.
+ *   q_out, k_out outputs of out_dtype (NVFP4_BF16: round to nearest even, or NVFP4_F32), heads as
+ *                the inputs'; may be the inputs themselves if type and layout are equal, and must
+ *                not overlap them otherwise.  k_out NULL exactly when k is.
+ */
+int nvfp4_qk_norm_rope(int64_t tokens, int64_t head_dim, int x_dtype, const nvfp4_heads* q, const nvfp4_heads* k,
+                       const float* q_weight, const float* k_weight, float eps, const nvfp4_rope* rope, int out_dtype,
+                       const nvfp4_heads* q_out, const nvfp4_heads* k_out, void* stream);
+
+/*
+ * Append the new tokens' keys and values to the cache, keys normed and rotated on the way, in one
+ * launch; with q given, the queries leave normed and rotated in the same launch.
+ *   k: norm (k_weight not NULL) and rotation (rope not NULL) as nvfp4_qk_norm_rope, v as it is; both
+ *      stored at the token's position: E4M3 as nvfp4_fp8_kv_quantize encodes the fp32 value under the
+ *      head's scale, or bf16 rounded to nearest even.
+ *   rope->positions NULL: a token's position is its place in its sequence.
+ *   Tokens at a negative place, past the page table or on an invalid page are not stored.  Two tokens
+ *   that share a place (sequences that share a page) leave either one's bytes.
+ *   tokens >= 0 (0 is a no-op): rows of q, k, v.  kv->head_dim a multiple of 16, 16 to 512.
+ *   k, v         of x_dtype, kv->kv_heads heads.
+ *   q, q_out     both NULL, or q of x_dtype and q_out of q_out_dtype as in nvfp4_qk_norm_rope.
+ */
+int nvfp4_kv_append(const nvfp4_paged_kv* kv, int64_t tokens, int x_dtype, const nvfp4_heads* k, const nvfp4_heads* v,
+                    const float* k_weight, float eps, const nvfp4_rope* rope, const nvfp4_heads* q,
+                    const float* q_weight, int q_out_dtype, const nvfp4_heads* q_out, void* stream);
+
+/*
+ * Attention of new tokens over the paged cache (their own keys and values appended before):
+ *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j),  key-value head h / (q heads /
+ * kv heads), over the keys j the token sees: with causal = 1 those at positions up to its own,
+ * and with window > 0 only the last `window` of them; with causal = 0 all kv_len (window must be 0).
+ * One call takes any mix of single tokens and chunks.  A token that sees no key (an empty
+ * sequence, a position below 0, no valid page), or whose every score is -inf, gets zeros and lse =
+ * -inf.  Keys a token does not see have no influence, whatever their bytes hold (NaN, infinities).
+ *   q            bf16, heads a multiple of kv->kv_heads, at most 256 per key-value head.
+ *   head_dim     64, 128 or 256 (others: NVFP4_ERR_UNSUPPORTED).
+ *   scale        > 0 and finite, usually head_dim^-0.5.
+ *   max_q        the largest number of new tokens of one sequence, or 0 if not known: a hint that
+ *                picks kernels.  Results do not depend on its truth, speed does.
+ *   out          bf16 (round to nearest even), heads as q; must not overlap the inputs.
+ *   lse          device fp32 [tokens, q heads] contiguous, or NULL: ln sum_j exp(scale q.k_j).
+ *   workspace    device, 16-byte aligned, nvfp4_paged_attention_workspace_size() bytes for the same
+ *                arguments; contents need no initialisation and are clobbered.
+ * Scores, softmax statistics and sums are fp32; probabilities are rounded to fp16 (E4M3 cache) or
+ * bf16 (bf16 cache) for their product with V.  Deterministic: the same inputs and arguments
+ * give the same bits.
+ */
+int nvfp4_paged_attention(const nvfp4_paged_kv* kv, int64_t tokens, int64_t max_q, const nvfp4_heads* q, float scale,
+                          int causal, int64_t window, const nvfp4_heads* out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace nvfp4_paged_attention needs for these sizes, whatever the lengths: partial
+ * results of a key axis split over workgroups.  0 for bad sizes. */
+size_t nvfp4_paged_attention_workspace_size(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
+                                            int64_t kv_heads, int64_t head_dim, int dtype);
 
 /* Static description of a status code. */
 const char* nvfp4_status_string(int status);

@@ -26,6 +26,12 @@ Entry points (same names as the C ABI):
   gemm_swiglu(a, w_codes, w_scales, w_globals, h_dtype, h_global)
                                          -> (h, h as NVFP4): the fused gate+up GEMM with its
                                             SwiGLU activation, h = silu(gate) * up
+  qk_norm_rope(q, k, q_weight, k_weight, rope, positions)
+                                         -> (q, k): per-head norms and the position rotation
+  kv_append(kv, k, v, kv_len, cu_q, ...) -> new keys (normed, rotated) and values into a paged
+                                            cache (PagedKV: FP8 or bf16), queries in the same launch
+  paged_attention(q, kv, kv_len, cu_q, ...)
+                                         -> attention of new tokens over the paged cache
 """
 from __future__ import annotations
 
@@ -39,6 +45,7 @@ import torch
 __all__ = [
     "NVFP4Tensor", "NVFP4Error", "quantize", "gemm", "gemm_fused_segments", "gemm_nvfp4_out", "gemm_fused_gdn_gates", "MXFP4Tensor", "to_mxfp4", "mxfp4_gemm",
     "fp8_kv_quantize", "fp8_kv_dequantize", "interleave_gate_up", "gemm_swiglu", "decode_linear",
+    "PagedKV", "qk_norm_rope", "kv_append", "paged_attention",
     "library_path", "lib",
     "PER_TENSOR", "PER_ROW", "GIVEN", "MAX_SEGMENTS", "EXPORTED_SYMBOLS",
 ]
@@ -48,15 +55,38 @@ _LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
 PER_TENSOR, PER_ROW, GIVEN = 0, 1, 2
 _MODES = {"per_tensor": PER_TENSOR, "per_row": PER_ROW, "given": GIVEN}
-_F32, _BF16 = 0, 1
+_F32, _BF16, _E4M3 = 0, 1, 2
 MAX_SEGMENTS = 64
 EXPORTED_SYMBOLS = (
     "nvfp4_quantize", "nvfp4_quantize_workspace_size", "nvfp4_quantize_no_alloc", "nvfp4_gemm", "nvfp4_gemm_fused_segments",
     "nvfp4_gemm_nvfp4_out", "nvfp4_gemm_fused_gdn_gates", "nvfp4_to_mxfp4", "nvfp4_mxfp4_gemm",
     "nvfp4_gemm_workspace_size", "nvfp4_fp8_kv_quantize", "nvfp4_fp8_kv_dequantize",
-    "nvfp4_interleave_gate_up", "nvfp4_gemm_swiglu", "nvfp4_decode_linear", "nvfp4_status_string",
+    "nvfp4_interleave_gate_up", "nvfp4_gemm_swiglu", "nvfp4_decode_linear", "nvfp4_qk_norm_rope", "nvfp4_kv_append",
+    "nvfp4_paged_attention", "nvfp4_paged_attention_workspace_size", "nvfp4_status_string",
     "nvfp4_version",
 )
+
+
+class _Heads(ctypes.Structure):
+    """nvfp4_heads"""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    """nvfp4_rope"""
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class _PagedKV(ctypes.Structure):
+    """nvfp4_paged_kv"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("table_width", ctypes.c_int32), ("scale_count", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -97,6 +127,15 @@ def _load() -> ctypes.CDLL:
     L.nvfp4_interleave_gate_up.restype = i32
     L.nvfp4_gemm_swiglu.argtypes = [i64, i64, i64, p, p, p, i32, p, p, p, p, i32, i64, p, p, p, p]
     L.nvfp4_gemm_swiglu.restype = i32
+    f32, heads, rope, cache = ctypes.c_float, ctypes.POINTER(_Heads), ctypes.POINTER(_Rope), ctypes.POINTER(_PagedKV)
+    L.nvfp4_qk_norm_rope.argtypes = [i64, i64, i32, heads, heads, p, p, f32, rope, i32, heads, heads, p]
+    L.nvfp4_qk_norm_rope.restype = i32
+    L.nvfp4_kv_append.argtypes = [cache, i64, i32, heads, heads, p, f32, rope, heads, p, i32, heads, p]
+    L.nvfp4_kv_append.restype = i32
+    L.nvfp4_paged_attention.argtypes = [cache, i64, i64, heads, f32, i32, i64, heads, p, p, sz, p]
+    L.nvfp4_paged_attention.restype = i32
+    L.nvfp4_paged_attention_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i32]
+    L.nvfp4_paged_attention_workspace_size.restype = sz
     L.nvfp4_gemm_workspace_size.argtypes = [i64, i64, i64]
     L.nvfp4_gemm_workspace_size.restype = sz
     L.nvfp4_status_string.argtypes = [i32]
@@ -530,3 +569,210 @@ def fp8_kv_dequantize(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dty
     st = lib.nvfp4_fp8_kv_dequantize(_ptr(q), q.numel(), _ptr(scale), _ptr(y), _y_dtype(out_dtype), _stream(q.device))
     _check(st, "nvfp4_fp8_kv_dequantize")
     return y
+
+
+# ---- attention layers around a paged key-value cache ---------------------------------------------
+
+
+@dataclass
+class PagedKV:
+    """A paged key-value cache and its page table, all on one GPU.
+
+    k, v        [pages, kv_heads, page_size, head_dim]: uint8 (E4M3FN bytes under the calibrated
+                scales) or bfloat16; contiguous but for the page stride, so both may be halves of
+                one allocation ``[pages, 2, kv_heads, page_size, head_dim]``.
+    page_table  int32 [sequences, width]: the pages of each sequence in order; an entry outside
+                [0, pages) (say -1) stands for no page.
+    k_scale, v_scale  float32, one element or one per key-value head (FP8 caches only)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    page_table: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+
+def _heads_arg(t: torch.Tensor, name: str, dtypes: tuple, dev: torch.device, tokens: int | None = None,
+               heads: int | None = None, dim: int | None = None) -> _Heads:
+    """A [tokens, heads, dim] operand whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name}: a tensor [tokens, heads, dim]")
+    n, h, d = t.shape
+    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{tokens}, {'heads' if heads is None else heads}, {dim}]")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(x) for x in dtypes)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and n * h > 0:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name}: a tensor on {dev}")
+    return _Heads(t.data_ptr(), h, st, sh)
+
+
+def _i32_arg(t: torch.Tensor, name: str, numel: int, dev: torch.device) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 [{numel}]")
+    if t.shape[0] != numel:
+        raise ValueError(f"{name}: {t.shape[0]} elements, expected {numel}")
+    if t.device != dev:
+        raise ValueError(f"{name}: a tensor on {dev}")
+    return t.data_ptr()
+
+
+def _cache_arg(kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, dev: torch.device) -> _PagedKV:
+    if not isinstance(kv, PagedKV):
+        raise ValueError("kv: a PagedKV")
+    k, v, table = kv.k, kv.v, kv.page_table
+    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("kv.k, kv.v: tensors [pages, kv_heads, page_size, head_dim] of one shape")
+    if k.dtype not in (torch.uint8, torch.bfloat16) or v.dtype != k.dtype:
+        raise ValueError("kv.k, kv.v: both uint8 (E4M3 bytes) or both bfloat16")
+    pages, heads, page, dim = k.shape
+    inner = (page * dim, dim, 1)
+    if pages > 0 and (k.stride()[1:] != inner or v.stride()[1:] != inner):
+        raise ValueError("kv.k, kv.v: every page must be contiguous")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"kv: tensors on {dev}")
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2:
+        raise ValueError("kv.page_table: int32 [sequences, width]")
+    seqs, width = table.shape
+    if seqs * width > 0 and table.stride(1) != 1 and width > 1:
+        raise ValueError("kv.page_table: rows must be contiguous")
+    if table.device != dev:
+        raise ValueError(f"kv.page_table: a tensor on {dev}")
+    c = _PagedKV(k.data_ptr(), v.data_ptr(), pages, k.stride(0), v.stride(0), table.data_ptr(), table.stride(0), None, None,
+                 _i32_arg(cu_q, "cu_q", seqs + 1, dev), _i32_arg(kv_len, "kv_len", seqs, dev),
+                 _E4M3 if k.dtype == torch.uint8 else _BF16, heads, dim, page, seqs, width, 0)
+    if c.dtype == _E4M3:
+        if kv.k_scale is None or kv.v_scale is None:
+            raise ValueError("kv.k_scale, kv.v_scale: an FP8 cache needs its calibrated scales")
+        _require_f32(kv.k_scale, (1, heads), "kv.k_scale", dev)
+        _require_f32(kv.v_scale, kv.k_scale.numel(), "kv.v_scale", dev)
+        c.k_scale, c.v_scale, c.scale_count = kv.k_scale.data_ptr(), kv.v_scale.data_ptr(), kv.k_scale.numel()
+    return c
+
+
+def _weight_arg(w: torch.Tensor | None, name: str, dim: int, dev: torch.device) -> int | None:
+    if w is None:
+        return None
+    _require_f32(w, dim, name, dev)
+    return w.data_ptr()
+
+
+def _rope_arg(rope: torch.Tensor | None, positions: torch.Tensor | None, tokens: int, interleaved: bool,
+              dev: torch.device):
+    if rope is None:
+        _require(positions is None, "positions without a rope table")
+        return None
+    if not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
+        raise ValueError("rope: contiguous float32 [positions, rotated channels], cos then sin")
+    if rope.device != dev:
+        raise ValueError(f"rope: a tensor on {dev}")
+    pos = None if positions is None else _i32_arg(positions, "positions", tokens, dev)
+    return _Rope(rope.data_ptr(), rope.shape[0], pos, rope.shape[1], int(interleaved))
+
+
+def _run(dev: torch.device, what: str, fn, *args) -> None:
+    """fn(*args, stream) on dev's current stream, with dev current: the default stream belongs to
+    whichever device is."""
+    _on_gpu(dev)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _stream(dev)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), what)
+
+
+_X_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, rope: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                 out_dtype: torch.dtype | None = None, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Norm each head vector of q [T, Hq, D] and k [T, Hk, D] (bf16 or fp32, strided views welcome)
+    by its root mean square and the fp32 weight [D] (where given), and rotate its first R channels by the
+    angles of its token's position: rope fp32 [positions, R], cos (R/2) then sin (R/2) of every
+    position; positions int32 [T].  Channel i turns with i + R/2, or 2i with 2i + 1 when ``interleaved``.
+    Returns (q, k) of out_dtype (default: the input's); q_out, k_out may be the inputs themselves."""
+    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q: a tensor [tokens, heads, dim]")
+    dev, (T, Hq, D) = q.device, q.shape
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    qa = _heads_arg(q, "q", _X_DTYPES, dev)
+    ka = None if k is None else _heads_arg(k, "k", (q.dtype,), dev, T, None, D)
+    _require(rope is None or positions is not None, "rope needs positions")
+    _require(k is not None or (k_weight is None and k_out is None), "k_weight or k_out without k")
+    ra = _rope_arg(rope, positions, T, interleaved, dev)
+    qw, kw = _weight_arg(q_weight, "q_weight", D, dev), _weight_arg(k_weight, "k_weight", D, dev)
+    q_out = torch.empty((T, Hq, D), dtype=out_dtype, device=dev) if q_out is None else q_out
+    qo = _heads_arg(q_out, "q_out", (out_dtype,), dev, T, Hq, D)
+    ko = None
+    if k is not None:
+        k_out = torch.empty((T, k.shape[1], D), dtype=out_dtype, device=dev) if k_out is None else k_out
+        ko = _heads_arg(k_out, "k_out", (out_dtype,), dev, T, k.shape[1], D)
+    _run(dev, "nvfp4_qk_norm_rope", lib.nvfp4_qk_norm_rope, T, D, _BF16 if q.dtype == torch.bfloat16 else _F32, qa, ka, qw,
+         kw, eps, ra, _y_dtype(out_dtype), qo, ko)
+    return q_out, k_out
+
+
+def kv_append(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor,
+              k_weight: torch.Tensor | None = None, rope: torch.Tensor | None = None,
+              positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+              q: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+              q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Append the new tokens' keys and values [T, Hk, D] (bf16 or fp32) to the cache in one launch: keys
+    normed (k_weight given) and rotated (rope given) as in ``qk_norm_rope``, both stored as the cache's
+    type.  Rows cu_q[s] .. cu_q[s+1] - 1 are the new tokens of sequence s (int32 [S + 1]) and kv_len[s] its
+    length with them (int32 [S]).  positions int32 [T] (default: each token's place in its sequence).  With
+    q [T, Hq, D] the queries leave normed and rotated in the same launch: returns q_out (bf16 unless a
+    q_out of fp32 is given), else None."""
+    _require(isinstance(k, torch.Tensor) and k.dim() == 3, "k: a tensor [tokens, kv_heads, dim]")
+    dev, T = k.device, k.shape[0]
+    c = _cache_arg(kv, kv_len, cu_q, dev)
+    ka = _heads_arg(k, "k", _X_DTYPES, dev, T, c.kv_heads, c.head_dim)
+    va = _heads_arg(v, "v", (k.dtype,), dev, T, c.kv_heads, c.head_dim)
+    ra = _rope_arg(rope, positions, T, interleaved, dev)
+    kw, qw = _weight_arg(k_weight, "k_weight", c.head_dim, dev), _weight_arg(q_weight, "q_weight", c.head_dim, dev)
+    qa = qo = None
+    qdt = _BF16
+    if q is not None:
+        qa = _heads_arg(q, "q", (k.dtype,), dev, T, None, c.head_dim)
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+        qo = _heads_arg(q_out, "q_out", _X_DTYPES, dev, T, q.shape[1], c.head_dim)
+        qdt = _BF16 if q_out.dtype == torch.bfloat16 else _F32
+    else:
+        _require(q_weight is None and q_out is None, "q_weight or q_out without q")
+    _run(dev, "nvfp4_kv_append", lib.nvfp4_kv_append, c, T, _BF16 if k.dtype == torch.bfloat16 else _F32, ka, va, kw, eps,
+         ra, qa, qw, qdt, qo)
+    return q_out
+
+
+def paged_attention(q: torch.Tensor, kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, scale: float | None = None,
+                    causal: bool = True, window: int = 0, max_q: int = 0, out: torch.Tensor | None = None,
+                    return_lse: bool = False, workspace: torch.Tensor | None = None):
+    """Attention of the new tokens' queries q [T, Hq, D] (bf16) over the paged cache, their own keys
+    and values appended before.  Row cu_q[s] + i is token i of sequence s, at position kv_len[s] - n + i of
+    its n new tokens; it sees the keys up to its own (causal), the last ``window`` of them if window > 0, or
+    all kv_len[s] (causal=False).  Any mix of single tokens and chunks.  A token that sees no key gets zeros.
+    max_q: the longest chunk, if known; a hint for speed only.  workspace: uint8, at least
+    ``lib.nvfp4_paged_attention_workspace_size(...)`` bytes (allocated when None).
+    Returns out [T, Hq, D] bf16, or (out, lse [T, Hq] fp32 = ln sum exp(scale q.k))."""
+    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q: a tensor [tokens, heads, dim]")
+    dev, (T, Hq, D) = q.device, q.shape
+    c = _cache_arg(kv, kv_len, cu_q, dev)
+    qa = _heads_arg(q, "q", (torch.bfloat16,), dev, T, Hq, c.head_dim)
+    _require(c.kv_heads > 0 and Hq % c.kv_heads == 0, "q heads must be a multiple of the cache's")
+    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    oa = _heads_arg(out, "out", (torch.bfloat16,), dev, T, Hq, D)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    need = lib.nvfp4_paged_attention_workspace_size(T, max_q, c.num_seqs, Hq, c.kv_heads, D, c.dtype)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    else:
+        _require(isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
+                 "workspace: contiguous uint8")
+        _require(workspace.device == dev, f"workspace: a tensor on {dev}")
+    _run(dev, "nvfp4_paged_attention", lib.nvfp4_paged_attention, c, T, max_q, qa, D ** -0.5 if scale is None else scale,
+         int(causal), window, oa, _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return (out, lse) if return_lse else out

@@ -12,7 +12,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
-SOURCES = ["api.hip", "device.hip", "quantize.hip", "gemm.hip", "kv_fp8.hip", "mxfp4.hip"]
+SOURCES = ["api.hip", "device.hip", "quantize.hip", "gemm.hip", "kv_fp8.hip", "mxfp4.hip", "rope_append.hip", "paged_attention.hip", "paged_api.hip"]
 # The measurement script's calibration kernels (streaming read, copy, MFMA loop): a library of
 # their own, outside the hot path's C ABI.
 CALIB_LIB = os.path.join(HERE, "libnvfp4_calib.so")

@@ -29,7 +29,7 @@
 // huge, infinite or NaN scales).
 // Dequantize uses the hardware E4M3 decode (v_cvt_pk_f32_fp8, exact, NaN for 0x7F / 0xFF)
 // and one binary32 multiply.
-#include "nvfp4_device.h"
+#include "fp8_device.h"
 #include "nvfp4_internal.h"
 
 namespace nvfp4 {
@@ -37,45 +37,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kKvThreads = 256;
-
-__device__ __forceinline__ uint32_t fp8_encode(float x, float s) {
-  const float t = x / s;                                    // IEEE binary32 division
-  const float a = __builtin_fabsf(t);
-  if (a != a) return 0x7Fu;
-  return e4m3_encode_rne_sat(a) | ((__float_as_uint(t) >> 24) & 0x80u);
-}
-
-// Operands of the fast quantize path: s, r = fl32(1 / s) and the clamp fl32(440 s).
-struct FastQuotient {
-  float s, r, lim;
-};
-
-__device__ __forceinline__ bool fast_scale(float s) { return s >= 0x1p-64f && s <= 0x1p64f; }
-
-__device__ __forceinline__ float fast_quotient(float x, const FastQuotient& f) {
-  return div_rn(__builtin_amdgcn_fmed3f(x, -f.lim, f.lim), f.s, f.r);
-}
-
-// Bytes of e[0..3] in one dword (element 0 in the low byte), fast path, non-NaN inputs.
-__device__ __forceinline__ uint32_t fp8x4_fast(const float* e, const FastQuotient& f) {
-  uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fast_quotient(e[0], f), fast_quotient(e[1], f), 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fast_quotient(e[2], f), fast_quotient(e[3], f), (int)w, true);
-}
-
-__device__ __forceinline__ uint32_t fp8x4_exact(const float* e, float s) {
-  return fp8_encode(e[0], s) | fp8_encode(e[1], s) << 8 | fp8_encode(e[2], s) << 16 | fp8_encode(e[3], s) << 24;
-}
-
-// fl32(E4M3(byte) * s) of the four bytes of w (byte 0 first): the hardware decode is exact
-// and gives NaN for 0x7F / 0xFF, which the multiply keeps.
-__device__ __forceinline__ void fp8x4_decode(int w, float s, float* e) {
-  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
-  e[0] = lo[0] * s;
-  e[1] = lo[1] * s;
-  e[2] = hi[0] * s;
-  e[3] = hi[1] * s;
-}
 
 __device__ __forceinline__ void load8(const uint16_t* x, int64_t v, float (&e)[8]) {
   const uint4 w = reinterpret_cast<const uint4*>(x)[v];

@@ -1,0 +1,1077 @@
+// Attention of new tokens over the paged key-value cache for gfx950.
+//
+// What is computed, per query row (token t, head h; key-value head h / group):
+//   out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j) over the keys j the row sees,
+// in one pass over the keys with a running maximum m and sum l (exponentials in base 2, log2 e and the
+// key scale folded into the factor c):  s_j = q . k_j,  m' = max(m, s),  l <- l 2^{(m - m') c} + sum 2^{(s - m') c},
+// O <- O 2^{(m - m') c} + sum 2^{(s - m') c} v_j,  out = O / l * v_scale,  lse = (m c + log2 l) ln 2.
+// m, l, O and the scores are fp32.  The factor by which old values are scaled down is applied only when
+// the maximum grows by more than 2^8 (kLazy): until then probabilities are at most 2^8 instead of 1,
+// which neither fp32 sums nor fp16 probabilities (largest 65504) notice.
+//
+// Operands of the matrix instructions.  E4M3 values are exact in bf16 and in fp16.  Scores: bf16 queries
+// (as given) times bf16 keys, exact products.  Output: probabilities are rounded to fp16 next to fp16
+// values for an E4M3 cache (2^-12 relative), to bf16 for a bf16 cache, whose values may exceed
+// fp16's range.
+//
+// The matrix products are taken transposed, S^T = K Q^T and O^T = V^T P^T: a lane then holds scores of
+// ONE query row, reductions over keys stay mostly in the lane, and the score registers are the
+// probability operand of the second product without any movement between lanes (the order of the keys
+// in its K dimension is free as long as V^T is read in the same one).
+//
+// The rows of one sequence and key-value head are its new tokens times the group's query heads, packed:
+// row r is token r / group, head r % group, so all of them share the keys read.  Two kernels:
+//   stream_kernel   few rows (16 or 32): HBM-bound.  Every wavefront streams its own keys straight
+//                   from memory into matrix-operand registers, no LDS in the loop, no barriers.
+//   tile_kernel     many rows (128 or more): MFMA-bound.  Keys and values are converted once per
+//                   workgroup on their way into LDS.
+// Tiles of rows are found on the device: slot index -> sequence by a search over cu_q, since
+// floor(cu_q[s] group / BM) + s is a monotone numbering that leaves every sequence enough slots.
+//
+// Split of the key axis: with few row tiles, the key blocks of all (head, slot) segments form one
+// sequence that is cut into equal shares, one per workgroup, from the lengths as they are on the device.  A
+// segment inside one share is finished there; a cut one leaves (m, l, O) per share in the workspace,
+// joined by combine_kernel in a fixed order.
+//
+// Keys outside [0, kv_len) or on an invalid page are zeroed (V) and masked (scores); keys only some rows of
+// a tile see are masked by selection.  0 * inf would still reach rows that do not see the key, so
+// non-finite values of V are taken out of the product and added afterwards to the rows that do see
+// them (any positive probability times inf or NaN is inf or NaN).
+#include "paged_device.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxSlots = 1024;       // row tiles a split launch can plan
+constexpr int kStreamBlock = 128;     // keys per step of stream_kernel: 32 per wavefront
+constexpr int kTileBlock = 64;        // keys per step of tile_kernel
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kLazy = 8.0f;
+constexpr float kLn2 = 0.693147180559945f;
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// What a launch adds to the call's arguments.
+struct Launch {
+  int32_t slots;             // row tiles, an upper bound
+  int32_t rows_lo, rows_hi;  // sequences with rows in (rows_lo, rows_hi] are this launch's
+  int32_t split;             // 0: one workgroup per (slot, head)
+  int32_t workgroups;        // of a split launch
+  int32_t min_blocks;        // smallest share
+  int32_t* plan;             // [slots + 2]: first block of every slot, all blocks, blocks per share
+  float2* ml;                // [2 workgroups][BM]: m c, l
+  float* po;                 // [2 workgroups][BM][D]: O
+};
+
+// One row tile of one sequence.
+struct Tile {
+  int s, c0, n, len;         // sequence, its first row of q, new tokens, cache length
+  int row0, rows;            // first packed row, rows in the tile
+  int pos0;                  // position of the sequence's first new token (may be negative)
+  int hi_min, lo_max;        // keys in [lo_max, hi_min) are seen by every row
+  int block0, blocks;        // first key block and their number (at least 1)
+};
+
+__device__ __forceinline__ int cu_at(const AttentionArgs& a, int j) { return clamp_int(a.cu_q[j], 0, a.tokens); }
+
+template <int BM>
+__device__ __forceinline__ int first_slot(const AttentionArgs& a, int s) {
+  return (int)((uint32_t)(cu_at(a, s) * a.group) / BM) + s;
+}
+
+// Tile `i` of sequence s; false if there is none or it is another launch's.
+template <int BM, int KB>
+__device__ __forceinline__ bool tile_of(const AttentionArgs& a, const Launch& l, int s, int i, Tile& t) {
+  t.s = s;
+  t.c0 = cu_at(a, s);
+  t.n = clamp_int(a.cu_q[s + 1], t.c0, a.tokens) - t.c0;
+  const int all = t.n * a.group;
+  if (all <= l.rows_lo || all > l.rows_hi || i < 0 || (int64_t)i * BM >= all) return false;
+  t.len = clamp_int(a.kv_len[s], 0, a.table_width << a.page_shift);
+  t.row0 = i * BM;
+  t.rows = all - t.row0 < BM ? all - t.row0 : BM;
+  t.pos0 = t.len - t.n;
+  const int first = (int)fastdiv((uint32_t)t.row0, a.div_group);
+  const int last = (int)fastdiv((uint32_t)(t.row0 + t.rows - 1), a.div_group);
+  int hi = t.len, lo = 0;
+  t.hi_min = t.len;
+  t.lo_max = 0;
+  if (a.causal) {
+    hi = clamp_int(t.pos0 + last + 1, 0, t.len);
+    t.hi_min = clamp_int(t.pos0 + first + 1, 0, t.len);
+    if (a.window > 0) {
+      const int64_t l0 = (int64_t)t.pos0 + first - a.window + 1, l1 = (int64_t)t.pos0 + last - a.window + 1;
+      lo = l0 > 0 ? (int)l0 : 0;
+      t.lo_max = l1 > 0 ? (int)l1 : 0;
+    }
+  }
+  t.block0 = lo / KB;
+  t.blocks = hi > lo ? (hi + KB - 1) / KB - t.block0 : 1;
+  return true;
+}
+
+// Keys [lo, hi) that packed row r of the tile's sequence sees; none for rows past the tile.
+__device__ __forceinline__ void row_range(const AttentionArgs& a, const Tile& t, int r, int& lo, int& hi) {
+  lo = 0;
+  hi = 0;
+  if (r >= t.row0 + t.rows) return;
+  hi = t.len;
+  if (a.causal) {
+    const int pos = t.pos0 + (int)fastdiv((uint32_t)r, a.div_group);
+    hi = clamp_int(pos + 1, 0, t.len);
+    if (a.window > 0) {
+      const int64_t l0 = (int64_t)pos - a.window + 1;
+      lo = l0 > 0 ? (int)l0 : 0;
+    }
+  }
+}
+
+// Page of the 16-aligned key group at `key` (16 keys never straddle a page): its number, or -1.
+__device__ __forceinline__ int page_of(const AttentionArgs& a, const Tile& t, int key) {
+  if (key >= t.len) return -1;
+  const int p = a.page_table[t.s * a.table_stride + (key >> a.page_shift)];
+  return (uint32_t)p < (uint32_t)a.num_pages ? p : -1;
+}
+
+// ---- splitting the key axis ----------------------------------------------------------------------
+
+// First block of every slot (pre[0 .. slots], pre[slots] = all blocks of one head), by the whole workgroup.
+template <int BM, int KB>
+__device__ __forceinline__ void make_plan(const AttentionArgs& a, const Launch& l, int* pre, int* wave_sum) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kPer = kMaxSlots / kThreads;
+  for (int j = tid; j < kMaxSlots; j += kThreads) pre[j] = 0;
+  __syncthreads();
+  Tile t;
+  if (a.num_seqs <= 16) {              // few sequences: threads over the tiles of each
+    for (int s = 0; s < a.num_seqs; ++s) {
+      const int base = first_slot<BM>(a, s);
+      for (int i = tid; base + i < l.slots && tile_of<BM, KB>(a, l, s, i, t); i += kThreads) pre[base + i] = t.blocks;
+    }
+  } else {                             // many: one thread per sequence, few tiles each
+    for (int s = tid; s < a.num_seqs; s += kThreads) {
+      const int base = first_slot<BM>(a, s);
+      for (int i = 0; base + i < l.slots && tile_of<BM, KB>(a, l, s, i, t); ++i) pre[base + i] = t.blocks;
+    }
+  }
+  __syncthreads();
+  int v[kPer], sum = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    v[j] = pre[tid * kPer + j];
+    sum += v[j];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const int o = __shfl_up(inc, m, 64);
+    if (lane >= m) inc += o;
+  }
+  if (lane == 63) wave_sum[wave] = inc;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < wave; ++w) at += wave_sum[w];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    pre[tid * kPer + j] = at;
+    at += v[j];
+  }
+  if (tid == kThreads - 1) pre[kMaxSlots] = at;
+  __syncthreads();
+}
+
+// Calls work(tile, head, first block, end block, partial) for every piece of this workgroup; partial < 0:
+// the whole tile.  Uniform over the workgroup.
+template <int BM, int KB, typename Work>
+__device__ __forceinline__ void for_pieces(const AttentionArgs& a, const Launch& l, int* pre, int* wave_sum, Work work) {
+  Tile t;
+  if (!l.split) {
+    const int h = blockIdx.x % a.kv_heads;
+    const int slot = l.slots - 1 - (int)(blockIdx.x / a.kv_heads);     // late (long) tiles first
+    const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
+    if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t)) return;
+    work(t, h, 0, t.blocks, -1);
+    return;
+  }
+  make_plan<BM, KB>(a, l, pre, wave_sum);
+  const int all = pre[kMaxSlots];
+  const int64_t total = (int64_t)all * a.kv_heads;
+  const int64_t share = (total + l.workgroups - 1) / l.workgroups;
+  const int per = share > l.min_blocks ? (int)share : l.min_blocks;
+  if (blockIdx.x == 0) {
+    for (int j = threadIdx.x; j < l.slots; j += kThreads) l.plan[j] = pre[j];
+    if (threadIdx.x == 0) {
+      l.plan[l.slots] = all;
+      l.plan[l.slots + 1] = per;
+    }
+  }
+  // neighbouring shares (the same head's keys) on one XCD: workgroups are dealt to the 8 XCDs in turn
+  const int w = (blockIdx.x & 7) * (l.workgroups >> 3) + (blockIdx.x >> 3);
+  int64_t u = (int64_t)w * per;
+  const int64_t end = u + per < total ? u + per : total;
+  while (u < end) {
+    const int h = (int)(u / all), rem = (int)(u - (int64_t)h * all);
+    int lo = 0, hi = l.slots;                     // pre[lo] <= rem < pre[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= rem) lo = mid; else hi = mid;
+    }
+    const int count = pre[lo + 1] - pre[lo], off = rem - pre[lo];
+    const int take = end - u < count - off ? (int)(end - u) : count - off;
+    const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= lo; });
+    if (s >= 0 && tile_of<BM, KB>(a, l, s, lo - first_slot<BM>(a, s), t))
+      work(t, h, off, off + take, take == count ? -1 : 2 * w + (off > 0 ? 0 : 1));
+    u += take;
+  }
+}
+
+// ---- operand helpers -------------------------------------------------------------------------------
+
+// Four E4M3 bytes of a dword as fp16 / bf16 pairs (exact; 0x7F and 0xFF become NaN).
+__device__ __forceinline__ uint32_t fp8_bf16(uint32_t w, bool high) {
+  return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))
+              : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+}
+__device__ __forceinline__ uint32_t fp8_f16(uint32_t w, bool high) {
+  return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))
+              : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, half2_t));
+}
+template <bool FP8>
+__device__ __forceinline__ uint32_t p_pair(float lo, float hi) {
+  return FP8 ? f16_pair(lo, hi) : bf16_pair(lo, hi);
+}
+
+// Element t of 8 keys' dwords a[j] (E4M3: 4 elements a dword, bf16: 2), as an 8-long operand in key order.
+// All elements of the dwords at once: out[t] for t = 0 .. 3 (or 0, 1).
+__device__ __forceinline__ void transpose_fp8(const uint32_t (&a)[8], u32x4_t (&out)[4]) {
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t *x = a + 4 * half;
+    const uint32_t p = __builtin_amdgcn_perm(x[1], x[0], 0x05010400u), q = __builtin_amdgcn_perm(x[1], x[0], 0x07030602u);
+    const uint32_t r = __builtin_amdgcn_perm(x[3], x[2], 0x05010400u), s = __builtin_amdgcn_perm(x[3], x[2], 0x07030602u);
+    uint32_t* o = half ? hi : lo;
+    o[0] = __builtin_amdgcn_perm(r, p, 0x05040100u);
+    o[1] = __builtin_amdgcn_perm(r, p, 0x07060302u);
+    o[2] = __builtin_amdgcn_perm(s, q, 0x05040100u);
+    o[3] = __builtin_amdgcn_perm(s, q, 0x07060302u);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    out[t] = u32x4_t{fp8_f16(lo[t], false), fp8_f16(lo[t], true), fp8_f16(hi[t], false), fp8_f16(hi[t], true)};
+}
+__device__ __forceinline__ void transpose_bf16(const uint32_t (&a)[8], u32x4_t (&out)[2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[0][i] = __builtin_amdgcn_perm(a[2 * i + 1], a[2 * i], 0x05040100u);
+    out[1][i] = __builtin_amdgcn_perm(a[2 * i + 1], a[2 * i], 0x07060302u);
+  }
+}
+
+// Bits that are set in every non-finite element of a dword of the cache (E4M3 NaN bytes, bf16 inf or NaN).
+template <bool FP8>
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
+  return FP8 ? ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
+}
+
+// A fragment of V taken apart: the finite elements (others 0) and two 0/1 indicators, of elements that
+// are +inf or NaN and of those that are -inf or NaN.  1 is 0x3C00 in fp16, 0x3F80 in bf16.
+template <bool FP8>
+__device__ __forceinline__ void take_apart(u32x4_t v, u32x4_t& fin, u32x4_t& up, u32x4_t& down) {
+  constexpr uint32_t kExp = FP8 ? 0x7C007C00u : 0x7F807F80u, kStep = FP8 ? 0x04000400u : 0x00800080u;
+  constexpr uint32_t kMag = 0x7FFF7FFFu, kOne = FP8 ? 0x3C00u : 0x3F80u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = v[i], nf = (((w & kExp) + kStep) & 0x80008000u) >> 15;     // 1 per non-finite half
+    const uint32_t nan = (((w & kMag) + (0x7FFF7FFFu - kExp)) & 0x80008000u) >> 15;
+    const uint32_t neg = (w & 0x80008000u) >> 15;
+    fin[i] = w & ~(nf * 0xFFFFu);
+    up[i] = (nf & (nan | (neg ^ 0x00010001u))) * kOne;
+    down[i] = (nf & (nan | neg)) * kOne;
+  }
+}
+
+__device__ __forceinline__ f32x4_t mfma16_bf16(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+template <bool FP8>
+__device__ __forceinline__ f32x4_t mfma16_pv(u32x4_t a, u32x4_t b, f32x4_t c) {
+  if (FP8)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  return mfma16_bf16(a, b, c);
+}
+__device__ __forceinline__ f32x16_t mfma32_bf16(u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+template <bool FP8>
+__device__ __forceinline__ f32x16_t mfma32_pv(u32x4_t a, u32x4_t b, f32x16_t c) {
+  if (FP8)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  return mfma32_bf16(a, b, c);
+}
+
+// What the non-finite values of V add to an output, given how many of each sign the row sees.
+__device__ __forceinline__ float non_finite_part(float up, float down) {
+  return (up > 0.0f ? __builtin_inff() : 0.0f) + (down > 0.0f ? -__builtin_inff() : 0.0f);
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (W == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
+  }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// m c of a running maximum; a row that has seen no key keeps the lowest value.
+__device__ __forceinline__ float scaled_max(float m, float c) { return m == kLowest ? kLowest : m * c; }
+
+// ---- few rows ----------------------------------------------------------------------------------------
+
+// Wavefronts per SIMD of the instances, as their registers (queries, O, one block of K and of V) allow.
+constexpr int stream_waves(int d, bool fp8, int rb) {
+  const int regs = rb * (d / 8 + d / 4) + d / 4 * (fp8 ? 1 : 2) + 64;
+  return regs <= 128 ? 4 : (regs <= 168 ? 3 : (regs <= 256 ? 2 : 1));
+}
+
+// RB blocks of 16 rows; lane n = lane % 16 is the row, quarter = lane / 16.
+//   scores   S^T[g] (16 keys x 16 rows): lane holds keys g*16 + quarter*4 + i of its row
+//   K        A operand, lane = key, quarter = slice of the channels: 16 B loads, two matrix steps each
+//            for E4M3 (channels c*64 + quarter*16 + half*8 + j), one for bf16 (c*32 + quarter*8 + j); the
+//            queries are loaded in the same channel order
+//   V        lane % 16 = slice of D/16 channels, quarter = 8 keys (quarter*4 + j of both groups); bytes
+//            transposed in registers to A operands of 16 channels x 32 keys: O^T tile t holds
+//            channels (quarter*4 + i) * D/16 + t
+template <int D, bool FP8, int RB>
+__global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_kernel(AttentionArgs a, Launch l) {
+  constexpr int E = FP8 ? 1 : 2;            // bytes per element
+  constexpr int BM = 16 * RB;
+  constexpr int KC = D * E / 64;            // 16-byte key loads per lane and group
+  constexpr int ST = D / 32;                // matrix steps of a score
+  constexpr int NT = D / 16;                // output tiles, and channels per lane slice
+  constexpr int VW = NT * E / 4;            // dwords of V per lane and key
+  constexpr int PT = D + 4;                 // LDS pitch of the merge
+  __shared__ float merge[4][16][PT];
+  __shared__ float2 merge_ml[4][16];
+  __shared__ int pre[kMaxSlots + 1];
+  __shared__ int wave_sum[4];
+
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, quarter = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  for_pieces<BM, kStreamBlock>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
+    const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
+    u32x4_t q[RB][ST];
+    int lo[RB], hi[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int r = t.row0 + rb * 16 + n;
+      row_range(a, t, r, lo[rb], hi[rb]);
+      const bool live = rb * 16 + n < t.rows;
+      const int tok = (int)fastdiv((uint32_t)r, a.div_group), g = r - tok * a.group;
+      const uint16_t* x = a.q + (live ? (t.c0 + tok) * a.q_tok + (h * a.group + g) * a.q_head : 0);
+#pragma unroll
+      for (int st = 0; st < ST; ++st) {
+        const int d = FP8 ? (st >> 1) * 64 + quarter * 16 + (st & 1) * 8 : st * 32 + quarter * 8;
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(x + d);
+        q[rb][st] = live ? w : u32x4_t{0, 0, 0, 0};
+      }
+    }
+    f32x4_t o[RB][NT];
+    float m[RB], sum[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      m[rb] = kLowest;
+      sum[rb] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[rb][i] = f32x4_t{0, 0, 0, 0};
+    }
+
+    const int64_t head_at = ((int64_t)h << a.page_shift) * (D * E);
+    const int mask = (1 << a.page_shift) - 1;
+    auto key_at = [&](int b) { return (t.block0 + b) * kStreamBlock + wave * 32; };
+    auto pages = [&](int b, int (&p)[2]) {
+      p[0] = b < b1 ? page_of(a, t, key_at(b)) : -1;
+      p[1] = b < b1 ? page_of(a, t, key_at(b) + 16) : -1;
+    };
+    uint4 kr[2][KC];
+    uint32_t vr[8][VW];
+    auto load_k = [&](int b, const int (&p)[2]) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int in = (key_at(b) + g * 16) & mask, page = p[g] >= 0 ? p[g] : 0;
+        const uint8_t* kp = a.k + page * a.k_page + head_at + in * (D * E);
+#pragma unroll
+        for (int i = 0; i < KC; ++i) kr[g][i] = *reinterpret_cast<const uint4*>(kp + n * (D * E) + i * 64 + quarter * 16);
+      }
+    };
+    auto load_v = [&](int b, const int (&p)[2]) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int in = (key_at(b) + g * 16) & mask, page = p[g] >= 0 ? p[g] : 0;
+        const uint8_t* vp = a.v + page * a.v_page + head_at + in * (D * E);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words<VW>(vp + (quarter * 4 + j) * (D * E) + n * (NT * E), vr[g * 4 + j]);
+      }
+    };
+
+    // One block at a time: V of this block and K of the next are in flight while the other is used.
+    int p[2], pn[2];
+    pages(b0, p);
+    load_k(b0, p);
+    pages(b0 + 1, pn);
+    for (int b = b0; b < b1; ++b) {
+      const int key0 = key_at(b), valid = (p[0] >= 0 ? 1 : 0) | (p[1] >= 0 ? 2 : 0);
+      load_v(b, p);
+      f32x4_t s[RB][2];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) s[rb][0] = s[rb][1] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int st = 0; st < ST; ++st) {
+          u32x4_t ka;
+          if (FP8) {
+            const uint4 w = kr[g][st >> 1];
+            const uint32_t x = st & 1 ? w.z : w.x, y = st & 1 ? w.w : w.y;
+            ka = u32x4_t{fp8_bf16(x, false), fp8_bf16(x, true), fp8_bf16(y, false), fp8_bf16(y, true)};
+          } else {
+            const uint4 w = kr[g][st];
+            ka = u32x4_t{w.x, w.y, w.z, w.w};
+          }
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) s[rb][g] = mfma16_bf16(ka, q[rb][st], s[rb][g]);
+        }
+      if (b + 1 < b1) load_k(b + 1, pn);
+      p[0] = pn[0];
+      p[1] = pn[1];
+      pages(b + 2, pn);
+
+      const bool partial_keys = valid != 3 || key0 + 32 > t.hi_min || key0 < t.lo_max;
+      u32x4_t pr[RB];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        if (partial_keys) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key0 + g * 16 + quarter * 4 + i;
+              const bool seen = ((valid >> g) & 1) && key >= lo[rb] && key < hi[rb];
+              s[rb][g][i] = seen ? s[rb][g][i] : -__builtin_inff();
+            }
+        }
+        float mx = m[rb];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx = __builtin_fmaxf(mx, s[rb][g][i]);
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (__builtin_amdgcn_ballot_w64((mx - m[rb]) * c > kLazy) != 0) {
+          const float f0 = exp2_fast((m[rb] - mx) * c);
+          m[rb] = mx;
+          sum[rb] *= f0;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) o[rb][i] *= f0;
+        }
+        const float mc = m[rb] == kLowest ? 0.0f : m[rb] * c;
+        float p8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p8[j] = exp2_fast(__builtin_fmaf(s[rb][j >> 2][j & 3], c, -mc));
+          sum[rb] += p8[j];
+        }
+        pr[rb] = u32x4_t{p_pair<FP8>(p8[0], p8[1]), p_pair<FP8>(p8[2], p8[3]), p_pair<FP8>(p8[4], p8[5]),
+                         p_pair<FP8>(p8[6], p8[7])};
+      }
+
+      if (valid != 3 || key0 + 32 > t.len) {             // keys that do not exist: zero their values
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool there = ((valid >> (j >> 2)) & 1) && key0 + (j >> 2) * 16 + quarter * 4 + (j & 3) < t.len;
+#pragma unroll
+          for (int i = 0; i < VW; ++i) vr[j][i] = there ? vr[j][i] : 0u;
+        }
+      }
+      uint32_t bad = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < VW; ++i) bad |= non_finite<FP8>(vr[j][i]);
+      const bool any_bad = __builtin_amdgcn_ballot_w64(bad != 0) != 0;
+      u32x4_t seen1[RB];
+      if (any_bad) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + (i >> 1) * 16 + quarter * 4 + (i & 1) * 2;
+            const bool in = (valid >> (i >> 1)) & 1;
+            seen1[rb][i] = ((in && key >= lo[rb] && key < hi[rb] ? 1u : 0u) |
+                            (in && key + 1 >= lo[rb] && key + 1 < hi[rb] ? 0x10000u : 0u)) * (FP8 ? 0x3C00u : 0x3F80u);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = vr[j][i];
+        constexpr int PER = FP8 ? 4 : 2;
+        u32x4_t va[PER];
+        if constexpr (FP8) transpose_fp8(w, va); else transpose_bf16(w, va);
+        if (any_bad) {
+#pragma unroll
+          for (int x = 0; x < PER; ++x) {
+            u32x4_t fin, up, down;
+            take_apart<FP8>(va[x], fin, up, down);
+            va[x] = fin;
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+              const f32x4_t u = mfma16_pv<FP8>(up, seen1[rb], f32x4_t{0, 0, 0, 0});
+              const f32x4_t d = mfma16_pv<FP8>(down, seen1[rb], f32x4_t{0, 0, 0, 0});
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[rb][i * PER + x][y] += non_finite_part(u[y], d[y]);
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < PER; ++x)
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) o[rb][i * PER + x] = mfma16_pv<FP8>(va[x], pr[rb], o[rb][i * PER + x]);
+      }
+    }
+
+    // the four wavefronts' parts, 16 rows at a time
+    const float vs = FP8 ? a.v_scale[h * a.scale_stride] : 1.0f;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      float l0 = sum[rb];
+      l0 += __shfl_xor(l0, 16, 64);
+      l0 += __shfl_xor(l0, 32, 64);
+      __syncthreads();
+      if (quarter == 0) merge_ml[wave][n] = make_float2(scaled_max(m[rb], c), l0);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int i = 0; i < NT; i += 4)
+          *reinterpret_cast<f32x4_t*>(&merge[wave][n][(quarter * 4 + x) * NT + i]) =
+              f32x4_t{o[rb][i][x], o[rb][i + 1][x], o[rb][i + 2][x], o[rb][i + 3][x]};
+      __syncthreads();
+      const int row = tid >> 4, d = (tid & 15) * NT;
+      if (rb * 16 + row < t.rows) {
+        float mm = kLowest, ll = 0.0f, w[4], e[NT];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mm = __builtin_fmaxf(mm, merge_ml[v][row].x);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          w[v] = exp2_fast(merge_ml[v][row].x - mm);
+          ll += merge_ml[v][row].y * w[v];
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          e[i] = 0.0f;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) e[i] += merge[v][row][d + i] * w[v];
+        }
+        if (partial >= 0) {
+          const int64_t at = (int64_t)partial * BM + rb * 16 + row;
+          if (d == 0) l.ml[at] = make_float2(mm, ll);
+#pragma unroll
+          for (int i = 0; i < NT; i += 4)
+            *reinterpret_cast<float4*>(l.po + at * D + d + i) = make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
+        } else {
+          const int r = t.row0 + rb * 16 + row;
+          const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
+          const float f = ll == 0.0f ? 0.0f : vs / ll;
+          uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + d;
+#pragma unroll
+          for (int i = 0; i < NT; i += 4)
+            *reinterpret_cast<uint2*>(y + i) = make_uint2(bf16_pair(e[i] * f, e[i + 1] * f), bf16_pair(e[i + 2] * f, e[i + 3] * f));
+          if (a.lse && d == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
+        }
+      }
+    }
+  });
+}
+
+// ---- many rows ---------------------------------------------------------------------------------------
+
+// Four wavefronts of RW blocks of 32 rows each; lane % 32 is the row, half = lane / 32.
+//   scores   S^T (32 keys x 32 rows): register i of a lane is key 8*(i/4) + 4*half + i%4
+//   LDS      K as bf16 [key][D] and V^T as fp16 or bf16 [D][64 keys], both double-buffered, in 16-byte
+//            chunks permuted within a row so that neighbouring rows fall on different banks.  The
+//            keys of a V^T row are stored in the order the score registers hold them: chunk
+//            2*(key/16) + half holds keys 4*half + {0..3} and 8 + 4*half + {0..3} of its 16.
+template <int D, bool FP8, int RW>
+__global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_kernel(AttentionArgs a, Launch l) {
+  constexpr int E = FP8 ? 1 : 2;
+  constexpr int BM = 128 * RW, KB = kTileBlock;
+  constexpr int ST = D / 16;                // matrix steps of a score
+  constexpr int DB = D / 32;                // output tiles
+  constexpr int CH = D * E / 16;            // 16-byte chunks of a cached key
+  constexpr int KL = KB * CH / kThreads;    // key loads per thread
+  constexpr int VQ = D / 4;                 // channel quads
+  constexpr int VI = (8 * VQ + kThreads - 1) / kThreads;   // value items per thread: 8 keys x 4 channels
+  __shared__ __align__(16) uint16_t ks[2][KB * D];
+  __shared__ __align__(16) uint16_t vt[2][D * KB];
+  __shared__ int pre[kMaxSlots + 1];
+  __shared__ int wave_sum[4];
+  __shared__ int bad_block[2];              // block whose values hold something non-finite
+  __shared__ int no_page[2][4];             // per 16 keys of a block
+
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  auto k_chunk = [](int key, int ch) {       // LDS offset (elements) of 8 channels of a key
+    constexpr int N = D / 8;
+    const int sw = N >= 16 ? key & 15 : (key >> 1) & 7;
+    return key * D + ((ch ^ sw) & (N - 1)) * 8;
+  };
+  auto v_chunk = [](int d, int ch) {         // LDS offset of 8 keys of a channel
+    const int sw = ((d >> 1) & 7) ^ ((d >> 4) & 1);
+    return d * KB + ((ch ^ sw) & 7) * 8;
+  };
+
+  for_pieces<BM, KB>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
+    const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
+    const int wrow = wave * 32 * RW;         // the wavefront's first row in the tile
+    const bool busy = wrow < t.rows;
+    u32x4_t q[RW][ST];
+    int lo[RW], hi[RW];
+#pragma unroll
+    for (int rw = 0; rw < RW; ++rw) {
+      const int r = t.row0 + wrow + rw * 32 + n;
+      row_range(a, t, r, lo[rw], hi[rw]);
+      const bool live = wrow + rw * 32 + n < t.rows;
+      const int tok = (int)fastdiv((uint32_t)r, a.div_group), g = r - tok * a.group;
+      const uint16_t* x = a.q + (live ? (t.c0 + tok) * a.q_tok + (h * a.group + g) * a.q_head : 0);
+#pragma unroll
+      for (int st = 0; st < ST; ++st) {
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(x + st * 16 + half * 8);
+        q[rw][st] = live ? w : u32x4_t{0, 0, 0, 0};
+      }
+    }
+    // keys every row of the wavefront sees, and keys any of them sees
+    int w_first = 0, w_last = 0;
+    if (busy) {
+      const int rl = wrow + 32 * RW < t.rows ? wrow + 32 * RW - 1 : t.rows - 1;
+      w_first = (int)fastdiv((uint32_t)(t.row0 + wrow), a.div_group);
+      w_last = (int)fastdiv((uint32_t)(t.row0 + rl), a.div_group);
+    }
+    int hi_min = t.len, hi_max = t.len, lo_min = 0, lo_max = 0;
+    if (a.causal) {
+      hi_min = clamp_int(t.pos0 + w_first + 1, 0, t.len);
+      hi_max = clamp_int(t.pos0 + w_last + 1, 0, t.len);
+      if (a.window > 0) {
+        const int64_t l0 = (int64_t)t.pos0 + w_first - a.window + 1, l1 = (int64_t)t.pos0 + w_last - a.window + 1;
+        lo_min = l0 > 0 ? (int)l0 : 0;
+        lo_max = l1 > 0 ? (int)l1 : 0;
+      }
+    }
+
+    f32x16_t o[RW][DB];
+    float m[RW], sum[RW];
+#pragma unroll
+    for (int rw = 0; rw < RW; ++rw) {
+      m[rw] = kLowest;
+      sum[rw] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[rw][i][x] = 0.0f;
+    }
+
+    const int64_t head_at = ((int64_t)h << a.page_shift) * (D * E);
+    const int mask = (1 << a.page_shift) - 1;
+    uint4 kr[KL];
+    uint32_t vr[VI][8][E];                   // 4 channels of 8 keys
+    // block b of the piece into registers
+    auto fetch = [&](int b) {
+      const int key0 = (t.block0 + b) * KB;
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const int at = i * kThreads + tid, key = key0 + at / CH, ch = at % CH;
+        const int p = page_of(a, t, key);
+        kr[i] = *reinterpret_cast<const uint4*>(a.k + (p >= 0 ? p : 0) * a.k_page + head_at + (key & mask) * (D * E) + ch * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < VI; ++i) {
+        const int at = i * kThreads + tid, grp = at / VQ, quad = at % VQ;   // grp: chunk of 8 keys
+        if (8 * VQ % kThreads != 0 && grp >= 8) continue;
+        const int key = key0 + (grp >> 1) * 16 + (grp & 1) * 4;
+        const int p = page_of(a, t, key);
+        const uint8_t* vp = a.v + (p >= 0 ? p : 0) * a.v_page + head_at + (key & mask) * (D * E) + quad * (4 * E);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t w[E];
+          const int dk = (j & 3) + (j >> 2) * 8;
+          load_words<E>(vp + dk * (D * E), w);
+#pragma unroll
+          for (int x = 0; x < E; ++x) vr[i][j][x] = p >= 0 && key + dk < t.len ? w[x] : 0u;
+        }
+      }
+    };
+    // registers to LDS buffer `buf`
+    auto store = [&](int b, int buf) {
+      const int key0 = (t.block0 + b) * KB;
+      if (tid < 4) no_page[buf][tid] = page_of(a, t, key0 + tid * 16) < 0;
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const int at = i * kThreads + tid, key = at / CH, ch = at % CH;
+        const uint4 w = kr[i];
+        if (FP8) {
+          *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch)]) =
+              u32x4_t{fp8_bf16(w.x, false), fp8_bf16(w.x, true), fp8_bf16(w.y, false), fp8_bf16(w.y, true)};
+          *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch + 1)]) =
+              u32x4_t{fp8_bf16(w.z, false), fp8_bf16(w.z, true), fp8_bf16(w.w, false), fp8_bf16(w.w, true)};
+        } else {
+          *reinterpret_cast<uint4*>(&ks[buf][k_chunk(key, ch)]) = w;
+        }
+      }
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < VI; ++i) {
+        const int at = i * kThreads + tid, grp = at / VQ, quad = at % VQ;
+        if (8 * VQ % kThreads != 0 && grp >= 8) continue;
+#pragma unroll
+        for (int x = 0; x < E; ++x) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            w[j] = vr[i][j][x];
+            bad |= non_finite<FP8>(w[j]);
+          }
+          constexpr int PER = FP8 ? 4 : 2;
+          u32x4_t va[PER];
+          if constexpr (FP8) transpose_fp8(w, va); else transpose_bf16(w, va);
+#pragma unroll
+          for (int y = 0; y < PER; ++y)
+            *reinterpret_cast<u32x4_t*>(&vt[buf][v_chunk(quad * 4 + x * PER + y, grp)]) = va[y];
+        }
+      }
+      if (bad) bad_block[buf] = b;           // every writer writes the same
+    };
+
+    auto compute = [&](int b, int buf) {
+      const int key0 = (t.block0 + b) * KB;
+      if (!busy || key0 >= hi_max || key0 + KB <= lo_min) return;
+      const int gone = no_page[buf][0] | no_page[buf][1] << 1 | no_page[buf][2] << 2 | no_page[buf][3] << 3;
+      const bool partial_keys = gone != 0 || key0 + KB > hi_min || key0 < lo_max;
+      f32x16_t s[RW][2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int rw = 0; rw < RW; ++rw)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) s[rw][kb][x] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < ST; ++st) {
+          const u32x4_t ka = *reinterpret_cast<const u32x4_t*>(&ks[buf][k_chunk(kb * 32 + n, st * 2 + half)]);
+#pragma unroll
+          for (int rw = 0; rw < RW; ++rw) s[rw][kb] = mfma32_bf16(ka, q[rw][st], s[rw][kb]);
+        }
+      }
+      const bool any_bad = bad_block[buf] == b;
+      u32x4_t pr[RW][4];
+#pragma unroll
+      for (int rw = 0; rw < RW; ++rw) {
+        if (partial_keys) {
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const int key = key0 + kb * 32 + 8 * (x >> 2) + 4 * half + (x & 3);
+              const bool seen = !((gone >> (kb * 2 + (x >> 3))) & 1) && key >= lo[rw] && key < hi[rw];
+              s[rw][kb][x] = seen ? s[rw][kb][x] : -__builtin_inff();
+            }
+        }
+        float mx = m[rw];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[rw][kb][x]);
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (__builtin_amdgcn_ballot_w64((mx - m[rw]) * c > kLazy) != 0) {
+          const float f0 = exp2_fast((m[rw] - mx) * c);
+          m[rw] = mx;
+          sum[rw] *= f0;
+#pragma unroll
+          for (int i = 0; i < DB; ++i) o[rw][i] *= f0;
+        }
+        const float mc = m[rw] == kLowest ? 0.0f : m[rw] * c;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float p8[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              p8[j] = exp2_fast(__builtin_fmaf(s[rw][kb][g * 8 + j], c, -mc));
+              sum[rw] += p8[j];
+            }
+            pr[rw][kb * 2 + g] = u32x4_t{p_pair<FP8>(p8[0], p8[1]), p_pair<FP8>(p8[2], p8[3]), p_pair<FP8>(p8[4], p8[5]),
+                                         p_pair<FP8>(p8[6], p8[7])};
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          u32x4_t va = *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
+          if (any_bad) {
+            u32x4_t fin, up, down;
+            take_apart<FP8>(va, fin, up, down);
+            va = fin;
+#pragma unroll
+            for (int rw = 0; rw < RW; ++rw) {
+              u32x4_t seen1;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int key = key0 + g * 16 + 8 * (y >> 1) + 4 * half + (y & 1) * 2;
+                const bool in = !((gone >> g) & 1);
+                seen1[y] = ((in && key >= lo[rw] && key < hi[rw] ? 1u : 0u) |
+                            (in && key + 1 >= lo[rw] && key + 1 < hi[rw] ? 0x10000u : 0u)) * (FP8 ? 0x3C00u : 0x3F80u);
+              }
+              f32x16_t zero;
+#pragma unroll
+              for (int y = 0; y < 16; ++y) zero[y] = 0.0f;
+              const f32x16_t u = mfma32_pv<FP8>(up, seen1, zero), d = mfma32_pv<FP8>(down, seen1, zero);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[rw][i][y] += non_finite_part(u[y], d[y]);
+            }
+          }
+#pragma unroll
+          for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
+        }
+    };
+
+    __syncthreads();                          // the last piece's readers are done
+    if (tid < 2) bad_block[tid] = -1;
+    fetch(b0);
+    __syncthreads();
+    store(b0, 0);
+    __syncthreads();
+    for (int b = b0; b < b1; ++b) {
+      const int buf = (b - b0) & 1;
+      if (b + 1 < b1) fetch(b + 1);
+      compute(b, buf);
+      if (b + 1 < b1) store(b + 1, buf ^ 1);
+      __syncthreads();
+    }
+
+    const float vs = FP8 ? a.v_scale[h * a.scale_stride] : 1.0f;
+#pragma unroll
+    for (int rw = 0; rw < RW; ++rw) {
+      const float ll = sum[rw] + __shfl_xor(sum[rw], 32, 64);
+      const float mm = scaled_max(m[rw], c);
+      const int tr = wrow + rw * 32 + n;
+      if (tr >= t.rows) continue;
+      if (partial >= 0) {
+        const int64_t at = (int64_t)partial * BM + tr;
+        if (half == 0) l.ml[at] = make_float2(mm, ll);
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<float4*>(l.po + at * D + i * 32 + 8 * x + 4 * half) =
+                make_float4(o[rw][i][4 * x], o[rw][i][4 * x + 1], o[rw][i][4 * x + 2], o[rw][i][4 * x + 3]);
+      } else {
+        const int r = t.row0 + tr;
+        const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
+        const float f = ll == 0.0f ? 0.0f : vs / ll;
+        uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint2*>(y + i * 32 + 8 * x + 4 * half) =
+                make_uint2(bf16_pair(o[rw][i][4 * x] * f, o[rw][i][4 * x + 1] * f),
+                           bf16_pair(o[rw][i][4 * x + 2] * f, o[rw][i][4 * x + 3] * f));
+        if (a.lse && half == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
+      }
+    }
+  });
+}
+
+// ---- joining the parts of cut segments ---------------------------------------------------------------
+
+// One workgroup per (slot, head, row); D / 4 lanes hold a part's row, 256 / (D / 4) parts at a time.
+template <int D, int BM, int KB>
+__global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Launch l) {
+  constexpr int LP = D / 4, GR = kThreads / LP;
+  __shared__ float4 part[GR][LP];
+  __shared__ float red[4], lsum[GR];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x % BM, rest = blockIdx.x / BM;
+  const int h = rest % a.kv_heads, slot = rest / a.kv_heads;
+  const int all = l.plan[l.slots], per = l.plan[l.slots + 1];
+  const int p0 = l.plan[slot], count = l.plan[slot + 1] - p0;
+  if (count == 0) return;
+  const int64_t u0 = (int64_t)h * all + p0, u1 = u0 + count;
+  const int w0 = (int)(u0 / per), w1 = (int)((u1 - 1) / per);
+  if (w0 == w1) return;
+  Tile t;
+  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
+  if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t) || row >= t.rows) return;
+  auto index = [&](int w) { return (int64_t)(2 * w + (u0 < (int64_t)w * per ? 0 : 1)) * BM + row; };
+  float mm = kLowest;
+  for (int w = w0 + tid; w <= w1; w += kThreads) mm = __builtin_fmaxf(mm, l.ml[index(w)].x);
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) mm = __builtin_fmaxf(mm, __shfl_xor(mm, x, 64));
+  if (lane == 0) red[wave] = mm;
+  __syncthreads();
+  mm = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
+  const int g = tid / LP, x = tid % LP;
+  float4 acc = make_float4(0, 0, 0, 0);
+  float ll = 0.0f;
+  for (int w = w0 + g; w <= w1; w += GR) {
+    const int64_t at = index(w);
+    const float2 ml = l.ml[at];
+    const float4 v = *reinterpret_cast<const float4*>(l.po + at * D + x * 4);
+    const float f = exp2_fast(ml.x - mm);
+    ll += ml.y * f;
+    acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+  }
+  part[g][x] = acc;
+  if (x == 0) lsum[g] = ll;
+  __syncthreads();
+  if (g != 0) return;
+  for (int i = 1; i < GR; ++i) {
+    const float4 v = part[i][x];
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    ll += lsum[i];
+  }
+  const float vs = a.v_scale ? a.v_scale[h * a.scale_stride] : 1.0f;
+  const int r = t.row0 + row;
+  const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
+  const float f = ll == 0.0f ? 0.0f : vs / ll;
+  *reinterpret_cast<uint2*>(a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + x * 4) =
+      make_uint2(bf16_pair(acc.x * f, acc.y * f), bf16_pair(acc.z * f, acc.w * f));
+  if (a.lse && x == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
+}
+
+// ---- launching ----------------------------------------------------------------------------------------
+
+// One of the two kernels of a call: which rows it takes, its row tile and whether its key axis is cut.
+struct Choice {
+  bool used;
+  int bm, rows_lo, rows_hi;
+  int64_t slots;
+  bool split;
+  int workgroups;
+};
+
+struct Choices {
+  Choice stream, tile;
+};
+
+size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+size_t split_bytes(const Choice& c, int dim) {
+  if (!c.used || !c.split) return 0;
+  return align16((size_t)(c.slots + 2) * 4) + (size_t)2 * c.workgroups * c.bm * (8 + (size_t)dim * 4);
+}
+
+Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads, int64_t kv_heads, int dim) {
+  const int64_t group = q_heads / kv_heads;
+  const int64_t rows = (max_q > 0 && max_q < tokens ? max_q : tokens) * group;
+  Choices c{};
+  auto slots = [&](int bm) { return tokens * group / bm + num_seqs; };
+  const int rb = rows <= 16 || (rows > 32 && group <= 16) ? 1 : 2;
+  c.stream.used = rows <= 32 || (num_seqs > 1 && group <= 32);
+  c.tile.used = rows > 32;
+  c.stream.bm = 16 * rb;
+  c.stream.rows_hi = c.tile.used ? c.stream.bm : INT32_MAX;
+  c.stream.slots = slots(c.stream.bm);
+  c.stream.split = c.stream.slots <= kMaxSlots;
+  c.stream.workgroups = dim == 256 ? 512 : 1024;
+  c.tile.bm = 128;
+  c.tile.rows_lo = c.stream.used ? c.stream.bm : 0;
+  c.tile.rows_hi = INT32_MAX;
+  c.tile.slots = slots(c.tile.bm);
+  c.tile.workgroups = dim == 256 ? 256 : 512;
+  c.tile.split = c.tile.slots <= kMaxSlots && c.tile.slots * kv_heads < 4 * c.tile.workgroups;
+  return c;
+}
+
+template <int D, int BM, int KB, typename Kernel>
+int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_blocks, void* workspace, hipStream_t stream) {
+  Launch l{};
+  l.slots = (int32_t)c.slots;
+  l.rows_lo = c.rows_lo;
+  l.rows_hi = c.rows_hi;
+  l.min_blocks = min_blocks;
+  // nothing to cut where the table holds no more keys than the smallest share, or where block
+  // numbers could pass 31 bits
+  const int64_t cap = (((int64_t)a.table_width << a.page_shift) + KB - 1) / KB;
+  l.split = c.split && cap > min_blocks && cap * c.slots < INT32_MAX;
+  l.workgroups = c.workgroups;
+  int64_t grid = c.slots * a.kv_heads;
+  if (l.split) {
+    grid = c.workgroups;
+    char* p = static_cast<char*>(workspace);
+    l.plan = reinterpret_cast<int32_t*>(p);
+    l.ml = reinterpret_cast<float2*>(p + align16((size_t)(c.slots + 2) * 4));
+    l.po = reinterpret_cast<float*>(l.ml + (size_t)2 * c.workgroups * BM);
+  }
+  if (grid > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  kernel<<<(unsigned)grid, kThreads, 0, stream>>>(a, l);
+  if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+  if (l.split) {
+    combine_kernel<D, BM, KB><<<(unsigned)(c.slots * a.kv_heads * BM), kThreads, 0, stream>>>(a, l);
+    if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+  }
+  return NVFP4_OK;
+}
+
+template <int D, bool FP8>
+int launch_dim(const AttentionArgs& a, const Choices& c, void* workspace, hipStream_t stream) {
+  if (c.stream.used) {
+    const int st = c.stream.bm == 16
+        ? launch_one<D, 16, kStreamBlock>(stream_kernel<D, FP8, 1>, a, c.stream, 2, workspace, stream)
+        : launch_one<D, 32, kStreamBlock>(stream_kernel<D, FP8, 2>, a, c.stream, 2, workspace, stream);
+    if (st != NVFP4_OK) return st;
+  }
+  if (c.tile.used) return launch_one<D, 128, kTileBlock>(tile_kernel<D, FP8, 1>, a, c.tile, 4, workspace, stream);
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+size_t paged_attention_workspace_bytes(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
+                                       int64_t kv_heads, int head_dim) {
+  const Choices c = choose(tokens, max_q, num_seqs, q_heads, kv_heads, head_dim);
+  const size_t s = split_bytes(c.stream, head_dim), t = split_bytes(c.tile, head_dim);
+  return s > t ? s : t;
+}
+
+int launch_paged_attention(const AttentionArgs& a, int64_t max_q, int head_dim, void* workspace, hipStream_t stream) {
+  const Choices c = choose(a.tokens, max_q, a.num_seqs, a.q_heads, a.kv_heads, head_dim);
+  const bool fp8 = a.k_scale != nullptr;
+  switch (head_dim) {
+    case 64: return fp8 ? launch_dim<64, true>(a, c, workspace, stream) : launch_dim<64, false>(a, c, workspace, stream);
+    case 128: return fp8 ? launch_dim<128, true>(a, c, workspace, stream) : launch_dim<128, false>(a, c, workspace, stream);
+    default: return fp8 ? launch_dim<256, true>(a, c, workspace, stream) : launch_dim<256, false>(a, c, workspace, stream);
+  }
+}
+
+}  // namespace nvfp4
