@@ -591,99 +591,112 @@ class PagedKV:
     v_scale: torch.Tensor | None = None
 
 
-def _heads_arg(t: torch.Tensor, name: str, dtypes: tuple, dev: torch.device, tokens: int | None = None,
+# These operators run once per layer and token, so their checks are written for few Python steps:
+# devices are compared by index (-1: CPU), messages are built only when a check fails.
+
+
+def _shape_text(*dims) -> str:
+    return "[" + ", ".join("any" if d is None else str(d) for d in dims) + "]"
+
+
+def _heads_arg(t: torch.Tensor, name: str, dtypes: tuple, gpu: int, tokens: int | None = None,
                heads: int | None = None, dim: int | None = None) -> _Heads:
     """A [tokens, heads, dim] operand whose last dimension is contiguous."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name}: a tensor [tokens, heads, dim]")
     n, h, d = t.shape
     if (tokens is not None and n != tokens) or (heads is not None and h != heads) or (dim is not None and d != dim):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{tokens}, {'heads' if heads is None else heads}, {dim}]")
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {_shape_text(tokens, heads, dim)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(x) for x in dtypes)}")
     st, sh, sd = t.stride()
     if sd != 1 and n * h > 0:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name}: a tensor on {dev}")
+    if t.get_device() != gpu:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
     return _Heads(t.data_ptr(), h, st, sh)
 
 
-def _i32_arg(t: torch.Tensor, name: str, numel: int, dev: torch.device) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 [{numel}]")
-    if t.shape[0] != numel:
-        raise ValueError(f"{name}: {t.shape[0]} elements, expected {numel}")
-    if t.device != dev:
-        raise ValueError(f"{name}: a tensor on {dev}")
+def _vector_arg(t: torch.Tensor, name: str, dtype: torch.dtype, counts: tuple, gpu: int) -> int:
+    """A contiguous one-dimensional operand with one of the given element counts."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype}, one dimension")
+    if t.shape[0] not in counts:
+        raise ValueError(f"{name}: {t.shape[0]} elements, expected {' or '.join(map(str, counts))}")
+    if t.get_device() != gpu:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
     return t.data_ptr()
 
 
-def _cache_arg(kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, dev: torch.device) -> _PagedKV:
+def _cache_arg(kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, gpu: int) -> _PagedKV:
     if not isinstance(kv, PagedKV):
         raise ValueError("kv: a PagedKV")
     k, v, table = kv.k, kv.v, kv.page_table
     if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or k.dim() != 4 or k.shape != v.shape:
         raise ValueError("kv.k, kv.v: tensors [pages, kv_heads, page_size, head_dim] of one shape")
-    if k.dtype not in (torch.uint8, torch.bfloat16) or v.dtype != k.dtype:
+    dtype = k.dtype
+    fp8 = dtype is torch.uint8
+    if not (fp8 or dtype is torch.bfloat16) or v.dtype is not dtype:
         raise ValueError("kv.k, kv.v: both uint8 (E4M3 bytes) or both bfloat16")
     pages, heads, page, dim = k.shape
-    inner = (page * dim, dim, 1)
-    if pages > 0 and (k.stride()[1:] != inner or v.stride()[1:] != inner):
+    sk, sv, inner = k.stride(), v.stride(), (page * dim, dim, 1)
+    if pages > 0 and (sk[1:] != inner or sv[1:] != inner):
         raise ValueError("kv.k, kv.v: every page must be contiguous")
-    if k.device != dev or v.device != dev:
-        raise ValueError(f"kv: tensors on {dev}")
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2:
+    if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() != 2:
         raise ValueError("kv.page_table: int32 [sequences, width]")
     seqs, width = table.shape
-    if seqs * width > 0 and table.stride(1) != 1 and width > 1:
+    pitch, step = table.stride()
+    if step != 1 and width > 1 and seqs > 0:
         raise ValueError("kv.page_table: rows must be contiguous")
-    if table.device != dev:
-        raise ValueError(f"kv.page_table: a tensor on {dev}")
-    c = _PagedKV(k.data_ptr(), v.data_ptr(), pages, k.stride(0), v.stride(0), table.data_ptr(), table.stride(0), None, None,
-                 _i32_arg(cu_q, "cu_q", seqs + 1, dev), _i32_arg(kv_len, "kv_len", seqs, dev),
-                 _E4M3 if k.dtype == torch.uint8 else _BF16, heads, dim, page, seqs, width, 0)
-    if c.dtype == _E4M3:
+    if k.get_device() != gpu or v.get_device() != gpu or table.get_device() != gpu:
+        raise ValueError("kv: tensors on another device than the new tokens'")
+    ks = vs = None
+    count = 0
+    if fp8:
         if kv.k_scale is None or kv.v_scale is None:
             raise ValueError("kv.k_scale, kv.v_scale: an FP8 cache needs its calibrated scales")
-        _require_f32(kv.k_scale, (1, heads), "kv.k_scale", dev)
-        _require_f32(kv.v_scale, kv.k_scale.numel(), "kv.v_scale", dev)
-        c.k_scale, c.v_scale, c.scale_count = kv.k_scale.data_ptr(), kv.v_scale.data_ptr(), kv.k_scale.numel()
-    return c
+        ks = _vector_arg(kv.k_scale, "kv.k_scale", torch.float32, (1, heads), gpu)
+        count = kv.k_scale.shape[0]
+        vs = _vector_arg(kv.v_scale, "kv.v_scale", torch.float32, (count,), gpu)
+    return _PagedKV(k.data_ptr(), v.data_ptr(), pages, sk[0], sv[0], table.data_ptr(), pitch, ks, vs,
+                    _vector_arg(cu_q, "cu_q", torch.int32, (seqs + 1,), gpu),
+                    _vector_arg(kv_len, "kv_len", torch.int32, (seqs,), gpu),
+                    _E4M3 if fp8 else _BF16, heads, dim, page, seqs, width, count)
 
 
-def _weight_arg(w: torch.Tensor | None, name: str, dim: int, dev: torch.device) -> int | None:
-    if w is None:
-        return None
-    _require_f32(w, dim, name, dev)
-    return w.data_ptr()
+def _weight_arg(w: torch.Tensor | None, name: str, dim: int, gpu: int) -> int | None:
+    return None if w is None else _vector_arg(w, name, torch.float32, (dim,), gpu)
 
 
-def _rope_arg(rope: torch.Tensor | None, positions: torch.Tensor | None, tokens: int, interleaved: bool,
-              dev: torch.device):
+def _rope_arg(rope: torch.Tensor | None, positions: torch.Tensor | None, tokens: int, interleaved: bool, gpu: int):
     if rope is None:
         _require(positions is None, "positions without a rope table")
         return None
-    if not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
+    if not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.dtype is not torch.float32 or not rope.is_contiguous():
         raise ValueError("rope: contiguous float32 [positions, rotated channels], cos then sin")
-    if rope.device != dev:
-        raise ValueError(f"rope: a tensor on {dev}")
-    pos = None if positions is None else _i32_arg(positions, "positions", tokens, dev)
-    return _Rope(rope.data_ptr(), rope.shape[0], pos, rope.shape[1], int(interleaved))
+    if rope.get_device() != gpu:
+        raise ValueError("rope: on another device than the tokens")
+    rows, dim = rope.shape
+    pos = None if positions is None else _vector_arg(positions, "positions", torch.int32, (tokens,), gpu)
+    return _Rope(rope.data_ptr(), rows, pos, dim, 1 if interleaved else 0)
 
 
-def _run(dev: torch.device, what: str, fn, *args) -> None:
-    """fn(*args, stream) on dev's current stream, with dev current: the default stream belongs to
-    whichever device is."""
-    _on_gpu(dev)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream(dev)), what)
+def _run(gpu: int, what: str, fn, *args) -> None:
+    """fn(*args, stream) on that GPU's current stream, with the GPU current: the default stream belongs to
+    whichever is."""
+    if gpu < 0:
+        raise ValueError("tensors must be on a GPU, not the CPU")
+    if torch.cuda.current_device() == gpu:
+        st = fn(*args, torch.cuda.current_stream(gpu).cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), what)
+        with torch.cuda.device(gpu):
+            st = fn(*args, torch.cuda.current_stream(gpu).cuda_stream)
+    if st != 0:
+        raise NVFP4Error(st, what)
 
 
 _X_DTYPES = (torch.bfloat16, torch.float32)
+_BF16_ONLY = (torch.bfloat16,)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
@@ -697,22 +710,24 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, q_weight: torch
     position; positions int32 [T].  Channel i turns with i + R/2, or 2i with 2i + 1 when ``interleaved``.
     Returns (q, k) of out_dtype (default: the input's); q_out, k_out may be the inputs themselves."""
     _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q: a tensor [tokens, heads, dim]")
-    dev, (T, Hq, D) = q.device, q.shape
-    out_dtype = q.dtype if out_dtype is None else out_dtype
-    qa = _heads_arg(q, "q", _X_DTYPES, dev)
-    ka = None if k is None else _heads_arg(k, "k", (q.dtype,), dev, T, None, D)
+    gpu, (T, Hq, D), dtype = q.get_device(), q.shape, q.dtype
+    out_dtype = dtype if out_dtype is None else out_dtype
     _require(rope is None or positions is not None, "rope needs positions")
-    _require(k is not None or (k_weight is None and k_out is None), "k_weight or k_out without k")
-    ra = _rope_arg(rope, positions, T, interleaved, dev)
-    qw, kw = _weight_arg(q_weight, "q_weight", D, dev), _weight_arg(k_weight, "k_weight", D, dev)
-    q_out = torch.empty((T, Hq, D), dtype=out_dtype, device=dev) if q_out is None else q_out
-    qo = _heads_arg(q_out, "q_out", (out_dtype,), dev, T, Hq, D)
-    ko = None
+    qa = _heads_arg(q, "q", _X_DTYPES, gpu)
+    ra = _rope_arg(rope, positions, T, interleaved, gpu)
+    qw, kw = _weight_arg(q_weight, "q_weight", D, gpu), _weight_arg(k_weight, "k_weight", D, gpu)
+    od = _y_dtype(out_dtype)
+    q_out = q.new_empty((T, Hq, D), dtype=out_dtype) if q_out is None else q_out
+    qo = _heads_arg(q_out, "q_out", (out_dtype,), gpu, T, Hq, D)
+    ka = ko = None
     if k is not None:
-        k_out = torch.empty((T, k.shape[1], D), dtype=out_dtype, device=dev) if k_out is None else k_out
-        ko = _heads_arg(k_out, "k_out", (out_dtype,), dev, T, k.shape[1], D)
-    _run(dev, "nvfp4_qk_norm_rope", lib.nvfp4_qk_norm_rope, T, D, _BF16 if q.dtype == torch.bfloat16 else _F32, qa, ka, qw,
-         kw, eps, ra, _y_dtype(out_dtype), qo, ko)
+        ka = _heads_arg(k, "k", (dtype,), gpu, T, None, D)
+        k_out = k.new_empty((T, ka.heads, D), dtype=out_dtype) if k_out is None else k_out
+        ko = _heads_arg(k_out, "k_out", (out_dtype,), gpu, T, ka.heads, D)
+    else:
+        _require(k_weight is None and k_out is None, "k_weight or k_out without k")
+    _run(gpu, "nvfp4_qk_norm_rope", lib.nvfp4_qk_norm_rope, T, D, _BF16 if dtype is torch.bfloat16 else _F32, qa, ka, qw,
+         kw, eps, ra, od, qo, ko)
     return q_out, k_out
 
 
@@ -728,22 +743,23 @@ def kv_append(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tenso
     q [T, Hq, D] the queries leave normed and rotated in the same launch: returns q_out (bf16 unless a
     q_out of fp32 is given), else None."""
     _require(isinstance(k, torch.Tensor) and k.dim() == 3, "k: a tensor [tokens, kv_heads, dim]")
-    dev, T = k.device, k.shape[0]
-    c = _cache_arg(kv, kv_len, cu_q, dev)
-    ka = _heads_arg(k, "k", _X_DTYPES, dev, T, c.kv_heads, c.head_dim)
-    va = _heads_arg(v, "v", (k.dtype,), dev, T, c.kv_heads, c.head_dim)
-    ra = _rope_arg(rope, positions, T, interleaved, dev)
-    kw, qw = _weight_arg(k_weight, "k_weight", c.head_dim, dev), _weight_arg(q_weight, "q_weight", c.head_dim, dev)
+    gpu, T, dtype = k.get_device(), k.shape[0], k.dtype
+    c = _cache_arg(kv, kv_len, cu_q, gpu)
+    Hk, D = c.kv_heads, c.head_dim
+    ka = _heads_arg(k, "k", _X_DTYPES, gpu, T, Hk, D)
+    va = _heads_arg(v, "v", (dtype,), gpu, T, Hk, D)
+    ra = _rope_arg(rope, positions, T, interleaved, gpu)
+    kw, qw = _weight_arg(k_weight, "k_weight", D, gpu), _weight_arg(q_weight, "q_weight", D, gpu)
     qa = qo = None
     qdt = _BF16
     if q is not None:
-        qa = _heads_arg(q, "q", (k.dtype,), dev, T, None, c.head_dim)
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-        qo = _heads_arg(q_out, "q_out", _X_DTYPES, dev, T, q.shape[1], c.head_dim)
-        qdt = _BF16 if q_out.dtype == torch.bfloat16 else _F32
+        qa = _heads_arg(q, "q", (dtype,), gpu, T, None, D)
+        q_out = q.new_empty((T, qa.heads, D), dtype=torch.bfloat16) if q_out is None else q_out
+        qo = _heads_arg(q_out, "q_out", _X_DTYPES, gpu, T, qa.heads, D)
+        qdt = _BF16 if q_out.dtype is torch.bfloat16 else _F32
     else:
         _require(q_weight is None and q_out is None, "q_weight or q_out without q")
-    _run(dev, "nvfp4_kv_append", lib.nvfp4_kv_append, c, T, _BF16 if k.dtype == torch.bfloat16 else _F32, ka, va, kw, eps,
+    _run(gpu, "nvfp4_kv_append", lib.nvfp4_kv_append, c, T, _BF16 if dtype is torch.bfloat16 else _F32, ka, va, kw, eps,
          ra, qa, qw, qdt, qo)
     return q_out
 
@@ -759,20 +775,22 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, kv_len: torch.Tensor, cu_q: to
     ``lib.nvfp4_paged_attention_workspace_size(...)`` bytes (allocated when None).
     Returns out [T, Hq, D] bf16, or (out, lse [T, Hq] fp32 = ln sum exp(scale q.k))."""
     _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q: a tensor [tokens, heads, dim]")
-    dev, (T, Hq, D) = q.device, q.shape
-    c = _cache_arg(kv, kv_len, cu_q, dev)
-    qa = _heads_arg(q, "q", (torch.bfloat16,), dev, T, Hq, c.head_dim)
-    _require(c.kv_heads > 0 and Hq % c.kv_heads == 0, "q heads must be a multiple of the cache's")
-    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
-    oa = _heads_arg(out, "out", (torch.bfloat16,), dev, T, Hq, D)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    need = lib.nvfp4_paged_attention_workspace_size(T, max_q, c.num_seqs, Hq, c.kv_heads, D, c.dtype)
+    gpu, (T, Hq, D) = q.get_device(), q.shape
+    c = _cache_arg(kv, kv_len, cu_q, gpu)
+    Hk = c.kv_heads
+    qa = _heads_arg(q, "q", _BF16_ONLY, gpu, T, Hq, c.head_dim)
+    _require(Hk > 0 and Hq % Hk == 0, "q heads must be a multiple of the cache's")
+    out = q.new_empty((T, Hq, D)) if out is None else out
+    oa = _heads_arg(out, "out", _BF16_ONLY, gpu, T, Hq, D)
+    lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
+    need = lib.nvfp4_paged_attention_workspace_size(T, max_q, c.num_seqs, Hq, Hk, D, c.dtype)
+    have = need
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        workspace = q.new_empty((need,), dtype=torch.uint8) if need else None
     else:
-        _require(isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
-                 "workspace: contiguous uint8")
-        _require(workspace.device == dev, f"workspace: a tensor on {dev}")
-    _run(dev, "nvfp4_paged_attention", lib.nvfp4_paged_attention, c, T, max_q, qa, D ** -0.5 if scale is None else scale,
-         int(causal), window, oa, _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
+        have = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+        _require(have > 0 and workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace: contiguous uint8")
+        _require(workspace.get_device() == gpu, "workspace: on another device than q")
+    _run(gpu, "nvfp4_paged_attention", lib.nvfp4_paged_attention, c, T, max_q, qa, D ** -0.5 if scale is None else scale,
+         1 if causal else 0, window, oa, _ptr(lse), _ptr(workspace), have)
     return (out, lse) if return_lse else out

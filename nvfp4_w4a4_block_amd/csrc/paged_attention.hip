@@ -63,7 +63,9 @@ struct Launch {
   int32_t split;             // 0: one workgroup per (slot, head)
   int32_t workgroups;        // of a split launch
   int32_t min_blocks;        // smallest share
-  int32_t* plan;             // [slots + 2]: first block of every slot, all blocks, blocks per share
+  int32_t rows_grid;         // combine_kernel: workgroups per (slot, head)
+  int32_t* plan;             // written by the attention kernel for combine_kernel: [0] blocks per share, [1] all
+                             // blocks of a head, [2 ..] first block of every sequence (stream) or slot (tile)
   float2* ml;                // [2 workgroups][BM]: m c, l
   float* po;                 // [2 workgroups][BM][D]: O
 };
@@ -185,48 +187,159 @@ __device__ __forceinline__ void make_plan(const AttentionArgs& a, const Launch& 
   __syncthreads();
 }
 
-// Calls work(tile, head, first block, end block, partial) for every piece of this workgroup; partial < 0:
-// the whole tile.  Uniform over the workgroup.
-template <int BM, int KB, typename Work>
-__device__ __forceinline__ void for_pieces(const AttentionArgs& a, const Launch& l, int* pre, int* wave_sum, Work work) {
-  Tile t;
-  if (!l.split) {
-    const int h = blockIdx.x % a.kv_heads;
-    const int slot = l.slots - 1 - (int)(blockIdx.x / a.kv_heads);     // late (long) tiles first
-    const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
-    if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t)) return;
-    work(t, h, 0, t.blocks, -1);
-    return;
-  }
-  make_plan<BM, KB>(a, l, pre, wave_sum);
-  const int all = pre[kMaxSlots];
+// Shares of a split launch: `per` blocks each, in order over (head, tile, block).
+struct Shares {
+  int64_t total;
+  int per;
+};
+
+__device__ __forceinline__ Shares shares_of(const AttentionArgs& a, const Launch& l, int all) {
   const int64_t total = (int64_t)all * a.kv_heads;
   const int64_t share = (total + l.workgroups - 1) / l.workgroups;
-  const int per = share > l.min_blocks ? (int)share : l.min_blocks;
-  if (blockIdx.x == 0) {
-    for (int j = threadIdx.x; j < l.slots; j += kThreads) l.plan[j] = pre[j];
-    if (threadIdx.x == 0) {
-      l.plan[l.slots] = all;
-      l.plan[l.slots + 1] = per;
+  return Shares{total, share > l.min_blocks ? (int)share : l.min_blocks};
+}
+
+// This workgroup's share.  Workgroups are dealt to the 8 XCDs in turn; neighbouring shares (mostly the same
+// head's keys) go to one XCD, and a launch with less work than workgroups still uses all XCDs.
+__device__ __forceinline__ int my_share(const Shares& s) {
+  const int used = (int)((s.total + s.per - 1) / s.per), each = (used + 7) >> 3;
+  const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  return i < each ? x * each + i : used;
+}
+
+// A value that is the same in every lane, as the scalar it is: what follows from it (addresses, loop bounds, the
+// page table's loads) then stays on the scalar unit.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The unsplit launch: one workgroup per (slot, head), late (long) tiles first.
+template <int BM, int KB>
+__device__ __forceinline__ bool whole_tile(const AttentionArgs& a, const Launch& l, Tile& t, int& h) {
+  h = blockIdx.x % a.kv_heads;
+  const int slot = l.slots - 1 - (int)(blockIdx.x / a.kv_heads);
+  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
+  return s >= 0 && tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t);
+}
+
+// Calls work(tile, head, first block, end block, partial) for every piece of this workgroup's share; partial <
+// 0: the whole tile.  Uniform over the workgroup.  Exact block counts per row tile (early tiles of a causal
+// chunk see fewer keys), planned by the whole workgroup over all slots.
+template <int BM, int KB, typename Work>
+__device__ __forceinline__ void tile_pieces(const AttentionArgs& a, const Launch& l, int* pre, int* wave_sum, Work work) {
+  Tile t;
+  int64_t u = 0, end = 1;
+  int all = 0, w = 0, h = 0;
+  if (l.split) {
+    make_plan<BM, KB>(a, l, pre, wave_sum);
+    all = uniform(pre[kMaxSlots]);
+    const Shares sh = shares_of(a, l, all);
+    if (blockIdx.x == 0) {
+      for (int j = threadIdx.x; j <= l.slots; j += kThreads) l.plan[2 + j] = pre[j];
+      if (threadIdx.x == 0) {
+        l.plan[0] = sh.per;
+        l.plan[1] = all;
+      }
     }
+    w = my_share(sh);
+    u = (int64_t)w * sh.per;
+    end = u + sh.per < sh.total ? u + sh.per : sh.total;
   }
-  // neighbouring shares (the same head's keys) on one XCD: workgroups are dealt to the 8 XCDs in turn
-  const int w = (blockIdx.x & 7) * (l.workgroups >> 3) + (blockIdx.x >> 3);
-  int64_t u = (int64_t)w * per;
-  const int64_t end = u + per < total ? u + per : total;
   while (u < end) {
-    const int h = (int)(u / all), rem = (int)(u - (int64_t)h * all);
-    int lo = 0, hi = l.slots;                     // pre[lo] <= rem < pre[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= rem) lo = mid; else hi = mid;
+    int off = 0, take, partial = -1;
+    if (l.split) {
+      h = (int)(u / all);
+      const int rem = (int)(u - (int64_t)h * all);
+      int lo = 0, hi = l.slots;                   // pre[lo] <= rem < pre[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (uniform(pre[mid]) <= rem) lo = mid; else hi = mid;
+      }
+      const int first = uniform(pre[lo]), count = uniform(pre[lo + 1]) - first;
+      off = rem - first;
+      take = end - u < count - off ? (int)(end - u) : count - off;
+      u += take;
+      const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= lo; });
+      if (s < 0 || !tile_of<BM, KB>(a, l, s, lo - first_slot<BM>(a, s), t)) continue;
+      if (take != count) partial = 2 * w + (off > 0 ? 0 : 1);
+    } else {
+      u = end;
+      if (!whole_tile<BM, KB>(a, l, t, h)) return;
+      take = t.blocks;
     }
-    const int count = pre[lo + 1] - pre[lo], off = rem - pre[lo];
-    const int take = end - u < count - off ? (int)(end - u) : count - off;
-    const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= lo; });
-    if (s >= 0 && tile_of<BM, KB>(a, l, s, lo - first_slot<BM>(a, s), t))
-      work(t, h, off, off + take, take == count ? -1 : 2 * w + (off > 0 ? 0 : 1));
-    u += take;
+    work(t, h, off, off + take, partial);
+  }
+}
+
+// Row tiles of sequence s in this launch, and the key blocks given to each of them: those of the whole
+// sequence (its new tokens are few here, so its tiles see nearly the same keys).
+template <int BM, int KB>
+__device__ __forceinline__ int sequence_tiles(const AttentionArgs& a, const Launch& l, int s, int& block0, int& blocks) {
+  const int c0 = cu_at(a, s), n = clamp_int(a.cu_q[s + 1], c0, a.tokens) - c0, rows = n * a.group;
+  const int len = clamp_int(a.kv_len[s], 0, a.table_width << a.page_shift);
+  const int64_t lo = a.window > 0 ? (int64_t)len - n - a.window + 1 : 0;
+  block0 = lo > 0 ? (int)lo / KB : 0;
+  const int nb = (len + KB - 1) / KB - block0;
+  blocks = nb > 1 ? nb : 1;
+  return rows > l.rows_lo && rows <= l.rows_hi ? (rows + BM - 1) / BM : 0;
+}
+
+// As tile_pieces, planned by every wavefront for itself over the sequences, 64 at a time: one round of
+// loads and a scan, no barrier.  All wavefronts write the same values to `pre`, so each may read it back at
+// once.
+template <int BM, int KB, typename Work>
+__device__ __forceinline__ void stream_pieces(const AttentionArgs& a, const Launch& l, int* pre, Work work) {
+  const int lane = threadIdx.x & 63;
+  Tile t;
+  int64_t u = 0, end = 1;
+  int all = 0, w = 0, h = 0;
+  if (l.split) {
+    for (int s0 = 0; s0 < a.num_seqs; s0 += 64) {
+      const int s = s0 + lane;
+      int units = 0, block0, blocks;
+      if (s < a.num_seqs) units = sequence_tiles<BM, KB>(a, l, s, block0, blocks) * blocks;
+      int inc = units;
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) {
+        const int o = __shfl_up(inc, m, 64);
+        if (lane >= m) inc += o;
+      }
+      if (s < a.num_seqs) pre[s] = all + inc - units;
+      all += __builtin_amdgcn_readlane(inc, 63);
+    }
+    if (lane == 0) pre[a.num_seqs] = all;
+    const Shares sh = shares_of(a, l, all);
+    if (blockIdx.x == 0 && threadIdx.x < 64) {
+      for (int j = lane; j <= a.num_seqs; j += 64) l.plan[2 + j] = pre[j];
+      if (lane == 0) {
+        l.plan[0] = sh.per;
+        l.plan[1] = all;
+      }
+    }
+    w = my_share(sh);
+    u = (int64_t)w * sh.per;
+    end = u + sh.per < sh.total ? u + sh.per : sh.total;
+  }
+  while (u < end) {
+    int off = 0, take, partial = -1;
+    if (l.split) {
+      h = (int)(u / all);
+      const int rem = (int)(u - (int64_t)h * all);
+      const int s = wave_search(a.num_seqs, [&](int j) { return pre[j] <= rem; });
+      int block0, blocks;
+      const int tiles = sequence_tiles<BM, KB>(a, l, s, block0, blocks);
+      const int at = rem - uniform(pre[s]), i = at / blocks;
+      off = at - i * blocks;
+      take = end - u < blocks - off ? (int)(end - u) : blocks - off;
+      u += take;
+      if (i >= tiles || !tile_of<BM, KB>(a, l, s, i, t)) continue;
+      t.block0 = block0;
+      t.blocks = blocks;
+      if (take != blocks) partial = 2 * w + (off > 0 ? 0 : 1);
+    } else {
+      u = end;
+      if (!whole_tile<BM, KB>(a, l, t, h)) return;
+      take = t.blocks;
+    }
+    work(t, h, off, off + take, partial);
   }
 }
 
@@ -372,12 +485,11 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
   __shared__ float merge[4][16][PT];
   __shared__ float2 merge_ml[4][16];
   __shared__ int pre[kMaxSlots + 1];
-  __shared__ int wave_sum[4];
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  for_pieces<BM, kStreamBlock>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
+  stream_pieces<BM, kStreamBlock>(a, l, pre, [&](const Tile& t, int h, int b0, int b1, int partial) {
     const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
     u32x4_t q[RB][ST];
     int lo[RB], hi[RB];
@@ -550,6 +662,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
               const f32x4_t d = mfma16_pv<FP8>(down, seen1[rb], f32x4_t{0, 0, 0, 0});
 #pragma unroll
               for (int y = 0; y < 4; ++y) o[rb][i * PER + x][y] += non_finite_part(u[y], d[y]);
+              __builtin_amdgcn_sched_barrier(0);     // rare: keep its registers few
             }
           }
         }
@@ -651,7 +764,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     return d * KB + ((ch ^ sw) & 7) * 8;
   };
 
-  for_pieces<BM, KB>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
+  tile_pieces<BM, KB>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
     const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
     const int wrow = wave * 32 * RW;         // the wavefront's first row in the tile
     const bool busy = wrow < t.rows;
@@ -774,7 +887,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     auto compute = [&](int b, int buf) {
       const int key0 = (t.block0 + b) * KB;
       if (!busy || key0 >= hi_max || key0 + KB <= lo_min) return;
-      const int gone = no_page[buf][0] | no_page[buf][1] << 1 | no_page[buf][2] << 2 | no_page[buf][3] << 3;
+      const int gone = uniform(no_page[buf][0] | no_page[buf][1] << 1 | no_page[buf][2] << 2 | no_page[buf][3] << 3);
       const bool partial_keys = gone != 0 || key0 + KB > hi_min || key0 < lo_max;
       f32x16_t s[RW][2];
 #pragma unroll
@@ -790,7 +903,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           for (int rw = 0; rw < RW; ++rw) s[rw][kb] = mfma32_bf16(ka, q[rw][st], s[rw][kb]);
         }
       }
-      const bool any_bad = bad_block[buf] == b;
+      const bool any_bad = uniform(bad_block[buf]) == b;
       u32x4_t pr[RW][4];
 #pragma unroll
       for (int rw = 0; rw < RW; ++rw) {
@@ -854,9 +967,14 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
               f32x16_t zero;
 #pragma unroll
               for (int y = 0; y < 16; ++y) zero[y] = 0.0f;
-              const f32x16_t u = mfma32_pv<FP8>(up, seen1, zero), d = mfma32_pv<FP8>(down, seen1, zero);
+              const f32x16_t u = mfma32_pv<FP8>(up, seen1, zero);
 #pragma unroll
-              for (int y = 0; y < 16; ++y) o[rw][i][y] += non_finite_part(u[y], d[y]);
+              for (int y = 0; y < 16; ++y) o[rw][i][y] += non_finite_part(u[y], 0.0f);
+              __builtin_amdgcn_sched_barrier(0);     // rare: keep its registers few
+              const f32x16_t d = mfma32_pv<FP8>(down, seen1, zero);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[rw][i][y] += non_finite_part(0.0f, d[y]);
+              __builtin_amdgcn_sched_barrier(0);
             }
           }
 #pragma unroll
@@ -914,24 +1032,35 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 
 // ---- joining the parts of cut segments ---------------------------------------------------------------
 
-// One workgroup per (slot, head, row); D / 4 lanes hold a part's row, 256 / (D / 4) parts at a time.
-template <int D, int BM, int KB>
+// Workgroups per (slot, head), a row each in turn; D / 4 lanes hold a part's row, 256 / (D / 4) parts at a time.
+// STREAM: shares were planned per sequence, otherwise per slot.
+template <int D, int BM, int KB, bool STREAM>
 __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Launch l) {
   constexpr int LP = D / 4, GR = kThreads / LP;
   __shared__ float4 part[GR][LP];
   __shared__ float red[4], lsum[GR];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int row = blockIdx.x % BM, rest = blockIdx.x / BM;
+  const int row0 = blockIdx.x % l.rows_grid, rest = blockIdx.x / l.rows_grid;
   const int h = rest % a.kv_heads, slot = rest / a.kv_heads;
-  const int all = l.plan[l.slots], per = l.plan[l.slots + 1];
-  const int p0 = l.plan[slot], count = l.plan[slot + 1] - p0;
-  if (count == 0) return;
+  const int per = l.plan[0], all = l.plan[1];
+  Tile t;
+  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
+  if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t)) return;
+  int p0, count;
+  if (STREAM) {
+    int block0;
+    sequence_tiles<BM, KB>(a, l, s, block0, count);
+    p0 = l.plan[2 + s] + (slot - first_slot<BM>(a, s)) * count;
+  } else {
+    p0 = l.plan[2 + slot];
+    count = l.plan[3 + slot] - p0;
+  }
+  if (count <= 0) return;
   const int64_t u0 = (int64_t)h * all + p0, u1 = u0 + count;
   const int w0 = (int)(u0 / per), w1 = (int)((u1 - 1) / per);
   if (w0 == w1) return;
-  Tile t;
-  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
-  if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t) || row >= t.rows) return;
+  for (int row = row0; row < t.rows; row += l.rows_grid) {
+  __syncthreads();
   auto index = [&](int w) { return (int64_t)(2 * w + (u0 < (int64_t)w * per ? 0 : 1)) * BM + row; };
   float mm = kLowest;
   for (int w = w0 + tid; w <= w1; w += kThreads) mm = __builtin_fmaxf(mm, l.ml[index(w)].x);
@@ -954,7 +1083,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
   part[g][x] = acc;
   if (x == 0) lsum[g] = ll;
   __syncthreads();
-  if (g != 0) return;
+  if (g != 0) continue;
   for (int i = 1; i < GR; ++i) {
     const float4 v = part[i][x];
     acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
@@ -967,6 +1096,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
   *reinterpret_cast<uint2*>(a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + x * 4) =
       make_uint2(bf16_pair(acc.x * f, acc.y * f), bf16_pair(acc.z * f, acc.w * f));
   if (a.lse && x == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
+  }
 }
 
 // ---- launching ----------------------------------------------------------------------------------------
@@ -978,6 +1108,7 @@ struct Choice {
   int64_t slots;
   bool split;
   int workgroups;
+  int rows_grid;             // workgroups per (slot, head) that join parts
 };
 
 struct Choices {
@@ -988,7 +1119,7 @@ size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 size_t split_bytes(const Choice& c, int dim) {
   if (!c.used || !c.split) return 0;
-  return align16((size_t)(c.slots + 2) * 4) + (size_t)2 * c.workgroups * c.bm * (8 + (size_t)dim * 4);
+  return align16((size_t)(c.slots + 3) * 4) + (size_t)2 * c.workgroups * c.bm * (8 + (size_t)dim * 4);
 }
 
 Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads, int64_t kv_heads, int dim) {
@@ -1004,7 +1135,9 @@ Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
   c.stream.slots = slots(c.stream.bm);
   c.stream.split = c.stream.slots <= kMaxSlots;
   c.stream.workgroups = dim == 256 ? 512 : 1024;
+  c.stream.rows_grid = (int)(rows < c.stream.bm ? rows : c.stream.bm);
   c.tile.bm = 128;
+  c.tile.rows_grid = c.tile.bm;
   c.tile.rows_lo = c.stream.used ? c.stream.bm : 0;
   c.tile.rows_hi = INT32_MAX;
   c.tile.slots = slots(c.tile.bm);
@@ -1013,7 +1146,7 @@ Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
   return c;
 }
 
-template <int D, int BM, int KB, typename Kernel>
+template <int D, int BM, int KB, bool STREAM, typename Kernel>
 int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_blocks, void* workspace, hipStream_t stream) {
   Launch l{};
   l.slots = (int32_t)c.slots;
@@ -1030,14 +1163,15 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
     grid = c.workgroups;
     char* p = static_cast<char*>(workspace);
     l.plan = reinterpret_cast<int32_t*>(p);
-    l.ml = reinterpret_cast<float2*>(p + align16((size_t)(c.slots + 2) * 4));
+    l.ml = reinterpret_cast<float2*>(p + align16((size_t)(c.slots + 3) * 4));
     l.po = reinterpret_cast<float*>(l.ml + (size_t)2 * c.workgroups * BM);
   }
   if (grid > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
   kernel<<<(unsigned)grid, kThreads, 0, stream>>>(a, l);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   if (l.split) {
-    combine_kernel<D, BM, KB><<<(unsigned)(c.slots * a.kv_heads * BM), kThreads, 0, stream>>>(a, l);
+    l.rows_grid = c.rows_grid;
+    combine_kernel<D, BM, KB, STREAM><<<(unsigned)(c.slots * a.kv_heads * c.rows_grid), kThreads, 0, stream>>>(a, l);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   }
   return NVFP4_OK;
@@ -1047,11 +1181,11 @@ template <int D, bool FP8>
 int launch_dim(const AttentionArgs& a, const Choices& c, void* workspace, hipStream_t stream) {
   if (c.stream.used) {
     const int st = c.stream.bm == 16
-        ? launch_one<D, 16, kStreamBlock>(stream_kernel<D, FP8, 1>, a, c.stream, 2, workspace, stream)
-        : launch_one<D, 32, kStreamBlock>(stream_kernel<D, FP8, 2>, a, c.stream, 2, workspace, stream);
+        ? launch_one<D, 16, kStreamBlock, true>(stream_kernel<D, FP8, 1>, a, c.stream, 2, workspace, stream)
+        : launch_one<D, 32, kStreamBlock, true>(stream_kernel<D, FP8, 2>, a, c.stream, 2, workspace, stream);
     if (st != NVFP4_OK) return st;
   }
-  if (c.tile.used) return launch_one<D, 128, kTileBlock>(tile_kernel<D, FP8, 1>, a, c.tile, 4, workspace, stream);
+  if (c.tile.used) return launch_one<D, 128, kTileBlock, false>(tile_kernel<D, FP8, 1>, a, c.tile, 4, workspace, stream);
   return NVFP4_OK;
 }
 
