@@ -395,20 +395,25 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   return FP8 ? ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
 }
 
-// A fragment of V taken apart: the finite elements (others 0) and two 0/1 indicators, of elements that
-// are +inf or NaN and of those that are -inf or NaN.  1 is 0x3C00 in fp16, 0x3F80 in bf16.
+// The dword without its non-finite elements.
 template <bool FP8>
-__device__ __forceinline__ void take_apart(u32x4_t v, u32x4_t& fin, u32x4_t& up, u32x4_t& down) {
-  constexpr uint32_t kExp = FP8 ? 0x7C007C00u : 0x7F807F80u, kStep = FP8 ? 0x04000400u : 0x00800080u;
-  constexpr uint32_t kMag = 0x7FFF7FFFu, kOne = FP8 ? 0x3C00u : 0x3F80u;
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  const uint32_t bits = non_finite<FP8>(w);
+  return FP8 ? w & ~((bits >> 7) * 0xFFu) : w & ~((bits >> 15) * 0xFFFFu);
+}
+
+// Which of a dword's elements are +inf or NaN (`up`), and -inf or NaN (`down`), one bit each; E4M3 has NaN only.
+template <bool FP8>
+__device__ __forceinline__ void non_finite_signs(uint32_t w, uint32_t& up, uint32_t& down) {
+  up = down = 0;
+  const uint32_t nf = non_finite<FP8>(w);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = v[i], nf = (((w & kExp) + kStep) & 0x80008000u) >> 15;     // 1 per non-finite half
-    const uint32_t nan = (((w & kMag) + (0x7FFF7FFFu - kExp)) & 0x80008000u) >> 15;
-    const uint32_t neg = (w & 0x80008000u) >> 15;
-    fin[i] = w & ~(nf * 0xFFFFu);
-    up[i] = (nf & (nan | (neg ^ 0x00010001u))) * kOne;
-    down[i] = (nf & (nan | neg)) * kOne;
+  for (int e = 0; e < (FP8 ? 4 : 2); ++e) {
+    const bool is = (nf >> (FP8 ? 8 * e + 7 : 16 * e + 15)) & 1;
+    const bool nan = FP8 || ((w >> (16 * e)) & 0x7Fu) != 0;
+    const bool neg = !FP8 && ((w >> (16 * e + 15)) & 1);
+    up |= (is && (nan || !neg) ? 1u : 0u) << e;
+    down |= (is && (nan || neg) ? 1u : 0u) << e;
   }
 }
 
@@ -431,9 +436,9 @@ __device__ __forceinline__ f32x16_t mfma32_pv(u32x4_t a, u32x4_t b, f32x16_t c) 
   return mfma32_bf16(a, b, c);
 }
 
-// What the non-finite values of V add to an output, given how many of each sign the row sees.
-__device__ __forceinline__ float non_finite_part(float up, float down) {
-  return (up > 0.0f ? __builtin_inff() : 0.0f) + (down > 0.0f ? -__builtin_inff() : 0.0f);
+// What the non-finite values of V that a row sees add to an output.
+__device__ __forceinline__ float non_finite_part(uint32_t up, uint32_t down) {
+  return (up ? __builtin_inff() : 0.0f) + (down ? -__builtin_inff() : 0.0f);
 }
 
 template <int W>
@@ -482,7 +487,10 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
   constexpr int NT = D / 16;                // output tiles, and channels per lane slice
   constexpr int VW = NT * E / 4;            // dwords of V per lane and key
   constexpr int PT = D + 4;                 // LDS pitch of the merge
-  __shared__ float merge[4][16][PT];
+  constexpr int MW = (D / 4 + 31) / 32;     // dwords of marks: a bit per output of a lane
+  __shared__ __align__(16) float merge[4][16][PT];
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(merge);      // in the loop, before the merge
+  static_assert(RB * 2 * MW * kThreads <= 4 * 16 * PT, "marks fit the merge buffer");
   __shared__ float2 merge_ml[4][16];
   __shared__ int pre[kMaxSlots + 1];
 
@@ -546,7 +554,9 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
     };
 
     // One block at a time: V of this block and K of the next are in flight while the other is used.
-    int p[2], pn[2];
+    bool marked = false;
+    __syncthreads();                          // the last piece's merge has been read
+    int p[2], pn[2], pv[2];
     pages(b0, p);
     load_k(b0, p);
     pages(b0 + 1, pn);
@@ -573,6 +583,8 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
           for (int rb = 0; rb < RB; ++rb) s[rb][g] = mfma16_bf16(ka, q[rb][st], s[rb][g]);
         }
       if (b + 1 < b1) load_k(b + 1, pn);
+      pv[0] = p[0];
+      pv[1] = p[1];
       p[0] = pn[0];
       p[1] = pn[1];
       pages(b + 2, pn);
@@ -582,6 +594,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         if (partial_keys) {
+          asm volatile("");        // a branch, not selects paid by every block
 #pragma unroll
           for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -630,47 +643,63 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
 #pragma unroll
         for (int i = 0; i < VW; ++i) bad |= non_finite<FP8>(vr[j][i]);
       const bool any_bad = __builtin_amdgcn_ballot_w64(bad != 0) != 0;
-      u32x4_t seen1[RB];
+      constexpr int PER = FP8 ? 4 : 2;
       if (any_bad) {
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = key0 + (i >> 1) * 16 + quarter * 4 + (i & 1) * 2;
-            const bool in = (valid >> (i >> 1)) & 1;
-            seen1[rb][i] = ((in && key >= lo[rb] && key < hi[rb] ? 1u : 0u) |
-                            (in && key + 1 >= lo[rb] && key + 1 < hi[rb] ? 0x10000u : 0u)) * (FP8 ? 0x3C00u : 0x3F80u);
-          }
+          for (int i = 0; i < VW; ++i) vr[j][i] = finite_part<FP8>(vr[j][i]);
       }
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = vr[j][i];
-        constexpr int PER = FP8 ? 4 : 2;
         u32x4_t va[PER];
         if constexpr (FP8) transpose_fp8(w, va); else transpose_bf16(w, va);
-        if (any_bad) {
-#pragma unroll
-          for (int x = 0; x < PER; ++x) {
-            u32x4_t fin, up, down;
-            take_apart<FP8>(va[x], fin, up, down);
-            va[x] = fin;
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-              const f32x4_t u = mfma16_pv<FP8>(up, seen1[rb], f32x4_t{0, 0, 0, 0});
-              const f32x4_t d = mfma16_pv<FP8>(down, seen1[rb], f32x4_t{0, 0, 0, 0});
-#pragma unroll
-              for (int y = 0; y < 4; ++y) o[rb][i * PER + x][y] += non_finite_part(u[y], d[y]);
-              __builtin_amdgcn_sched_barrier(0);     // rare: keep its registers few
-            }
-          }
-        }
 #pragma unroll
         for (int x = 0; x < PER; ++x)
 #pragma unroll
           for (int rb = 0; rb < RB; ++rb) o[rb][i * PER + x] = mfma16_pv<FP8>(va[x], pr[rb], o[rb][i * PER + x]);
       }
+      if (any_bad) {
+        // Rare: mark this lane's outputs that see a non-finite value, by reading the block's values again.
+        if (!marked)
+          for (int i = 0; i < RB * 2 * MW; ++i) marks[i * kThreads + tid] = 0;
+        marked = true;
+#pragma unroll 1
+        for (int kk = 0; kk < 32; ++kk) {
+          const int key = key0 + kk, page = kk < 16 ? pv[0] : pv[1];
+          if (key >= t.len || page < 0) continue;
+          const uint8_t* vp = a.v + page * a.v_page + head_at + (key & mask) * (D * E) + quarter * (4 * NT * E);
+          uint32_t seen = 0;
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) seen |= (key >= lo[rb] && key < hi[rb] ? 1u : 0u) << rb;
+#pragma unroll 1
+          for (int i = 0; i < NT * E; ++i) {           // the dwords of 4 slices of NT channels
+            uint32_t up, down;
+            non_finite_signs<FP8>(*reinterpret_cast<const uint32_t*>(vp + 4 * i), up, down);
+            const int bit = i * PER;
+            for (int rb = 0; rb < RB; ++rb) {
+              if (!((seen >> rb) & 1)) continue;
+              marks[((rb * 2) * MW + (bit >> 5)) * kThreads + tid] |= up << (bit & 31);
+              marks[((rb * 2 + 1) * MW + (bit >> 5)) * kThreads + tid] |= down << (bit & 31);
+            }
+          }
+        }
+      }
+    }
+    if (marked) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int bit = x * NT + i;
+            o[rb][i][x] += non_finite_part((marks[((rb * 2) * MW + (bit >> 5)) * kThreads + tid] >> (bit & 31)) & 1,
+                                           (marks[((rb * 2 + 1) * MW + (bit >> 5)) * kThreads + tid] >> (bit & 31)) & 1);
+          }
     }
 
     // the four wavefronts' parts, 16 rows at a time
@@ -741,15 +770,17 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
   constexpr int ST = D / 16;                // matrix steps of a score
   constexpr int DB = D / 32;                // output tiles
   constexpr int CH = D * E / 16;            // 16-byte chunks of a cached key
-  constexpr int KL = KB * CH / kThreads;    // key loads per thread
+  constexpr int KL = 16 * CH / 64;          // key loads per lane: 16 keys a wavefront
   constexpr int VQ = D / 4;                 // channel quads
-  constexpr int VI = (8 * VQ + kThreads - 1) / kThreads;   // value items per thread: 8 keys x 4 channels
+  constexpr int VI = 2 * VQ > 64 ? 2 * VQ / 64 : 1;        // value items per lane: 8 keys x 4 channels
   __shared__ __align__(16) uint16_t ks[2][KB * D];
   __shared__ __align__(16) uint16_t vt[2][D * KB];
   __shared__ int pre[kMaxSlots + 1];
   __shared__ int wave_sum[4];
   __shared__ int bad_block[2];              // block whose values hold something non-finite
   __shared__ int no_page[2][4];             // per 16 keys of a block
+  constexpr int MW = D / 64;                // dwords of marks: a bit per output of a lane
+  __shared__ uint32_t marks[RW * 2 * MW][kThreads];
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -763,6 +794,9 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     const int sw = ((d >> 1) & 7) ^ ((d >> 4) & 1);
     return d * KB + ((ch ^ sw) & 7) * 8;
   };
+
+  const int v_quad = lane % VQ;
+  auto v_grp = [&](int i) { return VI > 1 ? i : (lane / VQ) & 1; };    // which 8 of the wavefront's 16 keys
 
   tile_pieces<BM, KB>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
     const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
@@ -817,39 +851,29 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     const int mask = (1 << a.page_shift) - 1;
     uint4 kr[KL];
     uint32_t vr[VI][8][E];                   // 4 channels of 8 keys
-    // block b of the piece into registers
-    auto fetch = [&](int b) {
-      const int key0 = (t.block0 + b) * KB;
+    // Wavefront w brings in keys 16 w .. 16 w + 15 of a block, which lie in one page.
+    auto my_page = [&](int b) { return b < b1 ? page_of(a, t, (t.block0 + b) * KB + wave * 16) : -1; };
+    auto fetch = [&](int b, int p) {
+      const int in = ((t.block0 + b) * KB + wave * 16) & mask;
+      const uint8_t* kp = a.k + (p >= 0 ? p : 0) * a.k_page + head_at + in * (D * E);
+      const uint8_t* vp = a.v + (p >= 0 ? p : 0) * a.v_page + head_at + in * (D * E);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const int at = i * kThreads + tid, key = key0 + at / CH, ch = at % CH;
-        const int p = page_of(a, t, key);
-        kr[i] = *reinterpret_cast<const uint4*>(a.k + (p >= 0 ? p : 0) * a.k_page + head_at + (key & mask) * (D * E) + ch * 16);
-      }
+      for (int i = 0; i < KL; ++i) kr[i] = *reinterpret_cast<const uint4*>(kp + (i * 64 + lane) * 16);
 #pragma unroll
       for (int i = 0; i < VI; ++i) {
-        const int at = i * kThreads + tid, grp = at / VQ, quad = at % VQ;   // grp: chunk of 8 keys
-        if (8 * VQ % kThreads != 0 && grp >= 8) continue;
-        const int key = key0 + (grp >> 1) * 16 + (grp & 1) * 4;
-        const int p = page_of(a, t, key);
-        const uint8_t* vp = a.v + (p >= 0 ? p : 0) * a.v_page + head_at + (key & mask) * (D * E) + quad * (4 * E);
+        if (VQ < 32 && lane >= 2 * VQ) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t w[E];
-          const int dk = (j & 3) + (j >> 2) * 8;
-          load_words<E>(vp + dk * (D * E), w);
-#pragma unroll
-          for (int x = 0; x < E; ++x) vr[i][j][x] = p >= 0 && key + dk < t.len ? w[x] : 0u;
-        }
+        for (int j = 0; j < 8; ++j)
+          load_words<E>(vp + ((j & 3) + (j >> 2) * 8 + v_grp(i) * 4) * (D * E) + v_quad * (4 * E), vr[i][j]);
       }
     };
     // registers to LDS buffer `buf`
-    auto store = [&](int b, int buf) {
-      const int key0 = (t.block0 + b) * KB;
-      if (tid < 4) no_page[buf][tid] = page_of(a, t, key0 + tid * 16) < 0;
+    auto store = [&](int b, int p, int buf) {
+      const int key0 = (t.block0 + b) * KB + wave * 16;
+      if (lane == 0) no_page[buf][wave] = p < 0;
 #pragma unroll
       for (int i = 0; i < KL; ++i) {
-        const int at = i * kThreads + tid, key = at / CH, ch = at % CH;
+        const int at = i * 64 + lane, key = wave * 16 + at / CH, ch = at % CH;
         const uint4 w = kr[i];
         if (FP8) {
           *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch)]) =
@@ -860,30 +884,50 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           *reinterpret_cast<uint4*>(&ks[buf][k_chunk(key, ch)]) = w;
         }
       }
+      if (VQ < 32 && lane >= 2 * VQ) return;
+      if (p < 0 || key0 + 16 > t.len) {      // keys that do not exist: zero their values
+#pragma unroll
+        for (int i = 0; i < VI; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int x = 0; x < E; ++x)
+              vr[i][j][x] = p >= 0 && key0 + (j & 3) + (j >> 2) * 8 + v_grp(i) * 4 < t.len ? vr[i][j][x] : 0u;
+      }
       uint32_t bad = 0;
 #pragma unroll
+      for (int i = 0; i < VI; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int x = 0; x < E; ++x) bad |= non_finite<FP8>(vr[i][j][x]);
+      if (__builtin_amdgcn_ballot_w64(bad != 0) != 0) {
+        bad_block[buf] = b;                  // every writer writes the same
+#pragma unroll
+        for (int i = 0; i < VI; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int x = 0; x < E; ++x) vr[i][j][x] = finite_part<FP8>(vr[i][j][x]);
+      }
+#pragma unroll
       for (int i = 0; i < VI; ++i) {
-        const int at = i * kThreads + tid, grp = at / VQ, quad = at % VQ;
-        if (8 * VQ % kThreads != 0 && grp >= 8) continue;
 #pragma unroll
         for (int x = 0; x < E; ++x) {
           uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            w[j] = vr[i][j][x];
-            bad |= non_finite<FP8>(w[j]);
-          }
+          for (int j = 0; j < 8; ++j) w[j] = vr[i][j][x];
           constexpr int PER = FP8 ? 4 : 2;
           u32x4_t va[PER];
           if constexpr (FP8) transpose_fp8(w, va); else transpose_bf16(w, va);
 #pragma unroll
           for (int y = 0; y < PER; ++y)
-            *reinterpret_cast<u32x4_t*>(&vt[buf][v_chunk(quad * 4 + x * PER + y, grp)]) = va[y];
+            *reinterpret_cast<u32x4_t*>(&vt[buf][v_chunk(v_quad * 4 + x * PER + y, wave * 2 + v_grp(i))]) = va[y];
         }
       }
-      if (bad) bad_block[buf] = b;           // every writer writes the same
     };
 
+    bool marked = false;
     auto compute = [&](int b, int buf) {
       const int key0 = (t.block0 + b) * KB;
       if (!busy || key0 >= hi_max || key0 + KB <= lo_min) return;
@@ -903,11 +947,11 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           for (int rw = 0; rw < RW; ++rw) s[rw][kb] = mfma32_bf16(ka, q[rw][st], s[rw][kb]);
         }
       }
-      const bool any_bad = uniform(bad_block[buf]) == b;
       u32x4_t pr[RW][4];
 #pragma unroll
       for (int rw = 0; rw < RW; ++rw) {
         if (partial_keys) {
+          asm volatile("");        // a branch, not selects paid by every block
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -949,53 +993,70 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          u32x4_t va = *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
-          if (any_bad) {
-            u32x4_t fin, up, down;
-            take_apart<FP8>(va, fin, up, down);
-            va = fin;
-#pragma unroll
-            for (int rw = 0; rw < RW; ++rw) {
-              u32x4_t seen1;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int key = key0 + g * 16 + 8 * (y >> 1) + 4 * half + (y & 1) * 2;
-                const bool in = !((gone >> g) & 1);
-                seen1[y] = ((in && key >= lo[rw] && key < hi[rw] ? 1u : 0u) |
-                            (in && key + 1 >= lo[rw] && key + 1 < hi[rw] ? 0x10000u : 0u)) * (FP8 ? 0x3C00u : 0x3F80u);
-              }
-              f32x16_t zero;
-#pragma unroll
-              for (int y = 0; y < 16; ++y) zero[y] = 0.0f;
-              const f32x16_t u = mfma32_pv<FP8>(up, seen1, zero);
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[rw][i][y] += non_finite_part(u[y], 0.0f);
-              __builtin_amdgcn_sched_barrier(0);     // rare: keep its registers few
-              const f32x16_t d = mfma32_pv<FP8>(down, seen1, zero);
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[rw][i][y] += non_finite_part(0.0f, d[y]);
-              __builtin_amdgcn_sched_barrier(0);
-            }
-          }
+          const u32x4_t va = *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
 #pragma unroll
           for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
         }
+      if (uniform(bad_block[buf]) == b) {
+        // Rare: mark this lane's outputs that see a non-finite value, by reading the block's values again.
+        if (!marked)
+          for (int i = 0; i < RW * 2 * MW; ++i) marks[i][tid] = 0;
+        marked = true;
+#pragma unroll 1
+        for (int kk = 0; kk < KB; ++kk) {
+          const int key = key0 + kk, p = page_of(a, t, key);
+          if (p < 0) continue;
+          const uint8_t* vp = a.v + p * a.v_page + head_at + (key & mask) * (D * E) + half * (4 * E);
+          uint32_t seen = 0;
+#pragma unroll
+          for (int rw = 0; rw < RW; ++rw) seen |= (key >= lo[rw] && key < hi[rw] ? 1u : 0u) << rw;
+#pragma unroll 1
+          for (int i = 0; i < D / 8 * E; ++i) {          // dwords of this lane's 4-channel groups, 8 channels apart
+            constexpr int PER = FP8 ? 4 : 2;
+            uint32_t up, down;
+            non_finite_signs<FP8>(*reinterpret_cast<const uint32_t*>(vp + (i / E) * (8 * E) + (i % E) * 4), up, down);
+            const int bit = i * PER;
+            for (int rw = 0; rw < RW; ++rw) {
+              if (!((seen >> rw) & 1)) continue;
+              marks[(rw * 2) * MW + (bit >> 5)][tid] |= up << (bit & 31);
+              marks[(rw * 2 + 1) * MW + (bit >> 5)][tid] |= down << (bit & 31);
+            }
+          }
+        }
+      }
     };
 
     __syncthreads();                          // the last piece's readers are done
     if (tid < 2) bad_block[tid] = -1;
-    fetch(b0);
+    int p = my_page(b0), pn = my_page(b0 + 1);     // page numbers come a block ahead of their loads
+    fetch(b0, p);
     __syncthreads();
-    store(b0, 0);
+    store(b0, p, 0);
     __syncthreads();
     for (int b = b0; b < b1; ++b) {
       const int buf = (b - b0) & 1;
-      if (b + 1 < b1) fetch(b + 1);
+      p = pn;
+      if (b + 1 < b1) {
+        fetch(b + 1, p);
+        pn = my_page(b + 2);
+      }
       compute(b, buf);
-      if (b + 1 < b1) store(b + 1, buf ^ 1);
+      if (b + 1 < b1) store(b + 1, p, buf ^ 1);
       __syncthreads();
     }
 
+    if (marked) {
+#pragma unroll
+      for (int rw = 0; rw < RW; ++rw)
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int bit = i * 16 + x;
+            o[rw][i][x] += non_finite_part((marks[(rw * 2) * MW + (bit >> 5)][tid] >> (bit & 31)) & 1,
+                                           (marks[(rw * 2 + 1) * MW + (bit >> 5)][tid] >> (bit & 31)) & 1);
+          }
+    }
     const float vs = FP8 ? a.v_scale[h * a.scale_stride] : 1.0f;
 #pragma unroll
     for (int rw = 0; rw < RW; ++rw) {
