@@ -755,6 +755,12 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
   });
 }
 
+// Ends a step of a hand-ordered instruction sequence.  Left to itself the compiler reads each LDS operand right
+// before its use, waits out the latency for every matrix instruction, and puts all exponentials in front of
+// all products; with a boundary after every matrix instruction the reads run four ahead and the vector
+// instructions between two products execute while the matrix pipe is busy.
+__device__ __forceinline__ void step() { __builtin_amdgcn_sched_barrier(0); }
+
 // ---- many rows ---------------------------------------------------------------------------------------
 
 // Four wavefronts of RW blocks of 32 rows each; lane % 32 is the row, half = lane / 32.
@@ -934,20 +940,31 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       const int gone = uniform(no_page[buf][0] | no_page[buf][1] << 1 | no_page[buf][2] << 2 | no_page[buf][3] << 3);
       const bool partial_keys = gone != 0 || key0 + KB > hi_min || key0 < lo_max;
       f32x16_t s[RW][2];
+      {
+        constexpr int AHEAD = 4;
+        u32x4_t f[AHEAD];
+        auto read = [&](int x) {
+          return *reinterpret_cast<const u32x4_t*>(&ks[buf][k_chunk((x / ST) * 32 + n, (x % ST) * 2 + half)]);
+        };
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+        for (int x = 0; x < AHEAD; ++x) f[x] = read(x);
+        step();
 #pragma unroll
-        for (int rw = 0; rw < RW; ++rw)
+        for (int x = 0; x < 2 * ST; ++x) {
+          const u32x4_t ka = f[x % AHEAD];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) s[rw][kb][x] = 0.0f;
+          for (int rw = 0; rw < RW; ++rw) {
+            f32x16_t z;
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          const u32x4_t ka = *reinterpret_cast<const u32x4_t*>(&ks[buf][k_chunk(kb * 32 + n, st * 2 + half)]);
-#pragma unroll
-          for (int rw = 0; rw < RW; ++rw) s[rw][kb] = mfma32_bf16(ka, q[rw][st], s[rw][kb]);
+            for (int y = 0; y < 16; ++y) z[y] = 0.0f;
+            s[rw][x / ST] = mfma32_bf16(ka, q[rw][x % ST], x % ST == 0 ? z : s[rw][x / ST]);
+          }
+          if (x + AHEAD < 2 * ST) f[x % AHEAD] = read(x + AHEAD);
+          step();
         }
       }
       u32x4_t pr[RW][4];
+      float mc[RW];
 #pragma unroll
       for (int rw = 0; rw < RW; ++rw) {
         if (partial_keys) {
@@ -974,29 +991,52 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 #pragma unroll
           for (int i = 0; i < DB; ++i) o[rw][i] *= f0;
         }
-        const float mc = m[rw] == kLowest ? 0.0f : m[rw] * c;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float p8[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              p8[j] = exp2_fast(__builtin_fmaf(s[rw][kb][g * 8 + j], c, -mc));
-              sum[rw] += p8[j];
-            }
-            pr[rw][kb * 2 + g] = u32x4_t{p_pair<FP8>(p8[0], p8[1]), p_pair<FP8>(p8[2], p8[3]), p_pair<FP8>(p8[4], p8[5]),
-                                         p_pair<FP8>(p8[6], p8[7])};
-          }
+        mc[rw] = m[rw] == kLowest ? 0.0f : m[rw] * c;
       }
+      // Exponentials of 8 keys (group g) and the product with V, a group behind.
+      {
+        float p8[RW][8];
+        u32x4_t f[DB];
+        auto read = [&](int g, int i) {
+          return *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
+        };
+        auto exps = [&](int g, int j) {
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
+          for (int rw = 0; rw < RW; ++rw) {
+            p8[rw][j] = exp2_fast(__builtin_fmaf(s[rw][g >> 1][(g & 1) * 8 + j], c, -mc[rw]));
+            sum[rw] += p8[rw][j];
+          }
+        };
+        auto pack = [&](int g) {
+#pragma unroll
+          for (int rw = 0; rw < RW; ++rw)
+            pr[rw][g] = u32x4_t{p_pair<FP8>(p8[rw][0], p8[rw][1]), p_pair<FP8>(p8[rw][2], p8[rw][3]),
+                                p_pair<FP8>(p8[rw][4], p8[rw][5]), p_pair<FP8>(p8[rw][6], p8[rw][7])};
+        };
+#pragma unroll
+        for (int i = 0; i < DB; ++i) f[i] = read(0, i);
+        step();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) exps(0, j);
+        pack(0);
+        step();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const u32x4_t va = *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
 #pragma unroll
-          for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
+          for (int i = 0; i < DB; ++i) {
+            const u32x4_t va = f[i];
+#pragma unroll
+            for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
+            if (g < 3) {
+              f[i] = read(g + 1, i);
+#pragma unroll
+              for (int j = i * 8 / DB; j < (i + 1) * 8 / DB; ++j) exps(g + 1, j);
+              if (i == DB - 1) pack(g + 1);
+            }
+            step();
+          }
         }
+      }
       if (uniform(bad_block[buf]) == b) {
         // Rare: mark this lane's outputs that see a non-finite value, by reading the block's values again.
         if (!marked)
