@@ -457,6 +457,16 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// Maximum and sum of x over lanes 32 apart (and, for the 16-row kernel, 16 apart): the two swapped halves.
+__device__ __forceinline__ float max_across_32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_across_16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // m c of a running maximum; a row that has seen no key keeps the lowest value.
@@ -590,7 +600,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
       pages(b + 2, pn);
 
       const bool partial_keys = valid != 3 || key0 + 32 > t.hi_min || key0 < t.lo_max;
-      u32x4_t pr[RB];
+      u32x4_t pr[RB] = {};
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         if (partial_keys) {
@@ -609,8 +619,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx = __builtin_fmaxf(mx, s[rb][g][i]);
-        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+        mx = max_across_32(max_across_16(mx));
         if (__builtin_amdgcn_ballot_w64((mx - m[rb]) * c > kLazy) != 0) {
           const float f0 = exp2_fast((m[rb] - mx) * c);
           m[rb] = mx;
@@ -624,9 +633,8 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
         for (int j = 0; j < 8; ++j) {
           p8[j] = exp2_fast(__builtin_fmaf(s[rb][j >> 2][j & 3], c, -mc));
           sum[rb] += p8[j];
+          if (j & 1) pr[rb][j >> 1] = p_pair<FP8>(p8[j - 1], p8[j]);
         }
-        pr[rb] = u32x4_t{p_pair<FP8>(p8[0], p8[1]), p_pair<FP8>(p8[2], p8[3]), p_pair<FP8>(p8[4], p8[5]),
-                         p_pair<FP8>(p8[6], p8[7])};
       }
 
       if (valid != 3 || key0 + 32 > t.len) {             // keys that do not exist: zero their values
@@ -939,104 +947,6 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       if (!busy || key0 >= hi_max || key0 + KB <= lo_min) return;
       const int gone = uniform(no_page[buf][0] | no_page[buf][1] << 1 | no_page[buf][2] << 2 | no_page[buf][3] << 3);
       const bool partial_keys = gone != 0 || key0 + KB > hi_min || key0 < lo_max;
-      f32x16_t s[RW][2];
-      {
-        constexpr int AHEAD = 4;
-        u32x4_t f[AHEAD];
-        auto read = [&](int x) {
-          return *reinterpret_cast<const u32x4_t*>(&ks[buf][k_chunk((x / ST) * 32 + n, (x % ST) * 2 + half)]);
-        };
-#pragma unroll
-        for (int x = 0; x < AHEAD; ++x) f[x] = read(x);
-        step();
-#pragma unroll
-        for (int x = 0; x < 2 * ST; ++x) {
-          const u32x4_t ka = f[x % AHEAD];
-#pragma unroll
-          for (int rw = 0; rw < RW; ++rw) {
-            f32x16_t z;
-#pragma unroll
-            for (int y = 0; y < 16; ++y) z[y] = 0.0f;
-            s[rw][x / ST] = mfma32_bf16(ka, q[rw][x % ST], x % ST == 0 ? z : s[rw][x / ST]);
-          }
-          if (x + AHEAD < 2 * ST) f[x % AHEAD] = read(x + AHEAD);
-          step();
-        }
-      }
-      u32x4_t pr[RW][4];
-      float mc[RW];
-#pragma unroll
-      for (int rw = 0; rw < RW; ++rw) {
-        if (partial_keys) {
-          asm volatile("");        // a branch, not selects paid by every block
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const int key = key0 + kb * 32 + 8 * (x >> 2) + 4 * half + (x & 3);
-              const bool seen = !((gone >> (kb * 2 + (x >> 3))) & 1) && key >= lo[rw] && key < hi[rw];
-              s[rw][kb][x] = seen ? s[rw][kb][x] : -__builtin_inff();
-            }
-        }
-        float mx = m[rw];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[rw][kb][x]);
-        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-        if (__builtin_amdgcn_ballot_w64((mx - m[rw]) * c > kLazy) != 0) {
-          const float f0 = exp2_fast((m[rw] - mx) * c);
-          m[rw] = mx;
-          sum[rw] *= f0;
-#pragma unroll
-          for (int i = 0; i < DB; ++i) o[rw][i] *= f0;
-        }
-        mc[rw] = m[rw] == kLowest ? 0.0f : m[rw] * c;
-      }
-      // Exponentials of 8 keys (group g) and the product with V, a group behind.
-      {
-        float p8[RW][8];
-        u32x4_t f[DB];
-        auto read = [&](int g, int i) {
-          return *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
-        };
-        auto exps = [&](int g, int j) {
-#pragma unroll
-          for (int rw = 0; rw < RW; ++rw) {
-            p8[rw][j] = exp2_fast(__builtin_fmaf(s[rw][g >> 1][(g & 1) * 8 + j], c, -mc[rw]));
-            sum[rw] += p8[rw][j];
-          }
-        };
-        auto pack = [&](int g) {
-#pragma unroll
-          for (int rw = 0; rw < RW; ++rw)
-            pr[rw][g] = u32x4_t{p_pair<FP8>(p8[rw][0], p8[rw][1]), p_pair<FP8>(p8[rw][2], p8[rw][3]),
-                                p_pair<FP8>(p8[rw][4], p8[rw][5]), p_pair<FP8>(p8[rw][6], p8[rw][7])};
-        };
-#pragma unroll
-        for (int i = 0; i < DB; ++i) f[i] = read(0, i);
-        step();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) exps(0, j);
-        pack(0);
-        step();
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-#pragma unroll
-          for (int i = 0; i < DB; ++i) {
-            const u32x4_t va = f[i];
-#pragma unroll
-            for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
-            if (g < 3) {
-              f[i] = read(g + 1, i);
-#pragma unroll
-              for (int j = i * 8 / DB; j < (i + 1) * 8 / DB; ++j) exps(g + 1, j);
-              if (i == DB - 1) pack(g + 1);
-            }
-            step();
-          }
-        }
-      }
       if (uniform(bad_block[buf]) == b) {
         // Rare: mark this lane's outputs that see a non-finite value, by reading the block's values again.
         if (!marked)
@@ -1061,6 +971,97 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
               marks[(rw * 2) * MW + (bit >> 5)][tid] |= up << (bit & 31);
               marks[(rw * 2 + 1) * MW + (bit >> 5)][tid] |= down << (bit & 31);
             }
+          }
+        }
+      }
+      f32x16_t s[RW][2];
+      {
+        constexpr int AHEAD = 4;
+        u32x4_t f[AHEAD];
+        auto read = [&](int x) {
+          return *reinterpret_cast<const u32x4_t*>(&ks[buf][k_chunk((x / ST) * 32 + n, (x % ST) * 2 + half)]);
+        };
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) f[x] = read(x);
+        step();
+#pragma unroll
+        for (int x = 0; x < 2 * ST; ++x) {
+          const u32x4_t ka = f[x % AHEAD];
+#pragma unroll
+          for (int rw = 0; rw < RW; ++rw) {
+            f32x16_t z;
+#pragma unroll
+            for (int y = 0; y < 16; ++y) z[y] = 0.0f;
+            s[rw][x / ST] = mfma32_bf16(ka, q[rw][x % ST], x % ST == 0 ? z : s[rw][x / ST]);
+          }
+          if (x + AHEAD < 2 * ST) f[x % AHEAD] = read(x + AHEAD);
+          step();
+        }
+      }
+      u32x4_t pr[RW][4] = {};
+      float mc[RW];
+#pragma unroll
+      for (int rw = 0; rw < RW; ++rw) {
+        if (partial_keys) {
+          asm volatile("");        // a branch, not selects paid by every block
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const int key = key0 + kb * 32 + 8 * (x >> 2) + 4 * half + (x & 3);
+              const bool seen = !((gone >> (kb * 2 + (x >> 3))) & 1) && key >= lo[rw] && key < hi[rw];
+              s[rw][kb][x] = seen ? s[rw][kb][x] : -__builtin_inff();
+            }
+        }
+        float mx = m[rw];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[rw][kb][x]);
+        mx = max_across_32(mx);
+        if (__builtin_amdgcn_ballot_w64((mx - m[rw]) * c > kLazy) != 0) {
+          const float f0 = exp2_fast((m[rw] - mx) * c);
+          m[rw] = mx;
+          sum[rw] *= f0;
+#pragma unroll
+          for (int i = 0; i < DB; ++i) o[rw][i] *= f0;
+        }
+        mc[rw] = m[rw] == kLowest ? 0.0f : m[rw] * c;
+      }
+      // Exponentials of 8 keys (group g) and the product with V, a group behind.
+      {
+        float p8[RW][8];
+        u32x4_t f[DB];
+        auto read = [&](int g, int i) {
+          return *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
+        };
+        auto exps = [&](int g, int j) {
+#pragma unroll
+          for (int rw = 0; rw < RW; ++rw) {
+            p8[rw][j] = exp2_fast(__builtin_fmaf(s[rw][g >> 1][(g & 1) * 8 + j], c, -mc[rw]));
+            sum[rw] += p8[rw][j];
+            if (j & 1) pr[rw][g][j >> 1] = p_pair<FP8>(p8[rw][j - 1], p8[rw][j]);
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < DB; ++i) f[i] = read(0, i);
+        step();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) exps(0, j);
+        step();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int i = 0; i < DB; ++i) {
+            const u32x4_t va = f[i];
+#pragma unroll
+            for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
+            if (g < 3) {
+              f[i] = read(g + 1, i);
+#pragma unroll
+              for (int j = i * 8 / DB; j < (i + 1) * 8 / DB; ++j) exps(g + 1, j);
+            }
+            step();
           }
         }
       }
