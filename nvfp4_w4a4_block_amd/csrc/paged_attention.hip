@@ -136,7 +136,7 @@ __device__ __forceinline__ void row_range(const AttentionArgs& a, const Tile& t,
 // Page of the 16-aligned key group at `key` (16 keys never straddle a page): its number, or -1.
 __device__ __forceinline__ int page_of(const AttentionArgs& a, const Tile& t, int key) {
   if (key >= t.len) return -1;
-  const int p = a.page_table[t.s * a.table_stride + (key >> a.page_shift)];
+  const int p = scalar_load(a.page_table + t.s * a.table_stride + (key >> a.page_shift));
   return (uint32_t)p < (uint32_t)a.num_pages ? p : -1;
 }
 
@@ -781,6 +781,9 @@ template <int D, bool FP8, int RW>
 __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_kernel(AttentionArgs a, Launch l) {
   constexpr int E = FP8 ? 1 : 2;
   constexpr int BM = 128 * RW, KB = kTileBlock;
+  // With one wavefront per SIMD half of its 512 registers are accumulation registers, which only matrix
+  // instructions and loads address: the output and the queries are kept there.
+  constexpr bool kAcc = RW * D > 128;
   constexpr int ST = D / 16;                // matrix steps of a score
   constexpr int DB = D / 32;                // output tiles
   constexpr int CH = D * E / 16;            // 16-byte chunks of a cached key
@@ -849,6 +852,12 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       }
     }
 
+    if constexpr (kAcc) {
+#pragma unroll
+      for (int rw = 0; rw < RW; ++rw)
+#pragma unroll
+        for (int st = 0; st < ST; ++st) asm volatile("" : "+a"(q[rw][st]));
+    }
     f32x16_t o[RW][DB];
     float m[RW], sum[RW];
 #pragma unroll
@@ -1064,6 +1073,12 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
             step();
           }
         }
+      }
+      if constexpr (kAcc) {
+#pragma unroll
+        for (int rw = 0; rw < RW; ++rw)
+#pragma unroll
+          for (int i = 0; i < DB; ++i) asm volatile("" : "+a"(o[rw][i]));
       }
     };
 
