@@ -81,9 +81,10 @@ struct Tile {
 
 __device__ __forceinline__ int cu_at(const AttentionArgs& a, int j) { return clamp_int(a.cu_q[j], 0, a.tokens); }
 
+// First slot of sequence s: its own number where this launch's sequences have one tile each.
 template <int BM>
-__device__ __forceinline__ int first_slot(const AttentionArgs& a, int s) {
-  return (int)((uint32_t)(cu_at(a, s) * a.group) / BM) + s;
+__device__ __forceinline__ int first_slot(const AttentionArgs& a, const Launch& l, int s) {
+  return l.rows_hi <= BM ? s : (int)((uint32_t)(cu_at(a, s) * a.group) / BM) + s;
 }
 
 // Tile `i` of sequence s; false if there is none or it is another launch's.
@@ -152,12 +153,12 @@ __device__ __forceinline__ void make_plan(const AttentionArgs& a, const Launch& 
   Tile t;
   if (a.num_seqs <= 16) {              // few sequences: threads over the tiles of each
     for (int s = 0; s < a.num_seqs; ++s) {
-      const int base = first_slot<BM>(a, s);
+      const int base = first_slot<BM>(a, l, s);
       for (int i = tid; base + i < l.slots && tile_of<BM, KB>(a, l, s, i, t); i += kThreads) pre[base + i] = t.blocks;
     }
   } else {                             // many: one thread per sequence, few tiles each
     for (int s = tid; s < a.num_seqs; s += kThreads) {
-      const int base = first_slot<BM>(a, s);
+      const int base = first_slot<BM>(a, l, s);
       for (int i = 0; base + i < l.slots && tile_of<BM, KB>(a, l, s, i, t); ++i) pre[base + i] = t.blocks;
     }
   }
@@ -216,8 +217,8 @@ template <int BM, int KB>
 __device__ __forceinline__ bool whole_tile(const AttentionArgs& a, const Launch& l, Tile& t, int& h) {
   h = blockIdx.x % a.kv_heads;
   const int slot = l.slots - 1 - (int)(blockIdx.x / a.kv_heads);
-  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
-  return s >= 0 && tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t);
+  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, l, j) <= slot; });
+  return s >= 0 && tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, l, s), t);
 }
 
 // Calls work(tile, head, first block, end block, partial) for every piece of this workgroup's share; partial <
@@ -257,8 +258,8 @@ __device__ __forceinline__ void tile_pieces(const AttentionArgs& a, const Launch
       off = rem - first;
       take = end - u < count - off ? (int)(end - u) : count - off;
       u += take;
-      const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= lo; });
-      if (s < 0 || !tile_of<BM, KB>(a, l, s, lo - first_slot<BM>(a, s), t)) continue;
+      const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, l, j) <= lo; });
+      if (s < 0 || !tile_of<BM, KB>(a, l, s, lo - first_slot<BM>(a, l, s), t)) continue;
       if (take != count) partial = 2 * w + (off > 0 ? 0 : 1);
     } else {
       u = end;
@@ -1149,70 +1150,94 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 
 // ---- joining the parts of cut segments ---------------------------------------------------------------
 
-// Workgroups per (slot, head), a row each in turn; D / 4 lanes hold a part's row, 256 / (D / 4) parts at a time.
+// A row's parts are read by `PARTS` groups of D / 4 lanes (4 channels each) and added in a fixed order; a workgroup
+// takes 256 / (D / 4) / PARTS rows at a time of one (slot, head), and rows_grid workgroups share its rows.  Few
+// row tiles are cut into many parts (PARTS as large as fits), many row tiles into few (PARTS = 1: no exchange).
 // STREAM: shares were planned per sequence, otherwise per slot.
-template <int D, int BM, int KB, bool STREAM>
+template <int D, int BM, int KB, bool STREAM, int PARTS>
 __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Launch l) {
-  constexpr int LP = D / 4, GR = kThreads / LP;
-  __shared__ float4 part[GR][LP];
-  __shared__ float red[4], lsum[GR];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int row0 = blockIdx.x % l.rows_grid, rest = blockIdx.x / l.rows_grid;
+  constexpr int LP = D / 4, GR = kThreads / LP, ROWS = GR / PARTS;
+  __shared__ float4 part[PARTS > 1 ? GR : 1][LP];
+  __shared__ float2 part_ml[PARTS > 1 ? GR : 1];
+  const int tid = threadIdx.x;
+  const int rest = blockIdx.x / l.rows_grid;
   const int h = rest % a.kv_heads, slot = rest / a.kv_heads;
-  const int per = l.plan[0], all = l.plan[1];
   Tile t;
-  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, j) <= slot; });
-  if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, s), t)) return;
+  const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, l, j) <= slot; });
+  if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, l, s), t)) return;
+  const int per = scalar_load(l.plan), all = scalar_load(l.plan + 1);
   int p0, count;
   if (STREAM) {
     int block0;
     sequence_tiles<BM, KB>(a, l, s, block0, count);
-    p0 = l.plan[2 + s] + (slot - first_slot<BM>(a, s)) * count;
+    p0 = scalar_load(l.plan + 2 + s) + (slot - first_slot<BM>(a, l, s)) * count;
   } else {
-    p0 = l.plan[2 + slot];
-    count = l.plan[3 + slot] - p0;
+    p0 = scalar_load(l.plan + 2 + slot);
+    count = scalar_load(l.plan + 3 + slot) - p0;
   }
   if (count <= 0) return;
   const int64_t u0 = (int64_t)h * all + p0, u1 = u0 + count;
   const int w0 = (int)(u0 / per), w1 = (int)((u1 - 1) / per);
   if (w0 == w1) return;
-  for (int row = row0; row < t.rows; row += l.rows_grid) {
-  __syncthreads();
-  auto index = [&](int w) { return (int64_t)(2 * w + (u0 < (int64_t)w * per ? 0 : 1)) * BM + row; };
-  float mm = kLowest;
-  for (int w = w0 + tid; w <= w1; w += kThreads) mm = __builtin_fmaxf(mm, l.ml[index(w)].x);
+  // the first part is its workgroup's last piece unless it starts with that share; all others begin theirs
+  const int64_t first = 2 * (int64_t)w0 + (u0 < (int64_t)w0 * per ? 0 : 1);
+  const int g = tid / LP, x = tid % LP, pg = g % PARTS;
+  for (int row0 = (blockIdx.x % l.rows_grid) * ROWS; row0 < t.rows; row0 += l.rows_grid * ROWS) {
+    const int row = row0 + g / PARTS;
+    const bool live = row < t.rows;
+    float m = kLowest, sum = 0.0f;
+    float4 acc = make_float4(0, 0, 0, 0);
+    if (live) {
+      for (int w = w0 + pg; w <= w1; w += 4 * PARTS) {
+        float2 ml[4];
+        float4 v[4];
 #pragma unroll
-  for (int x = 1; x < 64; x *= 2) mm = __builtin_fmaxf(mm, __shfl_xor(mm, x, 64));
-  if (lane == 0) red[wave] = mm;
-  __syncthreads();
-  mm = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
-  const int g = tid / LP, x = tid % LP;
-  float4 acc = make_float4(0, 0, 0, 0);
-  float ll = 0.0f;
-  for (int w = w0 + g; w <= w1; w += GR) {
-    const int64_t at = index(w);
-    const float2 ml = l.ml[at];
-    const float4 v = *reinterpret_cast<const float4*>(l.po + at * D + x * 4);
-    const float f = exp2_fast(ml.x - mm);
-    ll += ml.y * f;
-    acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
-  }
-  part[g][x] = acc;
-  if (x == 0) lsum[g] = ll;
-  __syncthreads();
-  if (g != 0) continue;
-  for (int i = 1; i < GR; ++i) {
-    const float4 v = part[i][x];
-    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-    ll += lsum[i];
-  }
-  const float vs = a.v_scale ? a.v_scale[h * a.scale_stride] : 1.0f;
-  const int r = t.row0 + row;
-  const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-  const float f = ll == 0.0f ? 0.0f : vs / ll;
-  *reinterpret_cast<uint2*>(a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + x * 4) =
-      make_uint2(bf16_pair(acc.x * f, acc.y * f), bf16_pair(acc.z * f, acc.w * f));
-  if (a.lse && x == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
+        for (int i = 0; i < 4; ++i) {
+          const int wi = w + i * PARTS;
+          const int64_t at = (wi == w0 ? first : 2 * (int64_t)(wi <= w1 ? wi : w1)) * BM + row;
+          ml[i] = l.ml[at];
+          v[i] = *reinterpret_cast<const float4*>(l.po + at * D + x * 4);
+          if (wi > w1) ml[i] = make_float2(kLowest, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (w + i * PARTS > w1) continue;
+          const float mx = __builtin_fmaxf(m, ml[i].x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml[i].x - mx);
+          m = mx;
+          sum = sum * f0 + ml[i].y * f1;
+          acc.x = acc.x * f0 + v[i].x * f1;
+          acc.y = acc.y * f0 + v[i].y * f1;
+          acc.z = acc.z * f0 + v[i].z * f1;
+          acc.w = acc.w * f0 + v[i].w * f1;
+        }
+      }
+    }
+    if (PARTS > 1) {
+      __syncthreads();
+      part[g][x] = acc;
+      if (x == 0) part_ml[g] = make_float2(m, sum);
+      __syncthreads();
+      if (pg != 0) continue;
+      for (int i = 1; i < PARTS; ++i) {
+        const float2 ml = part_ml[g + i];
+        const float4 v = part[g + i][x];
+        const float mx = __builtin_fmaxf(m, ml.x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml.x - mx);
+        m = mx;
+        sum = sum * f0 + ml.y * f1;
+        acc.x = acc.x * f0 + v.x * f1;
+        acc.y = acc.y * f0 + v.y * f1;
+        acc.z = acc.z * f0 + v.z * f1;
+        acc.w = acc.w * f0 + v.w * f1;
+      }
+    }
+    if (!live) continue;
+    const float vs = a.v_scale ? a.v_scale[h * a.scale_stride] : 1.0f;
+    const int r = t.row0 + row;
+    const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
+    const float f = sum == 0.0f ? 0.0f : vs / sum;
+    *reinterpret_cast<uint2*>(a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + x * 4) =
+        make_uint2(bf16_pair(acc.x * f, acc.y * f), bf16_pair(acc.z * f, acc.w * f));
+    if (a.lse && x == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (m + __builtin_log2f(sum)) * kLn2;
   }
 }
 
@@ -1225,7 +1250,7 @@ struct Choice {
   int64_t slots;
   bool split;
   int workgroups;
-  int rows_grid;             // workgroups per (slot, head) that join parts
+  int rows;                  // rows a tile holds, by the hint
 };
 
 struct Choices {
@@ -1249,12 +1274,12 @@ Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
   c.tile.used = rows > 32;
   c.stream.bm = 16 * rb;
   c.stream.rows_hi = c.tile.used ? c.stream.bm : INT32_MAX;
-  c.stream.slots = slots(c.stream.bm);
+  c.stream.slots = c.tile.used ? num_seqs : slots(c.stream.bm);
   c.stream.split = c.stream.slots <= kMaxSlots;
   c.stream.workgroups = dim == 256 ? 512 : 1024;
-  c.stream.rows_grid = (int)(rows < c.stream.bm ? rows : c.stream.bm);
+  c.stream.rows = (int)(rows < c.stream.bm ? rows : c.stream.bm);
   c.tile.bm = 128;
-  c.tile.rows_grid = c.tile.bm;
+  c.tile.rows = c.tile.bm;
   c.tile.rows_lo = c.stream.used ? c.stream.bm : 0;
   c.tile.rows_hi = INT32_MAX;
   c.tile.slots = slots(c.tile.bm);
@@ -1287,8 +1312,15 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
   kernel<<<(unsigned)grid, kThreads, 0, stream>>>(a, l);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   if (l.split) {
-    l.rows_grid = c.rows_grid;
-    combine_kernel<D, BM, KB, STREAM><<<(unsigned)(c.slots * a.kv_heads * c.rows_grid), kThreads, 0, stream>>>(a, l);
+    constexpr int kRows = kThreads / (D / 4);            // rows a workgroup holds at once, a part each
+    const int64_t segments = c.slots * a.kv_heads;
+    if (segments * c.rows < 1024) {
+      l.rows_grid = c.rows;
+      combine_kernel<D, BM, KB, STREAM, kRows><<<(unsigned)(segments * l.rows_grid), kThreads, 0, stream>>>(a, l);
+    } else {
+      l.rows_grid = (c.rows + kRows - 1) / kRows;
+      combine_kernel<D, BM, KB, STREAM, 1><<<(unsigned)(segments * l.rows_grid), kThreads, 0, stream>>>(a, l);
+    }
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   }
   return NVFP4_OK;
