@@ -32,7 +32,7 @@ struct RopeAppendArgs {
   const float *k_scale, *v_scale;
   const int32_t *cu_q, *kv_len;
   int32_t num_pages, page_shift, num_seqs, table_width, scale_stride, fp8;
-  int32_t groups;                // wavefront jobs per token
+  int32_t groups, jobs;          // groups of head vectors and wavefronts per token
 };
 
 int launch_rope_append(const RopeAppendArgs& a, int x_dtype, bool append, hipStream_t stream);

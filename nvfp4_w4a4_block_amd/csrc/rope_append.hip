@@ -9,10 +9,11 @@
 //
 // HBM-bound: every element is read once and written once.  A lane holds 8 consecutive channels (16 B
 // of bf16 in, 16 B of bf16 or 8 B of E4M3 out), a head vector is spread over D / 8 lanes (rounded up
-// to a power of two), so a wavefront takes 64 / lanes vectors of ONE token at a time: the token's
-// sequence, position, page and table row are wave-uniform and looked up once.  The partner channel of
-// the half-split rotation is R / 16 lanes away (one cross-lane read per channel); interleaved pairs
-// lie in the lane.  The sum of squares is a butterfly over the vector's lanes.
+// to a power of two).  A wavefront takes ONE token and up to U groups of 64 / lanes head vectors, each group of
+// queries, keys or values only: sequence, position, page, kind and their addresses are wave-uniform and
+// looked up once, all loads go out first, and a lane's angles serve every group (its channels are the same in
+// all).  The partner channel of the half-split rotation is R / 16 lanes away (one cross-lane read per
+// channel); interleaved pairs lie in the lane.  The sum of squares is a butterfly over the vector's lanes.
 #include "fp8_device.h"
 #include "paged_device.h"
 
@@ -35,152 +36,205 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&e)[8]) {
   return make_uint4(bf16_pair(e[0], e[1]), bf16_pair(e[2], e[3]), bf16_pair(e[4], e[5]), bf16_pair(e[6], e[7]));
 }
 
-__device__ __forceinline__ uint2 pack_fp8(const float (&e)[8], float s) {
+__device__ __forceinline__ uint2 pack_fp8(const float (&e)[8], const FastQuotient& f) {
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) nan |= e[i] != e[i];
-  if (fast_scale(s) && !nan) {
-    const FastQuotient f{s, 1.0f / s, 440.0f * s};
-    return make_uint2(fp8x4_fast(e, f), fp8x4_fast(e + 4, f));
-  }
-  return make_uint2(fp8x4_exact(e, s), fp8x4_exact(e + 4, s));
+  if (fast_scale(f.s) && !nan) return make_uint2(fp8x4_fast(e, f), fp8x4_fast(e + 4, f));
+  return make_uint2(fp8x4_exact(e, f.s), fp8x4_exact(e + 4, f.s));
 }
 
+// The operand of a kind, field by field: a reference into the kernel's arguments would put them in memory.
+__device__ __forceinline__ HeadsView pick(int kind, const HeadsView& q, const HeadsView& k, const HeadsView& v) {
+  return HeadsView{kind == 0 ? q.data : (kind == 1 ? k.data : v.data), kind == 0 ? q.tok : (kind == 1 ? k.tok : v.tok),
+                   kind == 0 ? q.head : (kind == 1 ? k.head : v.head), kind == 0 ? q.heads : (kind == 1 ? k.heads : v.heads)};
+}
 
-// LPR lanes per head vector (power of two), XT the input type, APPEND: keys and values go to the cache.
-template <typename XT, int LPR, bool APPEND>
+__device__ __forceinline__ FastQuotient quotient_of(float s) { return FastQuotient{s, 1.0f / s, 440.0f * s}; }
+
+// LPR lanes per head vector (power of two), U groups per wavefront, XT the input type, APPEND: keys and values go
+// to the cache.
+template <typename XT, int LPR, int U, bool APPEND>
 __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a) {
-  constexpr int RPW = 64 / LPR;                 // head vectors per wavefront
+  constexpr int RPW = 64 / LPR;                 // head vectors per group
   const int lane = threadIdx.x & 63;
   const int job = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
-  const int token = job / a.groups, group = job - token * a.groups;
+  const int token = job / a.jobs, group0 = (job - token * a.jobs) * U;
   if (token >= a.tokens) return;
-  const int li = lane & (LPR - 1);              // lane in its head vector
-  const int row = group * RPW + lane / LPR;     // q heads, then k heads, then v heads
-  const int d0 = li * 8;
-  const int kind = row < a.q.heads ? 0 : (row < a.q.heads + a.k.heads ? 1 : 2);
-  const int h = kind == 0 ? row : (kind == 1 ? row - a.q.heads : row - a.q.heads - a.k.heads);
-  const bool live = row < a.q.heads + a.k.heads + (APPEND ? a.v.heads : 0) && d0 < a.dim;
+  const int li = lane & (LPR - 1), d0 = li * 8; // lane in its head vector, its first channel
+  const int gq = (a.q.heads + RPW - 1) / RPW, gk = (a.k.heads + RPW - 1) / RPW;
 
-  // the vector's load goes out before the lookups below
-  float e[8];
+  // The sequence's search goes out ahead of the vectors' loads, which it would otherwise wait for (vector loads
+  // return in order); up to 63 sequences are one probe per lane.
+  const int32_t* cu = a.cu_q;
+  const bool one_probe = APPEND && a.num_seqs < 64;
+  int probe = 0;
+  if (one_probe) probe = cu[lane < a.num_seqs ? lane : a.num_seqs];
+  __builtin_amdgcn_sched_barrier(0);
+  float e[U][8];
+  int kind[U], head[U];                         // 0: query, 1: key, 2: value
+  bool live[U];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = 0.0f;
-  if (live) {
-    const HeadsView& x = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-    load8(static_cast<const XT*>(x.data) + token * x.tok + h * x.head + d0, e);
+  for (int u = 0; u < U; ++u) {
+    const int g = group0 + u;
+    kind[u] = g < gq ? 0 : (g < gq + gk ? 1 : 2);
+    const HeadsView x = pick(kind[u], a.q, a.k, a.v);
+    head[u] = (kind[u] == 0 ? g : (kind[u] == 1 ? g - gq : g - gq - gk)) * RPW + lane / LPR;
+    live[u] = g < a.groups && head[u] < x.heads && d0 < a.dim;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[u][i] = 0.0f;
+    if (live[u]) load8(static_cast<const XT*>(x.data) + token * x.tok + head[u] * x.head + d0, e[u]);
   }
 
   int64_t place = 0;                            // the token's place in its sequence
-  int seq = 0;
+  int64_t page_row = 0;                         // its row in a page
+  uint8_t *k_page = nullptr, *v_page = nullptr;
   if (APPEND) {
-    seq = wave_search(a.num_seqs + 1, [&](int j) { return a.cu_q[j] <= token; });
+    const int seq = one_probe
+        ? __builtin_popcountll(__builtin_amdgcn_ballot_w64(lane <= a.num_seqs && probe <= token)) - 1
+        : wave_search(a.num_seqs + 1, [=](int j) { return cu[j] <= token; });
     if (seq < 0 || seq >= a.num_seqs) return;   // the token belongs to nobody
-    place = (int64_t)a.kv_len[seq] - ((int64_t)a.cu_q[seq + 1] - token);
-  }
-
-  if (kind != 2) {
-    const float* w = kind == 0 ? a.q_weight : a.k_weight;
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += e[i] * e[i];
-#pragma unroll
-    for (int m = 1; m < LPR; m *= 2) sum += __shfl_xor(sum, m, 64);
-    if (w && live) {
-      const float r = 1.0f / __builtin_sqrtf(sum / (float)a.dim + a.eps);
-      float g[8];
-      load8(w + d0, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = e[i] * r * g[i];
+    place = (int64_t)scalar_load(a.kv_len + seq) - ((int64_t)scalar_load(a.cu_q + seq + 1) - token);
+    const int64_t block = place >> a.page_shift;
+    if (place >= 0 && block < a.table_width) {
+      const int page = scalar_load(a.page_table + seq * a.table_stride + block);
+      if (page >= 0 && page < a.num_pages) {
+        k_page = a.k_cache + page * a.k_page;
+        v_page = a.v_cache + page * a.v_page;
+        page_row = place & ((1 << a.page_shift) - 1);
+      }
     }
   }
-  if (a.table) {
-    const int64_t pos = a.positions ? a.positions[token] : place;
-    const bool known = pos >= 0 && pos < a.table_rows;
-    const float* t = a.table + (known ? pos : 0) * a.rot;
-    const int half = a.rot / 2;
-    const bool turns = d0 < a.rot && kind != 2;
-    const float nan = __builtin_nanf("");
+
+  const int half = a.rot / 2;
+  const int64_t pos = a.table && a.positions ? scalar_load(a.positions + token) : place;
+  const bool known = pos >= 0 && pos < a.table_rows;
+  const bool turns = a.table && d0 < a.rot, first = d0 < half;
+  float c[8], n[8];                             // interleaved: the first four
+  if (turns && known && kind[0] != 2) {         // groups are in the order of their kinds
+    const float* t = a.table + pos * a.rot;
     if (a.interleaved) {
-      if (turns && known) {
-        const float4 c = *reinterpret_cast<const float4*>(t + d0 / 2);
-        const float4 n = *reinterpret_cast<const float4*>(t + half + d0 / 2);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, nn[4] = {n.x, n.y, n.z, n.w};
+      const float4 x = *reinterpret_cast<const float4*>(t + d0 / 2), y = *reinterpret_cast<const float4*>(t + half + d0 / 2);
+      c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
+      n[0] = y.x; n[1] = y.y; n[2] = y.z; n[3] = y.w;
+    } else {
+      const int i0 = first ? d0 : d0 - half;
+      load8(t + i0, c);
+      load8(t + half + i0, n);
+      // the sine with the sign it takes in this half: x c + partner n
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = e[2 * i], y = e[2 * i + 1];
-          e[2 * i] = x * cc[i] - y * nn[i];
-          e[2 * i + 1] = y * cc[i] + x * nn[i];
+      for (int i = 0; i < 8; ++i) n[i] = first ? -n[i] : n[i];
+    }
+  }
+  float g[8];                                   // the weight of the current kind
+  int g_kind = -1;
+  FastQuotient f{0.0f, 0.0f, 0.0f};
+  int f_kind = -1;
+
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (group0 + u >= a.groups) break;
+    float(&v)[8] = e[u];
+    if (kind[u] != 2) {
+      const float* w = kind[u] == 0 ? a.q_weight : a.k_weight;
+      if (w) {
+        if (g_kind != kind[u] && d0 < a.dim) load8(w + d0, g);
+        g_kind = kind[u];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += v[i] * v[i];
+#pragma unroll
+        for (int m = 1; m < LPR; m *= 2) sum += __shfl_xor(sum, m, 64);
+        if (live[u]) {
+          const float r = 1.0f / __builtin_sqrtf(sum / (float)a.dim + a.eps);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = v[i] * r * g[i];
         }
       }
-    } else {
-      // every lane takes part in the cross-lane reads
-      const int step = half / 8;
-      const bool first = d0 < half;
-      const int partner = lane + (first ? step : -step);
-      float o[8];
+      if (a.table) {
+        if (a.interleaved) {
+          if (turns && known) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __shfl(e[i], partner & 63, 64);
-      if (turns && known) {
-        const int i0 = first ? d0 : d0 - half;
-        float c[8], n[8];
-        load8(t + i0, c);
-        load8(t + half + i0, n);
+            for (int i = 0; i < 4; ++i) {
+              const float x = v[2 * i], y = v[2 * i + 1];
+              v[2 * i] = x * c[i] - y * n[i];
+              v[2 * i + 1] = y * c[i] + x * n[i];
+            }
+          }
+        } else {
+          const int partner = lane + (first ? half / 8 : -(half / 8));
+          float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = first ? e[i] * c[i] - o[i] * n[i] : e[i] * c[i] + o[i] * n[i];
+          for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], partner & 63, 64);     // every lane takes part
+          if (turns && known) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * c[i] + o[i] * n[i];
+          }
+        }
+        if (turns && !known) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __builtin_nanf("");
+        }
       }
     }
-    if (turns && !known)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = nan;
-  }
-  if (!live) return;
-
-  if (kind == 0 || !APPEND) {
-    const HeadsView& o = kind == 0 ? a.q_out : a.k_out;
-    const int64_t at = token * o.tok + h * o.head + d0;
-    if (a.out_bf16) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.data) + at) = pack_bf16(e);
+    if (kind[u] == 0 || !APPEND) {
+      if (!live[u]) continue;
+      const HeadsView o = pick(kind[u], a.q_out, a.k_out, a.k_out);
+      const int64_t at = token * o.tok + head[u] * o.head + d0;
+      if (a.out_bf16) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.data) + at) = pack_bf16(v);
+      } else {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.data) + at);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
     } else {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.data) + at);
-      p[0] = make_float4(e[0], e[1], e[2], e[3]);
-      p[1] = make_float4(e[4], e[5], e[6], e[7]);
+      if (!k_page) return;                      // no page: keys and values are dropped
+      uint8_t* base = kind[u] == 1 ? k_page : v_page;
+      const int64_t at = (((int64_t)head[u] << a.page_shift) + page_row) * a.dim + d0;
+      if (a.fp8) {
+        // one scale per cache: its reciprocal serves every group of the kind
+        if (a.scale_stride != 0) {
+          if (live[u]) f = quotient_of((kind[u] == 1 ? a.k_scale : a.v_scale)[head[u]]);
+        } else if (f_kind != kind[u]) {
+          f = quotient_of(scalar_load(kind[u] == 1 ? a.k_scale : a.v_scale));
+          f_kind = kind[u];
+        }
+        if (live[u]) *reinterpret_cast<uint2*>(base + at) = pack_fp8(v, f);
+      } else if (live[u]) {
+        *reinterpret_cast<uint4*>(base + 2 * at) = pack_bf16(v);
+      }
     }
-    return;
-  }
-  const int64_t block = place >> a.page_shift;
-  if (place < 0 || block >= a.table_width) return;
-  const int page = a.page_table[seq * a.table_stride + block];
-  if (page < 0 || page >= a.num_pages) return;
-  const int64_t in_page =
-      (((int64_t)h << a.page_shift) + (place & ((1 << a.page_shift) - 1))) * a.dim + d0;
-  uint8_t* base = kind == 1 ? a.k_cache + page * a.k_page : a.v_cache + page * a.v_page;
-  if (a.fp8) {
-    const float s = (kind == 1 ? a.k_scale : a.v_scale)[h * a.scale_stride];
-    *reinterpret_cast<uint2*>(base + in_page) = pack_fp8(e, s);
-  } else {
-    *reinterpret_cast<uint4*>(base + 2 * in_page) = pack_bf16(e);
   }
 }
 
-template <typename XT, bool APPEND>
-int launch_lanes(RopeAppendArgs a, hipStream_t stream) {
-  int lanes = 2;
-  while (lanes * 8 < a.dim) lanes *= 2;
-  const int rows = a.q.heads + a.k.heads + (APPEND ? a.v.heads : 0);
-  a.groups = (rows + 64 / lanes - 1) / (64 / lanes);
-  const int64_t jobs = (int64_t)a.tokens * a.groups;
+template <typename XT, int LPR, bool APPEND>
+int launch_groups(RopeAppendArgs a, hipStream_t stream) {
+  constexpr int RPW = 64 / LPR;
+  auto groups = [](const HeadsView& x) { return (x.heads + RPW - 1) / RPW; };
+  a.groups = groups(a.q) + groups(a.k) + (APPEND ? groups(a.v) : 0);
+  // enough wavefronts to fill the GPU several times over: several groups each, else one for the shortest path
+  const bool many = (int64_t)a.tokens * a.groups >= 4 * 8192;
+  const int u = many ? 4 : 1;
+  a.jobs = (a.groups + u - 1) / u;
+  const int64_t jobs = (int64_t)a.tokens * a.jobs;
   if (jobs > INT32_MAX - 8) return NVFP4_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)((jobs + kThreads / 64 - 1) / (kThreads / 64));
-  switch (lanes) {
-    case 2: rope_append_kernel<XT, 2, APPEND><<<grid, kThreads, 0, stream>>>(a); break;
-    case 4: rope_append_kernel<XT, 4, APPEND><<<grid, kThreads, 0, stream>>>(a); break;
-    case 8: rope_append_kernel<XT, 8, APPEND><<<grid, kThreads, 0, stream>>>(a); break;
-    case 16: rope_append_kernel<XT, 16, APPEND><<<grid, kThreads, 0, stream>>>(a); break;
-    case 32: rope_append_kernel<XT, 32, APPEND><<<grid, kThreads, 0, stream>>>(a); break;
-    default: rope_append_kernel<XT, 64, APPEND><<<grid, kThreads, 0, stream>>>(a); break;
-  }
+  if (many)
+    rope_append_kernel<XT, LPR, 4, APPEND><<<grid, kThreads, 0, stream>>>(a);
+  else
+    rope_append_kernel<XT, LPR, 1, APPEND><<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+template <typename XT, bool APPEND>
+int launch_lanes(const RopeAppendArgs& a, hipStream_t stream) {
+  if (a.dim <= 16) return launch_groups<XT, 2, APPEND>(a, stream);
+  if (a.dim <= 32) return launch_groups<XT, 4, APPEND>(a, stream);
+  if (a.dim <= 64) return launch_groups<XT, 8, APPEND>(a, stream);
+  if (a.dim <= 128) return launch_groups<XT, 16, APPEND>(a, stream);
+  if (a.dim <= 256) return launch_groups<XT, 32, APPEND>(a, stream);
+  return launch_groups<XT, 64, APPEND>(a, stream);
 }
 
 }  // namespace
