@@ -22,6 +22,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kGroups = 2;
 
 __device__ __forceinline__ void load8(const uint16_t* x, float (&e)[8]) {
   widen(*reinterpret_cast<const uint4*>(x), e, x);
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
         g_kind = kind[u];
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += v[i] * v[i];
+        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[i], v[i], sum);
 #pragma unroll
         for (int m = 1; m < LPR; m *= 2) sum += __shfl_xor(sum, m, 64);
         if (live[u]) {
@@ -157,8 +158,8 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float x = v[2 * i], y = v[2 * i + 1];
-              v[2 * i] = x * c[i] - y * n[i];
-              v[2 * i + 1] = y * c[i] + x * n[i];
+              v[2 * i] = __builtin_fmaf(x, c[i], -(y * n[i]));
+              v[2 * i + 1] = __builtin_fmaf(y, c[i], x * n[i]);
             }
           }
         } else {
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
           for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], partner & 63, 64);     // every lane takes part
           if (turns && known) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = v[i] * c[i] + o[i] * n[i];
+            for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], c[i], o[i] * n[i]);
           }
         }
         if (turns && !known) {
@@ -215,13 +216,13 @@ int launch_groups(RopeAppendArgs a, hipStream_t stream) {
   a.groups = groups(a.q) + groups(a.k) + (APPEND ? groups(a.v) : 0);
   // enough wavefronts to fill the GPU several times over: several groups each, else one for the shortest path
   const bool many = (int64_t)a.tokens * a.groups >= 4 * 8192;
-  const int u = many ? 4 : 1;
+  const int u = many ? kGroups : 1;
   a.jobs = (a.groups + u - 1) / u;
   const int64_t jobs = (int64_t)a.tokens * a.jobs;
   if (jobs > INT32_MAX - 8) return NVFP4_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)((jobs + kThreads / 64 - 1) / (kThreads / 64));
   if (many)
-    rope_append_kernel<XT, LPR, 4, APPEND><<<grid, kThreads, 0, stream>>>(a);
+    rope_append_kernel<XT, LPR, kGroups, APPEND><<<grid, kThreads, 0, stream>>>(a);
   else
     rope_append_kernel<XT, LPR, 1, APPEND><<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
