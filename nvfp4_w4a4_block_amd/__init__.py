@@ -602,50 +602,65 @@ def _shape_text(*dims) -> str:
 def _heads_arg(t: torch.Tensor, name: str, dtypes: tuple, gpu: int, tokens: int | None = None,
                heads: int | None = None, dim: int | None = None) -> _Heads:
     """A [tokens, heads, dim] operand whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise ValueError(f"{name}: a tensor [tokens, heads, dim]")
-    n, h, d = t.shape
+    try:
+        n, h, d = t.shape
+        st, sh, sd = t.stride()
+        if ((n == tokens or tokens is None) and (d == dim or dim is None) and (h == heads or heads is None)
+                and (sd == 1 or n * h == 0) and t.dtype in dtypes and t.get_device() == gpu):
+            return _Heads(t.data_ptr(), h, st, sh)
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError(f"{name}: a tensor [tokens, heads, dim]") from None
     if (tokens is not None and n != tokens) or (heads is not None and h != heads) or (dim is not None and d != dim):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {_shape_text(tokens, heads, dim)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(x) for x in dtypes)}")
-    st, sh, sd = t.stride()
     if sd != 1 and n * h > 0:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.get_device() != gpu:
-        raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
-    return _Heads(t.data_ptr(), h, st, sh)
+    raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
 
 
 def _vector_arg(t: torch.Tensor, name: str, dtype: torch.dtype, counts: tuple, gpu: int) -> int:
     """A contiguous one-dimensional operand with one of the given element counts."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous():
+    try:
+        (n,) = t.shape
+        if n in counts and t.dtype is dtype and t.is_contiguous() and t.get_device() == gpu:
+            return t.data_ptr()
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError(f"{name}: contiguous {dtype}, one dimension") from None
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype}, one dimension")
-    if t.shape[0] not in counts:
-        raise ValueError(f"{name}: {t.shape[0]} elements, expected {' or '.join(map(str, counts))}")
-    if t.get_device() != gpu:
-        raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
-    return t.data_ptr()
+    if n not in counts:
+        raise ValueError(f"{name}: {n} elements, expected {' or '.join(map(str, counts))}")
+    raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
 
 
 def _cache_arg(kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, gpu: int) -> _PagedKV:
     if not isinstance(kv, PagedKV):
         raise ValueError("kv: a PagedKV")
     k, v, table = kv.k, kv.v, kv.page_table
-    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or k.dim() != 4 or k.shape != v.shape:
+    try:
+        pages, heads, page, dim = shape = k.shape
+        sk, sv = k.stride(), v.stride()
+        same = v.shape == shape
+    except (AttributeError, TypeError, ValueError):
+        same = False
+    if not same:
         raise ValueError("kv.k, kv.v: tensors [pages, kv_heads, page_size, head_dim] of one shape")
     dtype = k.dtype
     fp8 = dtype is torch.uint8
     if not (fp8 or dtype is torch.bfloat16) or v.dtype is not dtype:
         raise ValueError("kv.k, kv.v: both uint8 (E4M3 bytes) or both bfloat16")
-    pages, heads, page, dim = k.shape
-    sk, sv, inner = k.stride(), v.stride(), (page * dim, dim, 1)
+    inner = (page * dim, dim, 1)
     if pages > 0 and (sk[1:] != inner or sv[1:] != inner):
         raise ValueError("kv.k, kv.v: every page must be contiguous")
-    if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() != 2:
+    try:
+        seqs, width = table.shape
+        pitch, step = table.stride()
+        good = table.dtype is torch.int32
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
         raise ValueError("kv.page_table: int32 [sequences, width]")
-    seqs, width = table.shape
-    pitch, step = table.stride()
     if step != 1 and width > 1 and seqs > 0:
         raise ValueError("kv.page_table: rows must be contiguous")
     if k.get_device() != gpu or v.get_device() != gpu or table.get_device() != gpu:
@@ -664,6 +679,15 @@ def _cache_arg(kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, gpu: int) 
                     _E4M3 if fp8 else _BF16, heads, dim, page, seqs, width, count)
 
 
+def _out_heads(like: torch.Tensor, out: torch.Tensor | None, name: str, dtype: torch.dtype, gpu: int, tokens: int,
+               heads: int, dim: int) -> tuple[torch.Tensor, _Heads]:
+    """The given output, checked, or a new contiguous one."""
+    if out is not None:
+        return out, _heads_arg(out, name, (dtype,), gpu, tokens, heads, dim)
+    out = like.new_empty((tokens, heads, dim), dtype=dtype)
+    return out, _Heads(out.data_ptr(), heads, heads * dim, dim)
+
+
 def _weight_arg(w: torch.Tensor | None, name: str, dim: int, gpu: int) -> int | None:
     return None if w is None else _vector_arg(w, name, torch.float32, (dim,), gpu)
 
@@ -672,13 +696,25 @@ def _rope_arg(rope: torch.Tensor | None, positions: torch.Tensor | None, tokens:
     if rope is None:
         _require(positions is None, "positions without a rope table")
         return None
-    if not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.dtype is not torch.float32 or not rope.is_contiguous():
+    try:
+        rows, dim = rope.shape
+        good = rope.dtype is torch.float32 and rope.is_contiguous()
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
         raise ValueError("rope: contiguous float32 [positions, rotated channels], cos then sin")
     if rope.get_device() != gpu:
         raise ValueError("rope: on another device than the tokens")
-    rows, dim = rope.shape
     pos = None if positions is None else _vector_arg(positions, "positions", torch.int32, (tokens,), gpu)
     return _Rope(rope.data_ptr(), rows, pos, dim, 1 if interleaved else 0)
+
+
+def _raw_stream(gpu: int) -> int:
+    return torch.cuda.current_stream(gpu).cuda_stream
+
+
+# The same handle without building a Stream object around it, where this torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _run(gpu: int, what: str, fn, *args) -> None:
@@ -687,10 +723,10 @@ def _run(gpu: int, what: str, fn, *args) -> None:
     if gpu < 0:
         raise ValueError("tensors must be on a GPU, not the CPU")
     if torch.cuda.current_device() == gpu:
-        st = fn(*args, torch.cuda.current_stream(gpu).cuda_stream)
+        st = fn(*args, _raw_stream(gpu))
     else:
         with torch.cuda.device(gpu):
-            st = fn(*args, torch.cuda.current_stream(gpu).cuda_stream)
+            st = fn(*args, _raw_stream(gpu))
     if st != 0:
         raise NVFP4Error(st, what)
 
@@ -717,13 +753,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, q_weight: torch
     ra = _rope_arg(rope, positions, T, interleaved, gpu)
     qw, kw = _weight_arg(q_weight, "q_weight", D, gpu), _weight_arg(k_weight, "k_weight", D, gpu)
     od = _y_dtype(out_dtype)
-    q_out = q.new_empty((T, Hq, D), dtype=out_dtype) if q_out is None else q_out
-    qo = _heads_arg(q_out, "q_out", (out_dtype,), gpu, T, Hq, D)
+    q_out, qo = _out_heads(q, q_out, "q_out", out_dtype, gpu, T, Hq, D)
     ka = ko = None
     if k is not None:
         ka = _heads_arg(k, "k", (dtype,), gpu, T, None, D)
-        k_out = k.new_empty((T, ka.heads, D), dtype=out_dtype) if k_out is None else k_out
-        ko = _heads_arg(k_out, "k_out", (out_dtype,), gpu, T, ka.heads, D)
+        k_out, ko = _out_heads(k, k_out, "k_out", out_dtype, gpu, T, ka.heads, D)
     else:
         _require(k_weight is None and k_out is None, "k_weight or k_out without k")
     _run(gpu, "nvfp4_qk_norm_rope", lib.nvfp4_qk_norm_rope, T, D, _BF16 if dtype is torch.bfloat16 else _F32, qa, ka, qw,
@@ -754,8 +788,8 @@ def kv_append(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tenso
     qdt = _BF16
     if q is not None:
         qa = _heads_arg(q, "q", (dtype,), gpu, T, None, D)
-        q_out = q.new_empty((T, qa.heads, D), dtype=torch.bfloat16) if q_out is None else q_out
-        qo = _heads_arg(q_out, "q_out", _X_DTYPES, gpu, T, qa.heads, D)
+        q_out, qo = _out_heads(q, q_out, "q_out", torch.bfloat16 if q_out is None else q_out.dtype, gpu, T, qa.heads, D)
+        _require(q_out.dtype in _X_DTYPES, "q_out: bf16 or fp32")
         qdt = _BF16 if q_out.dtype is torch.bfloat16 else _F32
     else:
         _require(q_weight is None and q_out is None, "q_weight or q_out without q")
@@ -780,8 +814,7 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, kv_len: torch.Tensor, cu_q: to
     Hk = c.kv_heads
     qa = _heads_arg(q, "q", _BF16_ONLY, gpu, T, Hq, c.head_dim)
     _require(Hk > 0 and Hq % Hk == 0, "q heads must be a multiple of the cache's")
-    out = q.new_empty((T, Hq, D)) if out is None else out
-    oa = _heads_arg(out, "out", _BF16_ONLY, gpu, T, Hq, D)
+    out, oa = _out_heads(q, out, "out", torch.bfloat16, gpu, T, Hq, D)
     lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
     need = lib.nvfp4_paged_attention_workspace_size(T, max_q, c.num_seqs, Hq, Hk, D, c.dtype)
     have = need
