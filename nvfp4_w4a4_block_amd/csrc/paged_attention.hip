@@ -46,7 +46,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxSlots = 1024;       // row tiles a split launch can plan
 constexpr int kStreamBlock = 128;     // keys per step of stream_kernel: 32 per wavefront
-constexpr int kTileBlock = 64;        // keys per step of tile_kernel
+// Keys per step of tile_kernel: 32 where the output and the queries leave few registers.
+constexpr int tile_block(int d) { return d > 128 ? 32 : 64; }
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945f;
@@ -778,25 +779,31 @@ __device__ __forceinline__ void step() { __builtin_amdgcn_sched_barrier(0); }
 //            chunks permuted within a row so that neighbouring rows fall on different banks.  The
 //            keys of a V^T row are stored in the order the score registers hold them: chunk
 //            2*(key/16) + half holds keys 4*half + {0..3} and 8 + 4*half + {0..3} of its 16.
+template <int I>
+struct Buffer {
+  static constexpr int value = I;
+};
+
 template <int D, bool FP8, int RW>
 __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_kernel(AttentionArgs a, Launch l) {
   constexpr int E = FP8 ? 1 : 2;
-  constexpr int BM = 128 * RW, KB = kTileBlock;
+  constexpr int BM = 128 * RW, KB = tile_block(D);
   // With one wavefront per SIMD half of its 512 registers are accumulation registers, which only matrix
   // instructions and loads address: the output and the queries are kept there.
   constexpr bool kAcc = RW * D > 128;
   constexpr int ST = D / 16;                // matrix steps of a score
   constexpr int DB = D / 32;                // output tiles
   constexpr int CH = D * E / 16;            // 16-byte chunks of a cached key
-  constexpr int KL = 16 * CH / 64;          // key loads per lane: 16 keys a wavefront
+  constexpr int KW = KB / 4, NG = KB / 16;  // keys a wavefront brings in, 16-key groups of a block
+  constexpr int KL = KW * CH / 64;          // key loads per lane
   constexpr int VQ = D / 4;                 // channel quads
-  constexpr int VI = 2 * VQ > 64 ? 2 * VQ / 64 : 1;        // value items per lane: 8 keys x 4 channels
+  constexpr int VI = KW * VQ > 512 ? KW * VQ / 512 : 1;    // value items per lane: 8 keys x 4 channels
   __shared__ __align__(16) uint16_t ks[2][KB * D];
   __shared__ __align__(16) uint16_t vt[2][D * KB];
   __shared__ int pre[kMaxSlots + 1];
   __shared__ int wave_sum[4];
   __shared__ int bad_block[2];              // block whose values hold something non-finite
-  __shared__ int no_page[2][4];             // per 16 keys of a block
+  __shared__ int no_page[2][NG];            // per 16 keys of a block
   constexpr int MW = D / 64;                // dwords of marks: a bit per output of a lane
   __shared__ uint32_t marks[RW * 2 * MW][kThreads];
 
@@ -809,12 +816,13 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     return key * D + ((ch ^ sw) & (N - 1)) * 8;
   };
   auto v_chunk = [](int d, int ch) {         // LDS offset of 8 keys of a channel
-    const int sw = ((d >> 1) & 7) ^ ((d >> 4) & 1);
-    return d * KB + ((ch ^ sw) & 7) * 8;
+    const int sw = KB == 64 ? ((d >> 1) & 7) ^ ((d >> 4) & 1) : (d >> 2) & 3;
+    return d * KB + ((ch ^ sw) & (KB / 8 - 1)) * 8;
   };
 
   const int v_quad = lane % VQ;
-  auto v_grp = [&](int i) { return VI > 1 ? i : (lane / VQ) & 1; };    // which 8 of the wavefront's 16 keys
+  // which 8 of its 16-key group a value item holds
+  auto v_grp = [&](int i) { return KW == 8 ? wave & 1 : (VI > 1 ? i : (lane / VQ) & 1); };
 
   tile_pieces<BM, KB>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
     const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
@@ -873,43 +881,38 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 
     const int64_t head_at = ((int64_t)h << a.page_shift) * (D * E);
     const int mask = (1 << a.page_shift) - 1;
-    uint4 kr[KL];
+    u32x4_t kr[KL];
     uint32_t vr[VI][8][E];                   // 4 channels of 8 keys
-    // Wavefront w brings in keys 16 w .. 16 w + 15 of a block, which lie in one page.
-    auto my_page = [&](int b) { return b < b1 ? page_of(a, t, (t.block0 + b) * KB + wave * 16) : -1; };
+    // Wavefront w brings in KW keys of a block, those of one 16-key group (or half of it) and so of one page: rows
+    // KW w .. of K, and of V the one or two sets of 8 keys that a 16-byte chunk of a V^T row holds.
+    const int my_group = wave * KW / 16;
+    auto my_page = [&](int b) { return b < b1 ? page_of(a, t, (t.block0 + b) * KB + my_group * 16) : -1; };
     auto fetch = [&](int b, int p) {
-      const int in = ((t.block0 + b) * KB + wave * 16) & mask;
-      const uint8_t* kp = a.k + (p >= 0 ? p : 0) * a.k_page + head_at + in * (D * E);
+      const int in = ((t.block0 + b) * KB + my_group * 16) & mask;
+      const uint8_t* kp = a.k + (p >= 0 ? p : 0) * a.k_page + head_at + (in + (wave * KW & 15)) * (D * E);
       const uint8_t* vp = a.v + (p >= 0 ? p : 0) * a.v_page + head_at + in * (D * E);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) kr[i] = *reinterpret_cast<const uint4*>(kp + (i * 64 + lane) * 16);
+      for (int i = 0; i < KL; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(kp + (i * 64 + lane) * 16);
 #pragma unroll
-      for (int i = 0; i < VI; ++i) {
-        if (VQ < 32 && lane >= 2 * VQ) continue;
+      for (int i = 0; i < VI; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           load_words<E>(vp + ((j & 3) + (j >> 2) * 8 + v_grp(i) * 4) * (D * E) + v_quad * (4 * E), vr[i][j]);
-      }
     };
-    // registers to LDS buffer `buf`
-    auto store = [&](int b, int p, int buf) {
-      const int key0 = (t.block0 + b) * KB + wave * 16;
-      if (lane == 0) no_page[buf][wave] = p < 0;
-#pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const int at = i * 64 + lane, key = wave * 16 + at / CH, ch = at % CH;
-        const uint4 w = kr[i];
-        if (FP8) {
-          *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch)]) =
-              u32x4_t{fp8_bf16(w.x, false), fp8_bf16(w.x, true), fp8_bf16(w.y, false), fp8_bf16(w.y, true)};
-          *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch + 1)]) =
-              u32x4_t{fp8_bf16(w.z, false), fp8_bf16(w.z, true), fp8_bf16(w.w, false), fp8_bf16(w.w, true)};
-        } else {
-          *reinterpret_cast<uint4*>(&ks[buf][k_chunk(key, ch)]) = w;
-        }
-      }
-      if (VQ < 32 && lane >= 2 * VQ) return;
-      if (p < 0 || key0 + 16 > t.len) {      // keys that do not exist: zero their values
+    // From registers to LDS, in NU small units that the score product takes in between its matrix instructions:
+    // keys (one converted 16-byte chunk each), values (a few byte moves, or one channel's 8 keys), and the search
+    // for non-finite values.  A tail or a missing page is zeroed first, non-finite values are taken out and
+    // the values written again after: both are rare.
+    constexpr int NK = FP8 ? 2 * KL : KL, PER = FP8 ? 4 : 2, NV = VI * E * (FP8 ? 8 : 2), NB = VI * E * 2;
+    constexpr int NU = NK + NV + NB;
+    uint32_t tv[VI * E][8];
+    uint32_t bad = 0;
+    auto stage_begin = [&](int b, int p, int buf) {
+      const int key0 = (t.block0 + b) * KB + my_group * 16;
+      if (lane == 0) no_page[buf][my_group] = p < 0;
+      bad = 0;
+      if (p < 0 || key0 + 16 > t.len) {      // keys that do not exist
+        asm volatile("");
 #pragma unroll
         for (int i = 0; i < VI; ++i)
 #pragma unroll
@@ -918,44 +921,82 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
             for (int x = 0; x < E; ++x)
               vr[i][j][x] = p >= 0 && key0 + (j & 3) + (j >> 2) * 8 + v_grp(i) * 4 < t.len ? vr[i][j][x] : 0u;
       }
-      uint32_t bad = 0;
+    };
+    auto stage_unit = [&](int u, int buf) {
+      if (u < NK) {
+        const int i = FP8 ? u / 2 : u, at = i * 64 + lane, key = wave * KW + at / CH, ch = at % CH;
+        if (FP8) {
+          const uint32_t lo = kr[i][(u & 1) * 2], hi = kr[i][(u & 1) * 2 + 1];
+          *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch + (u & 1))]) =
+              u32x4_t{fp8_bf16(lo, false), fp8_bf16(lo, true), fp8_bf16(hi, false), fp8_bf16(hi, true)};
+        } else {
+          *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, ch)]) = kr[i];
+        }
+      } else if (u < NK + NB) {
+        const int v = (u - NK) / 2, h4 = (u - NK) & 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bad |= non_finite<FP8>(vr[v / E][h4 * 4 + j][v % E]);
+      } else {
+        const int v = (u - NK - NB) / (FP8 ? 8 : 2), s = (u - NK - NB) % (FP8 ? 8 : 2);
+        auto w = [&](int j) { return vr[v / E][j][v % E]; };
+        auto put = [&](int y, u32x4_t x) {
+          *reinterpret_cast<u32x4_t*>(&vt[buf][v_chunk(v_quad * 4 + (v % E) * PER + y, my_group * 2 + v_grp(v / E))]) = x;
+        };
+        if (FP8) {
+          uint32_t(&z)[8] = tv[v];
+          const int o = (s >> 1) * 4;         // keys 0..3 then 4..7
+          if (s < 4 && !(s & 1)) {
+            z[o] = __builtin_amdgcn_perm(w(o + 1), w(o), 0x05010400u);
+            z[o + 1] = __builtin_amdgcn_perm(w(o + 1), w(o), 0x07030602u);
+            z[o + 2] = __builtin_amdgcn_perm(w(o + 3), w(o + 2), 0x05010400u);
+            z[o + 3] = __builtin_amdgcn_perm(w(o + 3), w(o + 2), 0x07030602u);
+          } else if (s < 4) {
+            const uint32_t c0 = __builtin_amdgcn_perm(z[o + 2], z[o], 0x05040100u);
+            const uint32_t c1 = __builtin_amdgcn_perm(z[o + 2], z[o], 0x07060302u);
+            const uint32_t c2 = __builtin_amdgcn_perm(z[o + 3], z[o + 1], 0x05040100u);
+            const uint32_t c3 = __builtin_amdgcn_perm(z[o + 3], z[o + 1], 0x07060302u);
+            z[o] = c0; z[o + 1] = c1; z[o + 2] = c2; z[o + 3] = c3;
+          } else {
+            const int y = s - 4;
+            put(y, u32x4_t{fp8_f16(z[y], false), fp8_f16(z[y], true), fp8_f16(z[4 + y], false), fp8_f16(z[4 + y], true)});
+          }
+        } else {
+          const uint32_t sel = s ? 0x07060302u : 0x05040100u;
+          put(s, u32x4_t{__builtin_amdgcn_perm(w(1), w(0), sel), __builtin_amdgcn_perm(w(3), w(2), sel),
+                         __builtin_amdgcn_perm(w(5), w(4), sel), __builtin_amdgcn_perm(w(7), w(6), sel)});
+        }
+      }
+    };
+    auto stage_end = [&](int b, int buf) {
+      if (__builtin_amdgcn_ballot_w64(bad != 0) == 0) return;
+      bad_block[buf] = b;                    // every writer writes the same
 #pragma unroll
       for (int i = 0; i < VI; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int x = 0; x < E; ++x) bad |= non_finite<FP8>(vr[i][j][x]);
-      if (__builtin_amdgcn_ballot_w64(bad != 0) != 0) {
-        bad_block[buf] = b;                  // every writer writes the same
+          for (int x = 0; x < E; ++x) vr[i][j][x] = finite_part<FP8>(vr[i][j][x]);
 #pragma unroll
-        for (int i = 0; i < VI; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int x = 0; x < E; ++x) vr[i][j][x] = finite_part<FP8>(vr[i][j][x]);
-      }
-#pragma unroll
-      for (int i = 0; i < VI; ++i) {
-#pragma unroll
-        for (int x = 0; x < E; ++x) {
-          uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = vr[i][j][x];
-          constexpr int PER = FP8 ? 4 : 2;
-          u32x4_t va[PER];
-          if constexpr (FP8) transpose_fp8(w, va); else transpose_bf16(w, va);
-#pragma unroll
-          for (int y = 0; y < PER; ++y)
-            *reinterpret_cast<u32x4_t*>(&vt[buf][v_chunk(v_quad * 4 + x * PER + y, wave * 2 + v_grp(i))]) = va[y];
-        }
-      }
+      for (int u = NK + NB; u < NU; ++u) stage_unit(u, buf);
     };
 
     bool marked = false;
-    auto compute = [&](int b, int buf) {
+    // The scores of block b with block b + 1 (page p) staged on the way; after it the registers take block b + 2.
+    auto compute = [&](int b, int p, int p2, auto static_buf) {
+      constexpr int buf = decltype(static_buf)::value;
       const int key0 = (t.block0 + b) * KB;
-      if (!busy || key0 >= hi_max || key0 + KB <= lo_min) return;
-      const int gone = uniform(no_page[buf][0] | no_page[buf][1] << 1 | no_page[buf][2] << 2 | no_page[buf][3] << 3);
+      stage_begin(b + 1, p, buf ^ 1);
+      if (!busy || key0 >= hi_max || key0 + KB <= lo_min) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) stage_unit(u, buf ^ 1);
+        stage_end(b + 1, buf ^ 1);
+        if (b + 2 < b1) fetch(b + 2, p2);
+        return;
+      }
+      int gone = 0;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) gone |= no_page[buf][g] << g;
+      gone = uniform(gone);
       const bool partial_keys = gone != 0 || key0 + KB > hi_min || key0 < lo_max;
       if (uniform(bad_block[buf]) == b) {
         // Rare: mark this lane's outputs that see a non-finite value, by reading the block's values again.
@@ -964,9 +1005,9 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
         marked = true;
 #pragma unroll 1
         for (int kk = 0; kk < KB; ++kk) {
-          const int key = key0 + kk, p = page_of(a, t, key);
-          if (p < 0) continue;
-          const uint8_t* vp = a.v + p * a.v_page + head_at + (key & mask) * (D * E) + half * (4 * E);
+          const int key = key0 + kk, pk = page_of(a, t, key);
+          if (pk < 0) continue;
+          const uint8_t* vp = a.v + pk * a.v_page + head_at + (key & mask) * (D * E) + half * (4 * E);
           uint32_t seen = 0;
 #pragma unroll
           for (int rw = 0; rw < RW; ++rw) seen |= (key >= lo[rw] && key < hi[rw] ? 1u : 0u) << rw;
@@ -984,9 +1025,9 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           }
         }
       }
-      f32x16_t s[RW][2];
+      f32x16_t s[RW][KB / 32];
       {
-        constexpr int AHEAD = 4;
+        constexpr int AHEAD = 4, NS = KB / 32 * ST;
         u32x4_t f[AHEAD];
         auto read = [&](int x) {
           return *reinterpret_cast<const u32x4_t*>(&ks[buf][k_chunk((x / ST) * 32 + n, (x % ST) * 2 + half)]);
@@ -995,7 +1036,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
         for (int x = 0; x < AHEAD; ++x) f[x] = read(x);
         step();
 #pragma unroll
-        for (int x = 0; x < 2 * ST; ++x) {
+        for (int x = 0; x < NS; ++x) {
           const u32x4_t ka = f[x % AHEAD];
 #pragma unroll
           for (int rw = 0; rw < RW; ++rw) {
@@ -1004,18 +1045,22 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
             for (int y = 0; y < 16; ++y) z[y] = 0.0f;
             s[rw][x / ST] = mfma32_bf16(ka, q[rw][x % ST], x % ST == 0 ? z : s[rw][x / ST]);
           }
-          if (x + AHEAD < 2 * ST) f[x % AHEAD] = read(x + AHEAD);
+          if (x + AHEAD < NS) f[x % AHEAD] = read(x + AHEAD);
+#pragma unroll
+          for (int u = x * NU / NS; u < (x + 1) * NU / NS; ++u) stage_unit(u, buf ^ 1);
           step();
         }
       }
-      u32x4_t pr[RW][4] = {};
+      stage_end(b + 1, buf ^ 1);
+      if (b + 2 < b1) fetch(b + 2, p2);
+      u32x4_t pr[RW][NG] = {};
       float mc[RW];
 #pragma unroll
       for (int rw = 0; rw < RW; ++rw) {
         if (partial_keys) {
           asm volatile("");        // a branch, not selects paid by every block
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
+          for (int kb = 0; kb < KB / 32; ++kb)
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               const int key = key0 + kb * 32 + 8 * (x >> 2) + 4 * half + (x & 3);
@@ -1025,7 +1070,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
         }
         float mx = m[rw];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB / 32; ++kb)
 #pragma unroll
           for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[rw][kb][x]);
         mx = max_across_32(mx);
@@ -1033,8 +1078,13 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           const float f0 = exp2_fast((m[rw] - mx) * c);
           m[rw] = mx;
           sum[rw] *= f0;
+          // (kAcc: taken out of the accumulation registers here and not ahead of the branch)
 #pragma unroll
-          for (int i = 0; i < DB; ++i) o[rw][i] *= f0;
+          for (int i = 0; i < DB; ++i) {
+            if constexpr (kAcc) asm volatile("" : "+a"(o[rw][i]));
+            o[rw][i] *= f0;
+            if constexpr (kAcc) asm volatile("" : "+a"(o[rw][i]));
+          }
         }
         mc[rw] = m[rw] == kLowest ? 0.0f : m[rw] * c;
       }
@@ -1060,13 +1110,13 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
         for (int j = 0; j < 8; ++j) exps(0, j);
         step();
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < NG; ++g) {
 #pragma unroll
           for (int i = 0; i < DB; ++i) {
             const u32x4_t va = f[i];
 #pragma unroll
             for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
-            if (g < 3) {
+            if (g + 1 < NG) {
               f[i] = read(g + 1, i);
 #pragma unroll
               for (int j = i * 8 / DB; j < (i + 1) * 8 / DB; ++j) exps(g + 1, j);
@@ -1085,20 +1135,24 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 
     __syncthreads();                          // the last piece's readers are done
     if (tid < 2) bad_block[tid] = -1;
-    int p = my_page(b0), pn = my_page(b0 + 1);     // page numbers come a block ahead of their loads
-    fetch(b0, p);
+    int p0 = my_page(b0), p1 = my_page(b0 + 1);    // page numbers come a block ahead of their loads
+    fetch(b0, p0);
     __syncthreads();
-    store(b0, p, 0);
+    stage_begin(b0, p0, 0);
+#pragma unroll
+    for (int u = 0; u < NU; ++u) stage_unit(u, 0);
+    stage_end(b0, 0);
+    if (b0 + 1 < b1) fetch(b0 + 1, p1);
     __syncthreads();
     for (int b = b0; b < b1; ++b) {
-      const int buf = (b - b0) & 1;
-      p = pn;
-      if (b + 1 < b1) {
-        fetch(b + 1, p);
-        pn = my_page(b + 2);
-      }
-      compute(b, buf);
-      if (b + 1 < b1) store(b + 1, p, buf ^ 1);
+      const int p2 = my_page(b + 2);
+      compute(b, p1, p2, Buffer<0>{});
+      p1 = p2;
+      __syncthreads();
+      if (++b == b1) break;
+      const int p3 = my_page(b + 2);
+      compute(b, p1, p3, Buffer<1>{});
+      p1 = p3;
       __syncthreads();
     }
 
@@ -1334,7 +1388,7 @@ int launch_dim(const AttentionArgs& a, const Choices& c, void* workspace, hipStr
         : launch_one<D, 32, kStreamBlock, true>(stream_kernel<D, FP8, 2>, a, c.stream, 2, workspace, stream);
     if (st != NVFP4_OK) return st;
   }
-  if (c.tile.used) return launch_one<D, 128, kTileBlock, false>(tile_kernel<D, FP8, 1>, a, c.tile, 4, workspace, stream);
+  if (c.tile.used) return launch_one<D, 128, tile_block(D), false>(tile_kernel<D, FP8, 1>, a, c.tile, 256 / tile_block(D), workspace, stream);
   return NVFP4_OK;
 }
 
