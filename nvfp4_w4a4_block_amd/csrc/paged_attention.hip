@@ -47,7 +47,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxSlots = 1024;       // row tiles a split launch can plan
 constexpr int kStreamBlock = 128;     // keys per step of stream_kernel: 32 per wavefront
 // Keys per step of tile_kernel: 32 where the output and the queries leave few registers.
-constexpr int tile_block(int d) { return d > 128 ? 32 : 64; }
+constexpr int tile_block(int d) { return 64; }
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945f;
