@@ -1034,6 +1034,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
         };
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x) f[x] = read(x);
+        __builtin_amdgcn_s_setprio(1);        // the wavefront at its matrix instructions goes first (+1.3 %)
         step();
 #pragma unroll
         for (int x = 0; x < NS; ++x) {
@@ -1051,6 +1052,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           step();
         }
       }
+      __builtin_amdgcn_s_setprio(0);
       stage_end(b + 1, buf ^ 1);
       if (b + 2 < b1) fetch(b + 2, p2);
       u32x4_t pr[RW][NG] = {};
