@@ -386,7 +386,7 @@ int nvfp4_fp8_kv_dequantize(const uint8_t* q, int64_t n, const float* scale, voi
 /* Head vectors x[t, h, 0 .. dim-1]: rows of `dim` contiguous elements at t * token_stride + h *
  * head_stride (elements), so that q, k and v may be column ranges of one fused projection.
  * data 16-byte aligned; both strides (of a dimension longer than one) times the element size a
- * multiple of 16 bytes. */
+ * multiple of 16 bytes, head_stride >= dim, token_stride >= 0; an output's rows must not overlap. */
 typedef struct {
   void* data;
   int64_t heads;

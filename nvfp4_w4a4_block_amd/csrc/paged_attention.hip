@@ -1235,8 +1235,8 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
   const int64_t u0 = (int64_t)h * all + p0, u1 = u0 + count;
   const int w0 = (int)(u0 / per), w1 = (int)((u1 - 1) / per);
   if (w0 == w1) return;
-  // the first part is its workgroup's last piece unless it starts with that share; all others begin theirs
-  const int64_t first = 2 * (int64_t)w0 + (u0 < (int64_t)w0 * per ? 0 : 1);
+  // the first part is the one its workgroup ended with (the odd slot), the others are the ones theirs began with
+  const int64_t first = 2 * (int64_t)w0 + 1;
   const int g = tid / LP, x = tid % LP, pg = g % PARTS;
   for (int row0 = (blockIdx.x % l.rows_grid) * ROWS; row0 < t.rows; row0 += l.rows_grid * ROWS) {
     const int row = row0 + g / PARTS;
@@ -1364,7 +1364,9 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
     l.ml = reinterpret_cast<float2*>(p + align16((size_t)(c.slots + 3) * 4));
     l.po = reinterpret_cast<float*>(l.ml + (size_t)2 * c.workgroups * BM);
   }
-  if (grid > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  if (grid * kThreads > (int64_t)UINT32_MAX ||
+      (l.split && c.slots * a.kv_heads * c.rows * kThreads > (int64_t)UINT32_MAX))
+    return NVFP4_ERR_UNSUPPORTED;
   kernel<<<(unsigned)grid, kThreads, 0, stream>>>(a, l);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   if (l.split) {

@@ -219,7 +219,7 @@ int launch_groups(RopeAppendArgs a, hipStream_t stream) {
   const int u = many ? kGroups : 1;
   a.jobs = (a.groups + u - 1) / u;
   const int64_t jobs = (int64_t)a.tokens * a.jobs;
-  if (jobs > INT32_MAX - 8) return NVFP4_ERR_UNSUPPORTED;
+  if (jobs * 64 + kThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;      // threads of a launch
   const unsigned grid = (unsigned)((jobs + kThreads / 64 - 1) / (kThreads / 64));
   if (many)
     rope_append_kernel<XT, LPR, kGroups, APPEND><<<grid, kThreads, 0, stream>>>(a);
