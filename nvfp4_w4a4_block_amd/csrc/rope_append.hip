@@ -33,6 +33,25 @@ __device__ __forceinline__ void load8(const float* x, float (&e)[8]) {
   e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
 }
 
+// 8 channels as they lie in memory, widened only when their group's turn comes: half the registers for bf16.
+template <typename XT>
+struct Raw {
+  uint4 w[sizeof(XT) / 2];
+};
+
+template <typename XT>
+__device__ __forceinline__ void load_raw(const XT* x, Raw<XT>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(XT) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(x)[i];
+}
+
+template <typename XT>
+__device__ __forceinline__ void widen_raw(const Raw<XT>& r, float (&e)[8]) {
+  constexpr int N = sizeof(XT) / 2;
+#pragma unroll
+  for (int i = 0; i < N; ++i) widen(r.w[i], e + i * (8 / N), static_cast<const XT*>(nullptr));
+}
+
 __device__ __forceinline__ uint4 pack_bf16(const float (&e)[8]) {
   return make_uint4(bf16_pair(e[0], e[1]), bf16_pair(e[2], e[3]), bf16_pair(e[4], e[5]), bf16_pair(e[6], e[7]));
 }
@@ -72,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
   int probe = 0;
   if (one_probe) probe = cu[lane < a.num_seqs ? lane : a.num_seqs];
   __builtin_amdgcn_sched_barrier(0);
-  float e[U][8];
+  Raw<XT> raw[U];
   int kind[U], head[U];                         // 0: query, 1: key, 2: value
   bool live[U];
 #pragma unroll
@@ -82,9 +101,8 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
     const HeadsView x = pick(kind[u], a.q, a.k, a.v);
     head[u] = (kind[u] == 0 ? g : (kind[u] == 1 ? g - gq : g - gq - gk)) * RPW + lane / LPR;
     live[u] = g < a.groups && head[u] < x.heads && d0 < a.dim;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[u][i] = 0.0f;
-    if (live[u]) load8(static_cast<const XT*>(x.data) + token * x.tok + head[u] * x.head + d0, e[u]);
+    raw[u] = Raw<XT>{};
+    if (live[u]) load_raw(static_cast<const XT*>(x.data) + token * x.tok + head[u] * x.head + d0, raw[u]);
   }
 
   int64_t place = 0;                            // the token's place in its sequence
@@ -135,7 +153,8 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (group0 + u >= a.groups) break;
-    float(&v)[8] = e[u];
+    float v[8];
+    widen_raw(raw[u], v);
     if (kind[u] != 2) {
       const float* w = kind[u] == 0 ? a.q_weight : a.k_weight;
       if (w) {
