@@ -31,7 +31,8 @@
 // Split of the key axis: with few row tiles, the key blocks of all (head, slot) segments form one
 // sequence that is cut into equal shares, one per workgroup, from the lengths as they are on the device.  A
 // segment inside one share is finished there; a cut one leaves (m, l, O) per share in the workspace,
-// joined by combine_kernel in a fixed order.
+// joined by combine_kernel in a fixed order.  Equal shares are what a batch of uneven lengths needs: 64 tokens
+// over caches of 512 to 32768 tokens (2.2 GB) take 406 us, 5.4 TB/s.
 //
 // Keys outside [0, kv_len) or on an invalid page are zeroed (V) and masked (scores); keys only some rows of
 // a tile see are masked by selection.  0 * inf would still reach rows that do not see the key, so
@@ -48,6 +49,11 @@ constexpr int kMaxSlots = 1024;       // row tiles a split launch can plan
 constexpr int kStreamBlock = 128;     // keys per step of stream_kernel: 32 per wavefront
 // Keys per step of tile_kernel: 32 where the output and the queries leave few registers.
 constexpr int tile_block(int d) { return 64; }
+// What cutting the key axis costs a tile_kernel launch, in key blocks: the extra prologues, the parts written and
+// joined take about 20 us, a block 0.8 to 2.6 us.  Tiles are kept whole where the longest workgroup's blocks are no
+// more than that above an even share: 1024 new tokens alone 45 us whole and 60 cut, over 32768 keys 970 whole
+// and 760 cut.
+constexpr int kCutCost = 16;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945f;
@@ -230,24 +236,39 @@ __device__ __forceinline__ void tile_pieces(const AttentionArgs& a, const Launch
   Tile t;
   int64_t u = 0, end = 1;
   int all = 0, w = 0, h = 0;
+  bool whole = false;
   if (l.split) {
     make_plan<BM, KB>(a, l, pre, wave_sum);
     all = uniform(pre[kMaxSlots]);
     const Shares sh = shares_of(a, l, all);
+    const int units = l.slots * a.kv_heads;
+    whole = (int64_t)((units + l.workgroups - 1) / l.workgroups) * all <= (int64_t)(kCutCost + sh.per) * l.slots;
     if (blockIdx.x == 0) {
       for (int j = threadIdx.x; j <= l.slots; j += kThreads) l.plan[2 + j] = pre[j];
       if (threadIdx.x == 0) {
-        l.plan[0] = sh.per;
+        l.plan[0] = whole ? INT32_MAX : sh.per;
         l.plan[1] = all;
       }
     }
-    w = my_share(sh);
-    u = (int64_t)w * sh.per;
-    end = u + sh.per < sh.total ? u + sh.per : sh.total;
+    if (whole) {
+      u = blockIdx.x;
+      end = u < units ? u + 1 : u;
+    } else {
+      w = my_share(sh);
+      u = (int64_t)w * sh.per;
+      end = u + sh.per < sh.total ? u + sh.per : sh.total;
+    }
   }
   while (u < end) {
     int off = 0, take, partial = -1;
-    if (l.split) {
+    if (whole) {
+      const int unit = (int)u, slot = l.slots - 1 - unit / a.kv_heads;
+      h = unit % a.kv_heads;
+      u = end;
+      const int s = wave_search(a.num_seqs, [&](int j) { return first_slot<BM>(a, l, j) <= slot; });
+      if (s < 0 || !tile_of<BM, KB>(a, l, s, slot - first_slot<BM>(a, l, s), t)) continue;
+      take = t.blocks;
+    } else if (l.split) {
       h = (int)(u / all);
       const int rem = (int)(u - (int64_t)h * all);
       int lo = 0, hi = l.slots;                   // pre[lo] <= rem < pre[hi]
@@ -482,6 +503,11 @@ constexpr int stream_waves(int d, bool fp8, int rb) {
   return regs <= 128 ? 4 : (regs <= 168 ? 3 : (regs <= 256 ? 2 : 1));
 }
 
+// HBM-bound: 2.2 GB of E4M3 cache in 375 us (5.8 TB/s, above what a copy reaches), 143 MB of bf16 cache in 30 us
+// (4.8 TB/s).  Registers, not LDS, hold the operands because no wavefront shares keys with another; one block of K
+// and one of V in flight per wavefront at three wavefronts per SIMD cover the latency (two blocks at two
+// wavefronts: 493 us).  Page numbers come through scalar loads: as vector loads they waited for the keys and values in
+// flight (480 us).
 // RB blocks of 16 rows; lane n = lane % 16 is the row, quarter = lane / 16.
 //   scores   S^T[g] (16 keys x 16 rows): lane holds keys g*16 + quarter*4 + i of its row
 //   K        A operand, lane = key, quarter = slice of the channels: 16 B loads, two matrix steps each
@@ -773,6 +799,14 @@ __device__ __forceinline__ void step() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---- many rows ---------------------------------------------------------------------------------------
 
+// MFMA-bound in principle, by the vector instructions beside it in fact: 8192 new tokens of 40 heads of 128 in 722 to
+// 770 us (890 to 950 TFLOP/s; a large bf16 library product reaches 1215 here).  Per wavefront and block 32 matrix instructions (32
+// cycles each) stand beside about 250 vector instructions, of which softmax's 32 scores a lane take 130 and the
+// staging of the next block 75.  A single wavefront issues a vector instruction every 8 cycles, two every 4 (measured),
+// so two wavefronts per SIMD are needed and everything that can goes between matrix instructions: staging into
+// the score product, exponentials into the second (837 -> 727 us for both).  64 rows a wavefront (RW = 2, half the
+// LDS reads, one wavefront per SIMD) is slower: 814 us; so is output through LDS in whole rows (no gain, more
+// registers).  Head dim 256 has registers for one wavefront per SIMD only: 1674 us, 821 TFLOP/s.
 // Four wavefronts of RW blocks of 32 rows each; lane % 32 is the row, half = lane / 32.
 //   scores   S^T (32 keys x 32 rows): register i of a lane is key 8*(i/4) + 4*half + i%4
 //   LDS      K as bf16 [key][D] and V^T as fp16 or bf16 [D][64 keys], both double-buffered, in 16-byte
@@ -1209,7 +1243,8 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 // A row's parts are read by `PARTS` groups of D / 4 lanes (4 channels each) and added in a fixed order; a workgroup
 // takes 256 / (D / 4) / PARTS rows at a time of one (slot, head), and rows_grid workgroups share its rows.  Few
 // row tiles are cut into many parts (PARTS as large as fits), many row tiles into few (PARTS = 1: no exchange).
-// STREAM: shares were planned per sequence, otherwise per slot.
+// STREAM: shares were planned per sequence, otherwise per slot.  A launch of its own (4 to 12 us): its reads wait for
+// every workgroup of the first anyway.
 template <int D, int BM, int KB, bool STREAM, int PARTS>
 __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Launch l) {
   constexpr int LP = D / 4, GR = kThreads / LP, ROWS = GR / PARTS;
@@ -1232,6 +1267,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
     count = scalar_load(l.plan + 3 + slot) - p0;
   }
   if (count <= 0) return;
+  if (per == INT32_MAX) return;              // tiles were kept whole
   const int64_t u0 = (int64_t)h * all + p0, u1 = u0 + count;
   const int w0 = (int)(u0 / per), w1 = (int)((u1 - 1) / per);
   if (w0 == w1) return;
@@ -1320,6 +1356,14 @@ size_t split_bytes(const Choice& c, int dim) {
   return align16((size_t)(c.slots + 3) * 4) + (size_t)2 * c.workgroups * c.bm * (8 + (size_t)dim * 4);
 }
 
+// Which kernel takes which sequences.  By the hint (or the call's tokens) a sequence has at most `rows` packed rows:
+//   up to 32      stream_kernel alone, 16 or 32 rows a tile (8 query heads a group, 4 tokens over 8192 keys: 17 us,
+//                 by tile_kernel 26; 16 sequences of 4 tokens, bf16: 47 and 59)
+//   more          tile_kernel, and beside it stream_kernel for the sequences that do have few rows; a single
+//                 sequence goes to tile_kernel alone
+// Both read the real lengths on the device, so a wrong hint costs time only.  The key axis may be cut where row
+// tiles are too few to fill the GPU twice (tile_kernel then decides on the device, kCutCost) or, for stream_kernel,
+// wherever the plan holds the sequences.
 Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads, int64_t kv_heads, int dim) {
   const int64_t group = q_heads / kv_heads;
   const int64_t rows = (max_q > 0 && max_q < tokens ? max_q : tokens) * group;
@@ -1340,7 +1384,7 @@ Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
   c.tile.rows_hi = INT32_MAX;
   c.tile.slots = slots(c.tile.bm);
   c.tile.workgroups = dim == 256 ? 256 : 512;
-  c.tile.split = c.tile.slots <= kMaxSlots && c.tile.slots * kv_heads < 4 * c.tile.workgroups;
+  c.tile.split = c.tile.slots <= kMaxSlots && c.tile.slots * kv_heads < 2 * c.tile.workgroups;
   return c;
 }
 
@@ -1358,7 +1402,8 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
   l.workgroups = c.workgroups;
   int64_t grid = c.slots * a.kv_heads;
   if (l.split) {
-    grid = c.workgroups;
+    // (tile_kernel may keep its tiles whole: then one workgroup each, handed out as they come)
+    if (STREAM || grid < c.workgroups) grid = c.workgroups;
     char* p = static_cast<char*>(workspace);
     l.plan = reinterpret_cast<int32_t*>(p);
     l.ml = reinterpret_cast<float2*>(p + align16((size_t)(c.slots + 3) * 4));
@@ -1386,6 +1431,8 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
 
 template <int D, bool FP8>
 int launch_dim(const AttentionArgs& a, const Choices& c, void* workspace, hipStream_t stream) {
+  // smallest shares: 2 blocks of 128 keys (one token over 4096 keys 12.0 us, 1 block 11.2, 4 blocks 13.4; over
+  // 16384 keys 17.6, 22.7 and 17.0) and 4 of 64 keys
   if (c.stream.used) {
     const int st = c.stream.bm == 16
         ? launch_one<D, 16, kStreamBlock, true>(stream_kernel<D, FP8, 1>, a, c.stream, 2, workspace, stream)
