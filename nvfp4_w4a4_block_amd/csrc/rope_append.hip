@@ -238,8 +238,9 @@ int launch_groups(RopeAppendArgs a, hipStream_t stream) {
   auto groups = [](const HeadsView& x) { return (x.heads + RPW - 1) / RPW; };
   a.groups = groups(a.q) + groups(a.k) + (APPEND ? groups(a.v) : 0);
   // Enough wavefronts to fill the GPU: several groups each, else one for the shortest path (12 groups of 128 channels
-  // a token: 2048 tokens 13.3 us with two groups and 13.8 with one, 512 tokens 5.9 and 5.6).
-  const bool many = (int64_t)a.tokens * a.groups >= 2 * 8192;
+  // a token: 2048 tokens 13.3 us with two groups and 13.8 with one, 512 tokens 5.9 and 5.6).  An fp32 lane has twice
+  // the bytes in flight already (4096 tokens 45.3 and 43.9).
+  const bool many = sizeof(XT) == 2 && (int64_t)a.tokens * a.groups >= 2 * 8192;
   const int u = many ? kGroups : 1;
   a.jobs = (a.groups + u - 1) / u;
   const int64_t jobs = (int64_t)a.tokens * a.jobs;
