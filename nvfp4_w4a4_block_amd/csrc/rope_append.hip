@@ -26,7 +26,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = 2;
+// Groups of a wavefront where there are many: an fp32 lane has twice the bytes in flight already (4096 tokens of 48
+// heads of 128: 45.3 us with two groups, 43.9 with one).
+template <typename XT>
+constexpr int kGroups = sizeof(XT) == 2 ? 2 : 1;
 
 __device__ __forceinline__ void load8(const uint16_t* x, float (&e)[8]) {
   widen(*reinterpret_cast<const uint4*>(x), e, x);
@@ -238,16 +241,15 @@ int launch_groups(RopeAppendArgs a, hipStream_t stream) {
   auto groups = [](const HeadsView& x) { return (x.heads + RPW - 1) / RPW; };
   a.groups = groups(a.q) + groups(a.k) + (APPEND ? groups(a.v) : 0);
   // Enough wavefronts to fill the GPU: several groups each, else one for the shortest path (12 groups of 128 channels
-  // a token: 2048 tokens 13.3 us with two groups and 13.8 with one, 512 tokens 5.9 and 5.6).  An fp32 lane has twice
-  // the bytes in flight already (4096 tokens 45.3 and 43.9).
-  const bool many = sizeof(XT) == 2 && (int64_t)a.tokens * a.groups >= 2 * 8192;
-  const int u = many ? kGroups : 1;
+  // a token: 2048 tokens 13.3 us with two groups and 13.8 with one, 512 tokens 5.9 and 5.6).
+  const bool many = (int64_t)a.tokens * a.groups >= 2 * 8192;
+  const int u = many ? kGroups<XT> : 1;
   a.jobs = (a.groups + u - 1) / u;
   const int64_t jobs = (int64_t)a.tokens * a.jobs;
   if (jobs * 64 + kThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;      // threads of a launch
   const unsigned grid = (unsigned)((jobs + kThreads / 64 - 1) / (kThreads / 64));
   if (many)
-    rope_append_kernel<XT, LPR, kGroups, APPEND><<<grid, kThreads, 0, stream>>>(a);
+    rope_append_kernel<XT, LPR, kGroups<XT>, APPEND><<<grid, kThreads, 0, stream>>>(a);
   else
     rope_append_kernel<XT, LPR, 1, APPEND><<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
