@@ -502,9 +502,9 @@ int nvfp4_kv_append(const nvfp4_paged_kv* kv, int64_t tokens, int x_dtype, const
  *   lse          device fp32 [tokens, q heads] contiguous, or NULL: ln sum_j exp(scale q.k_j).
  *   workspace    device, 16-byte aligned, nvfp4_paged_attention_workspace_size() bytes for the same
  *                arguments; contents need no initialisation and are clobbered.
- * Scores, softmax statistics and sums are fp32; probabilities are rounded to fp16 (E4M3 cache) or
- * bf16 (bf16 cache) for their product with V.  Deterministic: the same inputs and arguments
- * give the same bits.
+ * Scores, softmax statistics and sums are fp32; probabilities are rounded for their product with V: to fp16 beside an
+ * E4M3 cache (2^-11 relative, at most 2^-32 of the row's sum absolute), to bf16 beside a bf16 cache (2^-8
+ * relative), whose values may exceed fp16's range.  Deterministic: the same inputs and arguments give the same bits.
  */
 int nvfp4_paged_attention(const nvfp4_paged_kv* kv, int64_t tokens, int64_t max_q, const nvfp4_heads* q, float scale,
                           int causal, int64_t window, const nvfp4_heads* out, float* lse, void* workspace,

@@ -6,8 +6,10 @@
 // key scale folded into the factor c):  s_j = q . k_j,  m' = max(m, s),  l <- l 2^{(m - m') c} + sum 2^{(s - m') c},
 // O <- O 2^{(m - m') c} + sum 2^{(s - m') c} v_j,  out = O / l * v_scale,  lse = (m c + log2 l) ln 2.
 // m, l, O and the scores are fp32.  The factor by which old values are scaled down is applied only when
-// the maximum grows by more than 2^8 (kLazy): until then probabilities are at most 2^8 instead of 1,
-// which neither fp32 sums nor fp16 probabilities (largest 65504) notice.
+// the maximum grows by more than 2^8 (kLazy): until then probabilities are up to 2^8 times what they would be.
+// Beside an E4M3 cache they are held 2^7 times larger (kLift; l, O and m c in the same scale): at most 2^15, within
+// fp16's 65504, with a row's sum of at least 2^7.  fp16's smallest step, 2^-24, then takes at most 2^-32 of the sum from
+// a key; at a sum of 1 it took 2^-25, and a long flat tail beside a peak was lost altogether.
 //
 // Operands of the matrix instructions.  E4M3 values are exact in bf16 and in fp16.  Scores: bf16 queries
 // (as given) times bf16 keys, exact products.  Output: probabilities are rounded to fp16 next to fp16
@@ -56,6 +58,8 @@ constexpr int tile_block(int d) { return 64; }
 constexpr int kCutCost = 16;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
+template <bool FP8>
+constexpr float kLift = FP8 ? 7.0f : 0.0f;
 constexpr float kLn2 = 0.693147180559945f;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -73,7 +77,7 @@ struct Launch {
   int32_t rows_grid;         // combine_kernel: workgroups per (slot, head)
   int32_t* plan;             // written by the attention kernel for combine_kernel: [0] blocks per share, [1] all
                              // blocks of a head, [2 ..] first block of every sequence (stream) or slot (tile)
-  float2* ml;                // [2 workgroups][BM]: m c, l
+  float2* ml;                // [2 workgroups][BM]: m c - kLift, l
   float* po;                 // [2 workgroups][BM][D]: O
 };
 
@@ -492,8 +496,15 @@ __device__ __forceinline__ float max_across_16(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// m c of a running maximum; a row that has seen no key keeps the lowest value.
-__device__ __forceinline__ float scaled_max(float m, float c) { return m == kLowest ? kLowest : m * c; }
+// What a row's exponents are taken against, m c - kLift, from its running maximum; 0 for a row that has seen no key
+// (its scores are -inf, their exponentials 0 beside any finite value).
+template <bool FP8>
+__device__ __forceinline__ float exponent_base(float m, float c) {
+  return m == kLowest ? 0.0f : __builtin_fmaf(m, c, -kLift<FP8>);
+}
+// The same for joining parts, where a row that has seen no key must not weigh: the lowest value.
+template <bool FP8>
+__device__ __forceinline__ float scaled_max(float m, float c) { return m == kLowest ? kLowest : exponent_base<FP8>(m, c); }
 
 // ---- few rows ----------------------------------------------------------------------------------------
 
@@ -655,7 +666,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
 #pragma unroll
           for (int i = 0; i < NT; ++i) o[rb][i] *= f0;
         }
-        const float mc = m[rb] == kLowest ? 0.0f : m[rb] * c;
+        const float mc = exponent_base<FP8>(m[rb], c);
         float p8[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -746,7 +757,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
       l0 += __shfl_xor(l0, 16, 64);
       l0 += __shfl_xor(l0, 32, 64);
       __syncthreads();
-      if (quarter == 0) merge_ml[wave][n] = make_float2(scaled_max(m[rb], c), l0);
+      if (quarter == 0) merge_ml[wave][n] = make_float2(scaled_max<FP8>(m[rb], c), l0);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -1122,7 +1133,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
             if constexpr (kAcc) asm volatile("" : "+a"(o[rw][i]));
           }
         }
-        mc[rw] = m[rw] == kLowest ? 0.0f : m[rw] * c;
+        mc[rw] = exponent_base<FP8>(m[rw], c);
       }
       // Exponentials of 8 keys (group g) and the product with V, a group behind.
       {
@@ -1208,7 +1219,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 #pragma unroll
     for (int rw = 0; rw < RW; ++rw) {
       const float ll = sum[rw] + __shfl_xor(sum[rw], 32, 64);
-      const float mm = scaled_max(m[rw], c);
+      const float mm = scaled_max<FP8>(m[rw], c);
       const int tr = wrow + rw * 32 + n;
       if (tr >= t.rows) continue;
       if (partial >= 0) {

@@ -1,0 +1,67 @@
+"""Corners of the paged cache's operators against the plain 64-bit implementation: probabilities far below a row's
+largest, scores of every size, non-finite values whatever the keys' division over wavefronts and workgroups."""
+import math
+
+import pytest
+import torch
+
+from tests.gpu_helpers import DEV, nv
+from tests.paged_helpers import Batch, assert_close, decode
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def run(b: Batch, **kw):
+    kv, kv_len, cu, q = b.device()
+    out, lse = nv().paged_attention(q, kv, kv_len, cu, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), lse.cpu()
+
+
+def place(b: Batch, s: int, key: int):
+    """(page, row) of a key of sequence s."""
+    return int(b.table[s, key // b.page]), key % b.page
+
+
+def store(b: Batch, x: torch.Tensor) -> torch.Tensor:
+    return x.to(torch.float8_e4m3fn).view(torch.uint8) if b.fp8 else x.to(BF16)
+
+
+def one_channel_scores(b: Batch, scores: torch.Tensor) -> None:
+    """Keys of sequence 0 whose score, before the scale, is scores[key] for every query: channel 0 of q is 1."""
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.k.zero_()
+    if b.fp8:
+        b.ks, b.vs = torch.ones(1), torch.ones(1)
+    x = store(b, scores.float())
+    for key in range(b.kv[0]):
+        p, r = place(b, 0, key)
+        b.k[p, :, r, 0] = x[key]
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("n,L", [(1, 100), (1, 4000), (4, 700), (100, 900), (300, 4100)])
+@pytest.mark.parametrize("below", [23.0, 25.5, 29.0])
+def test_long_flat_tail_beside_a_peak(fp8, n, L, below):
+    # key 0 has the row's largest score and a zero value, every other key a probability of 2^-below beside it, so
+    # the output is what the small probabilities add up to.  Tolerance: a probability is held in a scale where the
+    # row's sum is at least 2^7 next to fp16, whose absolute rounding is 2^-25: 2^-32 of |v| per key, not
+    # the 2^-25 that a sum of 1 would leave.
+    b = Batch([n], [L], 10, 2, 128, fp8, seed=n)
+    scores = torch.zeros(L)
+    scores[0] = 16.0
+    one_channel_scores(b, scores)
+    p0, r0 = place(b, 0, 0)
+    b.v[p0, :, r0] = 0
+    scale = below * math.log(2) / 16
+    want, want_lse, tol, tol_lse = b.attention(scale)
+    if fp8:
+        for h in range(2):
+            V = decode(b.v[b.table[0].long(), h]).reshape(-1, 128)[:L].abs().cumsum(0)[L - n:]
+            tol[:, h * 5:h * 5 + 5] += (2.0 ** -32 - 2.0 ** -25) * V[:, None]
+    out, lse = run(b, scale=scale)
+    assert_close(out, want, tol, "out")
+    assert_close(lse, want_lse, tol_lse, "lse")
