@@ -468,6 +468,10 @@ __device__ __forceinline__ float non_finite_part(uint32_t up, uint32_t down) {
   return (up ? __builtin_inff() : 0.0f) + (down ? -__builtin_inff() : 0.0f);
 }
 
+// O / l (f is v_scale / l).  A row whose sum is 0 has zeros, selected and not multiplied: its O may be infinite or NaN,
+// from values at keys whose scores are all -inf.
+__device__ __forceinline__ float normalised(float o, float l, float f) { return l == 0.0f ? 0.0f : o * f; }
+
 template <int W>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   if constexpr (W == 1) {
@@ -790,11 +794,13 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
         } else {
           const int r = t.row0 + rb * 16 + row;
           const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-          const float f = ll == 0.0f ? 0.0f : vs / ll;
+          const float f = vs / ll;
           uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + d;
 #pragma unroll
           for (int i = 0; i < NT; i += 4)
-            *reinterpret_cast<uint2*>(y + i) = make_uint2(bf16_pair(e[i] * f, e[i + 1] * f), bf16_pair(e[i + 2] * f, e[i + 3] * f));
+            *reinterpret_cast<uint2*>(y + i) =
+                make_uint2(bf16_pair(normalised(e[i], ll, f), normalised(e[i + 1], ll, f)),
+                           bf16_pair(normalised(e[i + 2], ll, f), normalised(e[i + 3], ll, f)));
           if (a.lse && d == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
         }
       }
@@ -1234,15 +1240,15 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       } else {
         const int r = t.row0 + tr;
         const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-        const float f = ll == 0.0f ? 0.0f : vs / ll;
+        const float f = vs / ll;
         uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             *reinterpret_cast<uint2*>(y + i * 32 + 8 * x + 4 * half) =
-                make_uint2(bf16_pair(o[rw][i][4 * x] * f, o[rw][i][4 * x + 1] * f),
-                           bf16_pair(o[rw][i][4 * x + 2] * f, o[rw][i][4 * x + 3] * f));
+                make_uint2(bf16_pair(normalised(o[rw][i][4 * x], ll, f), normalised(o[rw][i][4 * x + 1], ll, f)),
+                           bf16_pair(normalised(o[rw][i][4 * x + 2], ll, f), normalised(o[rw][i][4 * x + 3], ll, f)));
         if (a.lse && half == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
       }
     }
@@ -1337,9 +1343,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
     const float vs = a.v_scale ? a.v_scale[h * a.scale_stride] : 1.0f;
     const int r = t.row0 + row;
     const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-    const float f = sum == 0.0f ? 0.0f : vs / sum;
+    const float f = vs / sum;
     *reinterpret_cast<uint2*>(a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + x * 4) =
-        make_uint2(bf16_pair(acc.x * f, acc.y * f), bf16_pair(acc.z * f, acc.w * f));
+        make_uint2(bf16_pair(normalised(acc.x, sum, f), normalised(acc.y, sum, f)),
+                   bf16_pair(normalised(acc.z, sum, f), normalised(acc.w, sum, f)));
     if (a.lse && x == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (m + __builtin_log2f(sum)) * kLn2;
   }
 }

@@ -65,3 +65,16 @@ def test_long_flat_tail_beside_a_peak(fp8, n, L, below):
     out, lse = run(b, scale=scale)
     assert_close(out, want, tol, "out")
     assert_close(lse, want_lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("n,L", [(1, 60), (3, 2100), (100, 130), (150, 3000)])
+def test_every_score_minus_infinity_gives_zeros_whatever_the_values(n, L):
+    b = Batch([n], [L], 10, 2, 128, False, seed=n)
+    b.k[:, :, :, 5] = -math.inf
+    b.q[:, :, 5] = b.q[:, :, 5].abs() + 1
+    for key, d, val in ((0, 3, math.inf), (17, 3, -math.inf), (40, 7, math.nan), (L - n, 9, math.inf)):
+        p, r = place(b, 0, key)
+        b.v[p, :, r, d] = val
+    for max_q in (0, n):
+        out, lse = run(b, max_q=max_q)
+        assert (out == 0).all() and (lse == -math.inf).all()
