@@ -492,12 +492,13 @@ int nvfp4_kv_append(const nvfp4_paged_kv* kv, int64_t tokens, int x_dtype, const
  * and with window > 0 only the last `window` of them; with causal = 0 all kv_len (window must be 0).
  * One call takes any mix of single tokens and chunks.  A token that sees no key (an empty
  * sequence, a position below 0, no valid page), or whose every score is -inf, gets zeros and lse =
- * -inf.  Keys a token does not see have no influence, whatever their bytes hold (NaN, infinities).
+ * -inf.  Keys a token does not see have no influence, whatever their bytes hold (NaN, infinities).  An infinite or
+ * NaN value at a key it does see reaches its output however small the probability.
  *   q            bf16, heads a multiple of kv->kv_heads, at most 256 per key-value head.
  *   head_dim     64, 128 or 256 (others: NVFP4_ERR_UNSUPPORTED).
  *   scale        > 0 and finite, usually head_dim^-0.5.
  *   max_q        the largest number of new tokens of one sequence, or 0 if not known: a hint that
- *                picks kernels.  Results do not depend on its truth, speed does.
+ *                picks kernels.  Results do not depend on its truth beyond rounding (the order of sums), speed does.
  *   out          bf16 (round to nearest even), heads as q; must not overlap the inputs.
  *   lse          device fp32 [tokens, q heads] contiguous, or NULL: ln sum_j exp(scale q.k_j).
  *   workspace    device, 16-byte aligned, nvfp4_paged_attention_workspace_size() bytes for the same

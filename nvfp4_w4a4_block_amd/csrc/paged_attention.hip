@@ -39,7 +39,7 @@
 // Keys outside [0, kv_len) or on an invalid page are zeroed (V) and masked (scores); keys only some rows of
 // a tile see are masked by selection.  0 * inf would still reach rows that do not see the key, so
 // non-finite values of V are taken out of the product and added afterwards to the rows that do see
-// them (any positive probability times inf or NaN is inf or NaN).
+// them (any positive probability times inf or NaN is inf or NaN, also one too small for fp32).
 #include "paged_device.h"
 
 namespace nvfp4 {
@@ -468,6 +468,13 @@ __device__ __forceinline__ float non_finite_part(uint32_t up, uint32_t down) {
   return (up ? __builtin_inff() : 0.0f) + (down ? -__builtin_inff() : 0.0f);
 }
 
+// A part's O times its weight, at most 1.  An infinite or NaN O (from such values, under positive probabilities) stays
+// what it is also where the weight underflows to 0: the answer does not depend on how the keys were divided.
+__device__ __forceinline__ float weighted(float o, float w) {
+  const float x = o * w;
+  return x != x ? o : x;
+}
+
 // O / l (f is v_scale / l).  A row whose sum is 0 has zeros, selected and not multiplied: its O may be infinite or NaN,
 // from values at keys whose scores are all -inf.
 __device__ __forceinline__ float normalised(float o, float l, float f) { return l == 0.0f ? 0.0f : o * f; }
@@ -783,7 +790,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
         for (int i = 0; i < NT; ++i) {
           e[i] = 0.0f;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) e[i] += merge[v][row][d + i] * w[v];
+          for (int v = 0; v < 4; ++v) e[i] += weighted(merge[v][row][d + i], w[v]);
         }
         if (partial >= 0) {
           const int64_t at = (int64_t)partial * BM + rb * 16 + row;
@@ -1314,10 +1321,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
           const float mx = __builtin_fmaxf(m, ml[i].x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml[i].x - mx);
           m = mx;
           sum = sum * f0 + ml[i].y * f1;
-          acc.x = acc.x * f0 + v[i].x * f1;
-          acc.y = acc.y * f0 + v[i].y * f1;
-          acc.z = acc.z * f0 + v[i].z * f1;
-          acc.w = acc.w * f0 + v[i].w * f1;
+          acc.x = weighted(acc.x, f0) + weighted(v[i].x, f1);
+          acc.y = weighted(acc.y, f0) + weighted(v[i].y, f1);
+          acc.z = weighted(acc.z, f0) + weighted(v[i].z, f1);
+          acc.w = weighted(acc.w, f0) + weighted(v[i].w, f1);
         }
       }
     }
@@ -1333,10 +1340,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
         const float mx = __builtin_fmaxf(m, ml.x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml.x - mx);
         m = mx;
         sum = sum * f0 + ml.y * f1;
-        acc.x = acc.x * f0 + v.x * f1;
-        acc.y = acc.y * f0 + v.y * f1;
-        acc.z = acc.z * f0 + v.z * f1;
-        acc.w = acc.w * f0 + v.w * f1;
+        acc.x = weighted(acc.x, f0) + weighted(v.x, f1);
+        acc.y = weighted(acc.y, f0) + weighted(v.y, f1);
+        acc.z = weighted(acc.z, f0) + weighted(v.z, f1);
+        acc.w = weighted(acc.w, f0) + weighted(v.w, f1);
       }
     }
     if (!live) continue;

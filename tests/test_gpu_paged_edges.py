@@ -78,3 +78,24 @@ def test_every_score_minus_infinity_gives_zeros_whatever_the_values(n, L):
     for max_q in (0, n):
         out, lse = run(b, max_q=max_q)
         assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,L", [(1, 200), (3, 5000), (100, 260), (100, 5000)])
+def test_infinite_values_under_tiny_probabilities(D, n, L):
+    # the key at `peak` is about 280 (natural) above the others: their probabilities are positive, but exp2 of the
+    # distance is 0 in fp32, wherever the keys' maxima are joined
+    for bad in (1, 33, 70, L // 2):
+        b = Batch([n], [L], 8, 2, D, False, seed=n + D)
+        peak = 5
+        b.q[:, :, 0] = 16.0
+        b.k[:, :, :, 0] = 0.0
+        p, r = place(b, 0, peak)
+        b.k[p, :, r, 0] = 280.0 / 16 * D ** 0.5
+        p, r = place(b, 0, bad)
+        b.v[p, :, r, 3], b.v[p, :, r, 7], b.v[p, :, r, D - 1] = math.inf, -math.inf, math.nan
+        want, want_lse, tol, tol_lse = b.attention()
+        for max_q in (0, n):
+            out, lse = run(b, max_q=max_q)
+            assert_close(out, want, tol, f"key {bad}, max_q {max_q}")
+            assert_close(lse, want_lse, tol_lse)
