@@ -60,6 +60,10 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
 template <bool FP8>
 constexpr float kLift = FP8 ? 7.0f : 0.0f;
+// An exponent is one fused multiply-add, s c - (m c - kLift), whose constant is rounded: at the row's largest key it is off
+// by half an ulp of m c, which passes 1 from |m c| = 2^24 on and would overflow or erase every probability of the row
+// further up.  From this size on the scores are taken against the maximum first (below it the rounding is under 2^-12).
+constexpr float kFar = 0x1p12f;
 constexpr float kLn2 = 0.693147180559945f;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -513,9 +517,16 @@ template <bool FP8>
 __device__ __forceinline__ float exponent_base(float m, float c) {
   return m == kLowest ? 0.0f : __builtin_fmaf(m, c, -kLift<FP8>);
 }
-// The same for joining parts, where a row that has seen no key must not weigh: the lowest value.
+// The same for joining parts, where a row that has seen no key must not weigh: the lowest value.  Kept finite, as
+// the difference of two parts' has to be.
 template <bool FP8>
-__device__ __forceinline__ float scaled_max(float m, float c) { return m == kLowest ? kLowest : exponent_base<FP8>(m, c); }
+__device__ __forceinline__ float scaled_max(float m, float c) {
+  return m == kLowest ? kLowest : __builtin_amdgcn_fmed3f(exponent_base<FP8>(m, c), kLowest, -kLowest);
+}
+// Whether any row of the wavefront has to have its scores taken against the maximum first.
+__device__ __forceinline__ bool far_scores(float base) {
+  return __builtin_amdgcn_ballot_w64(__builtin_fabsf(base) > kFar) != 0;
+}
 
 // ---- few rows ----------------------------------------------------------------------------------------
 
@@ -677,7 +688,14 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
 #pragma unroll
           for (int i = 0; i < NT; ++i) o[rb][i] *= f0;
         }
-        const float mc = exponent_base<FP8>(m[rb], c);
+        float mc = exponent_base<FP8>(m[rb], c);
+        if (far_scores(mc)) {
+          asm volatile("");        // a branch, as above
+          const float from = m[rb] == kLowest ? 0.0f : m[rb];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[rb][j >> 2][j & 3] -= from;
+          mc = -kLift<FP8>;
+        }
         float p8[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -1147,6 +1165,15 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           }
         }
         mc[rw] = exponent_base<FP8>(m[rw], c);
+        if (far_scores(mc[rw])) {
+          asm volatile("");        // a branch, as above
+          const float from = m[rw] == kLowest ? 0.0f : m[rw];
+#pragma unroll
+          for (int kb = 0; kb < KB / 32; ++kb)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) s[rw][kb][x] -= from;
+          mc[rw] = -kLift<FP8>;
+        }
       }
       // Exponentials of 8 keys (group g) and the product with V, a group behind.
       {

@@ -99,3 +99,24 @@ def test_infinite_values_under_tiny_probabilities(D, n, L):
             out, lse = run(b, max_q=max_q)
             assert_close(out, want, tol, f"key {bad}, max_q {max_q}")
             assert_close(lse, want_lse, tol_lse)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,L", [(1, 300), (1, 3000), (60, 300)])
+@pytest.mark.parametrize("power", [20, 24, 28, 31, 36, 60])
+def test_scores_of_every_size(fp8, sign, n, L, power):
+    # scores are multiples of 2^power (exact products), so each row's answer is the value of its largest: any rounding
+    # of scores of 16 * 2^power to fp32 stays below the 2^power between neighbours.  Nothing but that value
+    # remains of the sum; it is rounded to bf16 once: 2^-8 of it.
+    b = Batch([n], [L], 10, 2, 128, fp8, seed=power)
+    level = torch.randint(1, 12, (L,), generator=b.g).float()
+    level[7] = 15.0 if sign > 0 else 0.5
+    one_channel_scores(b, sign * level)
+    out, lse = run(b, scale=2.0 ** power)
+    p, r = place(b, 0, 7)
+    for h in range(2):
+        want = decode(b.v[p, h, r])[None, None].expand(n, 5, 128)
+        assert_close(out[:, h * 5:h * 5 + 5], want, 2.0 ** -8 * want.abs(), f"head {h}")
+    top = sign * float(level[7]) * 2.0 ** power
+    assert_close(lse, torch.full(lse.shape, top, dtype=torch.float64), torch.full(lse.shape, 2.0 ** -21 * abs(top), dtype=torch.float64))
