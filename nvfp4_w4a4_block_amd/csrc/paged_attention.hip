@@ -511,17 +511,23 @@ __device__ __forceinline__ float max_across_16(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// What a row's exponents are taken against, m c - kLift, from its running maximum; 0 for a row that has seen no key
-// (its scores are -inf, their exponentials 0 beside any finite value).
+// What a row's exponents are taken against, m c - kLift, from its running maximum; 0 while that is the lowest value: a
+// row that has seen no key (its scores are -inf, their exponentials 0 beside any finite value), or one whose
+// scores are all so small beside 1 / c that the maximum has not moved (c below 2.4e-38).
 template <bool FP8>
 __device__ __forceinline__ float exponent_base(float m, float c) {
   return m == kLowest ? 0.0f : __builtin_fmaf(m, c, -kLift<FP8>);
 }
-// The same for joining parts, where a row that has seen no key must not weigh: the lowest value.  Kept finite, as
-// the difference of two parts' has to be.
+// The same for joining parts, where a row without a sum must not weigh: the lowest value.  Kept finite, as the
+// difference of two parts' has to be.
 template <bool FP8>
-__device__ __forceinline__ float scaled_max(float m, float c) {
-  return m == kLowest ? kLowest : __builtin_amdgcn_fmed3f(exponent_base<FP8>(m, c), kLowest, -kLowest);
+__device__ __forceinline__ float scaled_max(float m, float c, float sum) {
+  return sum == 0.0f ? kLowest : __builtin_amdgcn_fmed3f(exponent_base<FP8>(m, c), kLowest, -kLowest);
+}
+// The factor that brings what was summed against maximum m to maximum mx.
+template <bool FP8>
+__device__ __forceinline__ float rescale(float m, float mx, float c) {
+  return exp2_fast(m == kLowest ? __builtin_fminf(-exponent_base<FP8>(mx, c), 0.0f) : (m - mx) * c);
 }
 // Whether any row of the wavefront has to have its scores taken against the maximum first.
 __device__ __forceinline__ bool far_scores(float base) {
@@ -682,7 +688,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
           for (int i = 0; i < 4; ++i) mx = __builtin_fmaxf(mx, s[rb][g][i]);
         mx = max_across_32(max_across_16(mx));
         if (__builtin_amdgcn_ballot_w64((mx - m[rb]) * c > kLazy) != 0) {
-          const float f0 = exp2_fast((m[rb] - mx) * c);
+          const float f0 = rescale<FP8>(m[rb], mx, c);
           m[rb] = mx;
           sum[rb] *= f0;
 #pragma unroll
@@ -786,7 +792,7 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
       l0 += __shfl_xor(l0, 16, 64);
       l0 += __shfl_xor(l0, 32, 64);
       __syncthreads();
-      if (quarter == 0) merge_ml[wave][n] = make_float2(scaled_max<FP8>(m[rb], c), l0);
+      if (quarter == 0) merge_ml[wave][n] = make_float2(scaled_max<FP8>(m[rb], c, l0), l0);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -1153,7 +1159,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
           for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[rw][kb][x]);
         mx = max_across_32(mx);
         if (__builtin_amdgcn_ballot_w64((mx - m[rw]) * c > kLazy) != 0) {
-          const float f0 = exp2_fast((m[rw] - mx) * c);
+          const float f0 = rescale<FP8>(m[rw], mx, c);
           m[rw] = mx;
           sum[rw] *= f0;
           // (kAcc: taken out of the accumulation registers here and not ahead of the branch)
@@ -1259,7 +1265,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 #pragma unroll
     for (int rw = 0; rw < RW; ++rw) {
       const float ll = sum[rw] + __shfl_xor(sum[rw], 32, 64);
-      const float mm = scaled_max<FP8>(m[rw], c);
+      const float mm = scaled_max<FP8>(m[rw], c, ll);
       const int tr = wrow + rw * 32 + n;
       if (tr >= t.rows) continue;
       if (partial >= 0) {

@@ -102,6 +102,17 @@ def test_infinite_values_under_tiny_probabilities(D, n, L):
 
 
 @pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("n", [1, 60])
+@pytest.mark.parametrize("scale", [1e-30, 1e-37, 3e-39])
+def test_smallest_softmax_scales(fp8, n, scale):
+    b = Batch([n], [333], 8, 2, 128, fp8, seed=n)
+    want, want_lse, tol, tol_lse = b.attention(scale)
+    out, lse = run(b, scale=scale)
+    assert_close(out, want, tol, "out")
+    assert_close(lse, want_lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("fp8", [True, False])
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("n,L", [(1, 300), (1, 3000), (60, 300)])
 @pytest.mark.parametrize("power", [20, 24, 28, 31, 36, 60])
