@@ -9,7 +9,9 @@
 // the maximum grows by more than 2^8 (kLazy): until then probabilities are up to 2^8 times what they would be.
 // Beside an E4M3 cache they are held 2^7 times larger (kLift; l, O and m c in the same scale): at most 2^15, within
 // fp16's 65504, with a row's sum of at least 2^7.  fp16's smallest step, 2^-24, then takes at most 2^-32 of the sum from
-// a key; at a sum of 1 it took 2^-25, and a long flat tail beside a peak was lost altogether.
+// a key; at a sum of 1 it took 2^-25, and a long flat tail beside a peak was lost altogether.  Beside a bf16 cache they
+// are held 2^8 times smaller, at most 1, so that O passes fp32's range only where a sum of the values does: values
+// may be as large as fp32's own, and bf16 probabilities have its exponents.
 //
 // Operands of the matrix instructions.  E4M3 values are exact in bf16 and in fp16.  Scores: bf16 queries
 // (as given) times bf16 keys, exact products.  Output: probabilities are rounded to fp16 next to fp16
@@ -59,7 +61,7 @@ constexpr int kCutCost = 16;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
 template <bool FP8>
-constexpr float kLift = FP8 ? 7.0f : 0.0f;
+constexpr float kLift = FP8 ? 7.0f : -8.0f;
 // An exponent is one fused multiply-add, s c - (m c - kLift), whose constant is rounded: at the row's largest key it is off
 // by half an ulp of m c, which passes 1 from |m c| = 2^24 on and would overflow or erase every probability of the row
 // further up.  From this size on the scores are taken against the maximum first (below it the rounding is under 2^-12).

@@ -131,3 +131,14 @@ def test_scores_of_every_size(fp8, sign, n, L, power):
         assert_close(out[:, h * 5:h * 5 + 5], want, 2.0 ** -8 * want.abs(), f"head {h}")
     top = sign * float(level[7]) * 2.0 ** power
     assert_close(lse, torch.full(lse.shape, top, dtype=torch.float64), torch.full(lse.shape, 2.0 ** -21 * abs(top), dtype=torch.float64))
+
+
+@pytest.mark.parametrize("n,L", [(1, 700), (1, 5000), (100, 1000)])
+def test_values_near_the_largest_bf16(n, L):
+    # scores rise along the keys by less than the step at which old values are scaled down
+    b = Batch([n], [L], 10, 2, 128, False, seed=n, v_gain=2.0 ** 121)
+    one_channel_scores(b, torch.arange(L) / L * 5.25)
+    want, _, tol, _ = b.attention(1.0)
+    out, _ = run(b, scale=1.0)
+    assert torch.isfinite(want).all()
+    assert_close(out, want, tol)
