@@ -496,6 +496,7 @@ int nvfp4_kv_append(const nvfp4_paged_kv* kv, int64_t tokens, int x_dtype, const
  * NaN value at a key it does see reaches its output however small the probability.
  *   q            bf16, heads a multiple of kv->kv_heads, at most 256 per key-value head.
  *   head_dim     64, 128 or 256 (others: NVFP4_ERR_UNSUPPORTED).
+ *   table_width * page_size  at most 2^30 (more: NVFP4_ERR_UNSUPPORTED).
  *   scale        > 0 and finite, usually head_dim^-0.5.
  *   max_q        the largest number of new tokens of one sequence, or 0 if not known: a hint that
  *                picks kernels.  Results do not depend on its truth beyond rounding (the order of sums), speed does.

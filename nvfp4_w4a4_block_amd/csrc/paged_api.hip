@@ -178,6 +178,9 @@ int nvfp4_paged_attention(const nvfp4_paged_kv* kv, int64_t tokens, int64_t max_
   if (st != NVFP4_OK) return st;
   const int64_t dim = kv->head_dim;
   if (dim != 64 && dim != 128 && dim != 256) return NVFP4_ERR_UNSUPPORTED;
+  // key numbers stay in 32 bits, also a block past the end, and where cu_q is not ordered and a tile is given the
+  // blocks of another
+  if ((int64_t)kv->table_width * kv->page_size > (int64_t)1 << 30) return NVFP4_ERR_UNSUPPORTED;
   if (!q || !out) return NVFP4_ERR_INVALID_ARG;
   if (tokens == 0 || kv->num_seqs == 0) return NVFP4_OK;
   HeadsView qv, ov;
