@@ -1458,7 +1458,8 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
   // nothing to cut where the table holds no more keys than the smallest share, or where block
   // numbers could pass 31 bits
   const int64_t cap = (((int64_t)a.table_width << a.page_shift) + KB - 1) / KB;
-  l.split = c.split && cap > min_blocks && cap * c.slots < INT32_MAX;
+  l.split = c.split && cap > min_blocks &&
+            plan_fits(STREAM, c.slots, a.num_seqs, (int64_t)a.tokens * a.group, c.rows_hi, BM, cap, a.kv_heads, c.workgroups);
   l.workgroups = c.workgroups;
   int64_t grid = c.slots * a.kv_heads;
   if (l.split) {

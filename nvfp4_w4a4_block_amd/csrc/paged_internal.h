@@ -56,6 +56,19 @@ struct AttentionArgs {
   int32_t causal, window;        // window 0: none
 };
 
+// Whether the blocks of a head that a split launch can plan, and a share of all heads' blocks, stay below 2^31
+// whatever cu_q holds on the device.  In order, its sequences have at most `slots` row tiles of at most `cap` blocks each;
+// where it is not (a caller's mistake, which must not lead to accesses out of range), every one of them may have
+// all `tokens * group` rows, or the `rows_hi` that a launch takes at most.  per_sequence: the plan adds up sequences, else
+// slots, each counted once.
+inline bool plan_fits(bool per_sequence, int64_t slots, int64_t num_seqs, int64_t rows, int64_t rows_hi, int64_t bm,
+                      int64_t cap, int64_t kv_heads, int64_t workgroups) {
+  const int64_t most = rows < rows_hi ? rows : rows_hi;
+  int64_t tiles = per_sequence ? num_seqs * ((most + bm - 1) / bm) : 0;
+  if (tiles < slots) tiles = slots;
+  return tiles * cap < INT32_MAX && tiles * cap / workgroups * kv_heads < INT32_MAX / 2;
+}
+
 int launch_paged_attention(const AttentionArgs& a, int64_t max_q, int head_dim, void* workspace, hipStream_t stream);
 size_t paged_attention_workspace_bytes(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
                                        int64_t kv_heads, int head_dim);
