@@ -821,8 +821,11 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, kv_len: torch.Tensor, cu_q: to
     if workspace is None:
         workspace = q.new_empty((need,), dtype=torch.uint8) if need else None
     else:
-        have = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
-        _require(have > 0 and workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace: contiguous uint8")
+        _require(isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.is_contiguous(),
+                 "workspace: contiguous uint8")
+        have = workspace.numel()
+        if have < need:
+            raise ValueError(f"workspace: {have} bytes, {need} needed")
         _require(workspace.get_device() == gpu, "workspace: on another device than q")
     _run(gpu, "nvfp4_paged_attention", lib.nvfp4_paged_attention, c, T, max_q, qa, D ** -0.5 if scale is None else scale,
          1 if causal else 0, window, oa, _ptr(lse), _ptr(workspace), have)

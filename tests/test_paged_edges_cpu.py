@@ -68,3 +68,18 @@ int main() {
     assert r.returncode == 0, r.stderr[-2000:]
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def test_binding_takes_a_workspace_of_the_size_asked_for(nv):
+    kv, n, cu, q, _ = batch(nv, S=1100, T=1100)
+    size = lambda T, S: nv.lib.nvfp4_paged_attention_workspace_size(T, 0, S, 4, 2, 64, 2)  # noqa: E731
+    assert size(1100, 1100) == 0 and size(4, 3) > 0
+    with pytest.raises(ValueError, match="GPU"):            # nothing else is wrong
+        nv.paged_attention(q, kv, n, cu, workspace=torch.empty(size(1100, 1100), dtype=torch.uint8))
+    kv, n, cu, q, _ = batch(nv)
+    with pytest.raises(ValueError, match="GPU"):
+        nv.paged_attention(q, kv, n, cu, workspace=torch.empty(size(4, 3), dtype=torch.uint8))
+    for bad in (torch.empty(0), torch.empty(0, dtype=torch.int32), torch.empty(64, 64, dtype=torch.uint8).T, 5,
+                torch.empty(0, dtype=torch.uint8), torch.empty(size(4, 3) - 1, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            nv.paged_attention(q, kv, n, cu, workspace=bad)
