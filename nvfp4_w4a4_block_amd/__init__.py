@@ -651,7 +651,7 @@ def _cache_arg(kv: PagedKV, kv_len: torch.Tensor, cu_q: torch.Tensor, gpu: int) 
     if not (fp8 or dtype is torch.bfloat16) or v.dtype is not dtype:
         raise ValueError("kv.k, kv.v: both uint8 (E4M3 bytes) or both bfloat16")
     inner = (page * dim, dim, 1)
-    if pages > 0 and (sk[1:] != inner or sv[1:] != inner):
+    if pages > 0 and (sk[1:] != inner or sv[1:] != inner) and (heads != 1 or sk[2:] != inner[1:] or sv[2:] != inner[1:]):
         raise ValueError("kv.k, kv.v: every page must be contiguous")
     try:
         seqs, width = table.shape

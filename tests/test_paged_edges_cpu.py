@@ -83,3 +83,19 @@ def test_binding_takes_a_workspace_of_the_size_asked_for(nv):
                 torch.empty(0, dtype=torch.uint8), torch.empty(size(4, 3) - 1, dtype=torch.uint8)):
         with pytest.raises(ValueError, match="workspace"):
             nv.paged_attention(q, kv, n, cu, workspace=bad)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_binding_takes_a_single_head_whatever_its_stride(nv, fp8):
+    # [pages, page_size, heads, dim] seen as [pages, heads, page_size, dim]: with one head every page is contiguous
+    kv, n, cu, q, k = batch(nv, fp8=fp8, Hk=1)
+    one = kv.k.reshape(5, 16, 1, 64).transpose(1, 2)
+    assert one.shape == kv.k.shape and one.is_contiguous() and one.stride() != kv.k.stride()
+    view = nv.PagedKV(one, one, kv.page_table, kv.k_scale, kv.v_scale)
+    with pytest.raises(ValueError, match="GPU"):
+        nv.paged_attention(q, view, n, cu)
+    with pytest.raises(ValueError, match="GPU"):
+        nv.kv_append(view, k, k, n, cu)
+    for bad in (one[:, :, ::2], one[..., :32], one.transpose(2, 3).contiguous().transpose(2, 3)):
+        with pytest.raises(ValueError, match="contiguous"):
+            nv.kv_append(nv.PagedKV(bad, bad, kv.page_table, kv.k_scale, kv.v_scale), k, k, n, cu)
