@@ -1416,6 +1416,9 @@ size_t split_bytes(const Choice& c, int dim) {
   return align16((size_t)(c.slots + 3) * 4) + (size_t)2 * c.workgroups * c.bm * (8 + (size_t)dim * 4);
 }
 
+// Threads of a launch, a 32-bit number.
+bool fits_a_launch(int64_t workgroups) { return workgroups <= (int64_t)UINT32_MAX / kThreads; }
+
 // Which kernel takes which sequences.  By the hint (or the call's tokens) a sequence has at most `rows` packed rows:
 //   up to 32      stream_kernel alone, 16 or 32 rows a tile (8 query heads a group, 4 tokens over 8192 keys: 17 us,
 //                 by tile_kernel 26; 16 sequences of 4 tokens, bf16: 47 and 59)
@@ -1445,6 +1448,8 @@ Choices choose(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
   c.tile.slots = slots(c.tile.bm);
   c.tile.workgroups = dim == 256 ? 256 : 512;
   c.tile.split = c.tile.slots <= kMaxSlots && c.tile.slots * kv_heads < 2 * c.tile.workgroups;
+  // (a join has up to a workgroup per row)
+  for (Choice* x : {&c.stream, &c.tile}) x->split = x->split && fits_a_launch(x->slots * kv_heads * x->rows);
   return c;
 }
 
@@ -1470,9 +1475,6 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
     l.ml = reinterpret_cast<float2*>(p + align16((size_t)(c.slots + 3) * 4));
     l.po = reinterpret_cast<float*>(l.ml + (size_t)2 * c.workgroups * BM);
   }
-  if (grid * kThreads > (int64_t)UINT32_MAX ||
-      (l.split && c.slots * a.kv_heads * c.rows * kThreads > (int64_t)UINT32_MAX))
-    return NVFP4_ERR_UNSUPPORTED;
   kernel<<<(unsigned)grid, kThreads, 0, stream>>>(a, l);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   if (l.split) {
@@ -1515,6 +1517,8 @@ size_t paged_attention_workspace_bytes(int64_t tokens, int64_t max_q, int64_t nu
 
 int launch_paged_attention(const AttentionArgs& a, int64_t max_q, int head_dim, void* workspace, hipStream_t stream) {
   const Choices c = choose(a.tokens, max_q, a.num_seqs, a.q_heads, a.kv_heads, head_dim);
+  for (const Choice& x : {c.stream, c.tile})           // before anything is enqueued
+    if (x.used && !fits_a_launch(x.slots * a.kv_heads)) return NVFP4_ERR_UNSUPPORTED;
   const bool fp8 = a.k_scale != nullptr;
   switch (head_dim) {
     case 64: return fp8 ? launch_dim<64, true>(a, c, workspace, stream) : launch_dim<64, false>(a, c, workspace, stream);

@@ -99,3 +99,11 @@ def test_binding_takes_a_single_head_whatever_its_stride(nv, fp8):
     for bad in (one[:, :, ::2], one[..., :32], one.transpose(2, 3).contiguous().transpose(2, 3)):
         with pytest.raises(ValueError, match="contiguous"):
             nv.kv_append(nv.PagedKV(bad, bad, kv.page_table, kv.k_scale, kv.v_scale), k, k, n, cu)
+
+
+def test_launch_limits_are_found_before_anything_is_enqueued(nv):
+    # two kernels serve this call; only the second one's grid passes the limit.  (Without a GPU a launch is an error of
+    # its own, status 4.)
+    q = nv._Heads(0x10000, 256, 256 * 128, 128)
+    c = cache(nv, kv_heads=8, num_seqs=2_000_000, k_page_stride=1 << 20, v_page_stride=1 << 20)
+    assert attend(nv, c, T=400_000, q=q, out=q, ws=None, wsb=0) == 2
