@@ -413,8 +413,9 @@ typedef struct {
  *   kv_len       int32 [num_seqs]: tokens of the sequence in the cache, new ones included, at most
  *                table_width * page_size: new token i of n has position kv_len - n + i.
  * cu_q, kv_len and the page table are read on the device by the kernels, so a captured graph
- * follows their contents; a value out of range is clamped and never makes a kernel access memory
- * outside the operands. */
+ * follows their contents.  A value out of range never makes a kernel access memory outside the
+ * operands: attention clamps cu_q to the call's rows and kv_len to what the table holds, appending
+ * drops the tokens whose place is outside. */
 typedef struct {
   void* k;
   void* v;
