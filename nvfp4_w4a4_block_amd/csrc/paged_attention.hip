@@ -51,8 +51,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxSlots = 1024;       // row tiles a split launch can plan
 constexpr int kStreamBlock = 128;     // keys per step of stream_kernel: 32 per wavefront
-// Keys per step of tile_kernel: 32 where the output and the queries leave few registers.
-constexpr int tile_block(int d) { return 64; }
+constexpr int kTileBlock = 64;        // keys per step of tile_kernel: one 16-key group per wavefront
 // What cutting the key axis costs a tile_kernel launch, in key blocks: the extra prologues, the parts written and
 // joined take about 20 us, a block 0.8 to 2.6 us.  Tiles are kept whole where the longest workgroup's blocks are no
 // more than that above an even share: 1024 new tokens alone 45 us whole and 60 cut, over 32768 keys 970 whole
@@ -854,10 +853,10 @@ __device__ __forceinline__ void step() { __builtin_amdgcn_sched_barrier(0); }
 // cycles each) stand beside about 250 vector instructions, of which softmax's 32 scores a lane take 130 and the
 // staging of the next block 75.  A single wavefront issues a vector instruction every 8 cycles, two every 4 (measured),
 // so two wavefronts per SIMD are needed and everything that can goes between matrix instructions: staging into
-// the score product, exponentials into the second (837 -> 727 us for both).  64 rows a wavefront (RW = 2, half the
+// the score product, exponentials into the second (837 -> 727 us for both).  64 rows a wavefront (half the
 // LDS reads, one wavefront per SIMD) is slower: 814 us; so is output through LDS in whole rows (no gain, more
 // registers).  Head dim 256 has registers for one wavefront per SIMD only: 1674 us, 821 TFLOP/s.
-// Four wavefronts of RW blocks of 32 rows each; lane % 32 is the row, half = lane / 32.
+// Four wavefronts of 32 rows each; lane % 32 is the row, half = lane / 32.
 //   scores   S^T (32 keys x 32 rows): register i of a lane is key 8*(i/4) + 4*half + i%4
 //   LDS      K as bf16 [key][D] and V^T as fp16 or bf16 [D][64 keys], both double-buffered, in 16-byte
 //            chunks permuted within a row so that neighbouring rows fall on different banks.  The
@@ -868,20 +867,20 @@ struct Buffer {
   static constexpr int value = I;
 };
 
-template <int D, bool FP8, int RW>
-__global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_kernel(AttentionArgs a, Launch l) {
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void tile_kernel(AttentionArgs a, Launch l) {
   constexpr int E = FP8 ? 1 : 2;
-  constexpr int BM = 128 * RW, KB = tile_block(D);
+  constexpr int BM = 128, KB = kTileBlock;
   // With one wavefront per SIMD half of its 512 registers are accumulation registers, which only matrix
   // instructions and loads address: the output and the queries are kept there.
-  constexpr bool kAcc = RW * D > 128;
+  constexpr bool kAcc = D > 128;
   constexpr int ST = D / 16;                // matrix steps of a score
   constexpr int DB = D / 32;                // output tiles
   constexpr int CH = D * E / 16;            // 16-byte chunks of a cached key
-  constexpr int KW = KB / 4, NG = KB / 16;  // keys a wavefront brings in, 16-key groups of a block
-  constexpr int KL = KW * CH / 64;          // key loads per lane
+  constexpr int NG = KB / 16;               // 16-key groups of a block, each brought in by one wavefront
+  constexpr int KL = 16 * CH / 64;          // key loads per lane
   constexpr int VQ = D / 4;                 // channel quads
-  constexpr int VI = KW * VQ > 512 ? KW * VQ / 512 : 1;    // value items per lane: 8 keys x 4 channels
+  constexpr int VI = VQ > 32 ? VQ / 32 : 1; // value items per lane: 8 keys x 4 channels
   __shared__ __align__(16) uint16_t ks[2][KB * D];
   __shared__ __align__(16) uint16_t vt[2][D * KB];
   __shared__ int pre[kMaxSlots + 1];
@@ -889,7 +888,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
   __shared__ int bad_block[2];              // block whose values hold something non-finite
   __shared__ int no_page[2][NG];            // per 16 keys of a block
   constexpr int MW = D / 64;                // dwords of marks: a bit per output of a lane
-  __shared__ uint32_t marks[RW * 2 * MW][kThreads];
+  __shared__ uint32_t marks[2 * MW][kThreads];
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -900,37 +899,36 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     return key * D + ((ch ^ sw) & (N - 1)) * 8;
   };
   auto v_chunk = [](int d, int ch) {         // LDS offset of 8 keys of a channel
-    const int sw = KB == 64 ? ((d >> 1) & 7) ^ ((d >> 4) & 1) : (d >> 2) & 3;
+    const int sw = ((d >> 1) & 7) ^ ((d >> 4) & 1);
     return d * KB + ((ch ^ sw) & (KB / 8 - 1)) * 8;
   };
 
   const int v_quad = lane % VQ;
   // which 8 of its 16-key group a value item holds
-  auto v_grp = [&](int i) { return KW == 8 ? wave & 1 : (VI > 1 ? i : (lane / VQ) & 1); };
+  auto v_grp = [&](int i) { return VI > 1 ? i : (lane / VQ) & 1; };
 
   tile_pieces<BM, KB>(a, l, pre, wave_sum, [&](const Tile& t, int h, int b0, int b1, int partial) {
     const float c = a.scale_log2 * (FP8 ? a.k_scale[h * a.scale_stride] : 1.0f);
-    const int wrow = wave * 32 * RW;         // the wavefront's first row in the tile
+    const int wrow = wave * 32;              // the wavefront's first row in the tile
     const bool busy = wrow < t.rows;
-    u32x4_t q[RW][ST];
-    int lo[RW], hi[RW];
-#pragma unroll
-    for (int rw = 0; rw < RW; ++rw) {
-      const int r = t.row0 + wrow + rw * 32 + n;
-      row_range(a, t, r, lo[rw], hi[rw]);
-      const bool live = wrow + rw * 32 + n < t.rows;
+    u32x4_t q[ST];
+    int lo, hi;
+    {
+      const int r = t.row0 + wrow + n;
+      row_range(a, t, r, lo, hi);
+      const bool live = wrow + n < t.rows;
       const int tok = (int)fastdiv((uint32_t)r, a.div_group), g = r - tok * a.group;
       const uint16_t* x = a.q + (live ? (t.c0 + tok) * a.q_tok + (h * a.group + g) * a.q_head : 0);
 #pragma unroll
       for (int st = 0; st < ST; ++st) {
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(x + st * 16 + half * 8);
-        q[rw][st] = live ? w : u32x4_t{0, 0, 0, 0};
+        q[st] = live ? w : u32x4_t{0, 0, 0, 0};
       }
     }
     // keys every row of the wavefront sees, and keys any of them sees
     int w_first = 0, w_last = 0;
     if (busy) {
-      const int rl = wrow + 32 * RW < t.rows ? wrow + 32 * RW - 1 : t.rows - 1;
+      const int rl = wrow + 32 < t.rows ? wrow + 31 : t.rows - 1;
       w_first = (int)fastdiv((uint32_t)(t.row0 + wrow), a.div_group);
       w_last = (int)fastdiv((uint32_t)(t.row0 + rl), a.div_group);
     }
@@ -947,33 +945,26 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 
     if constexpr (kAcc) {
 #pragma unroll
-      for (int rw = 0; rw < RW; ++rw)
-#pragma unroll
-        for (int st = 0; st < ST; ++st) asm volatile("" : "+a"(q[rw][st]));
+      for (int st = 0; st < ST; ++st) asm volatile("" : "+a"(q[st]));
     }
-    f32x16_t o[RW][DB];
-    float m[RW], sum[RW];
+    f32x16_t o[DB];
+    float m = kLowest, sum = 0.0f;
 #pragma unroll
-    for (int rw = 0; rw < RW; ++rw) {
-      m[rw] = kLowest;
-      sum[rw] = 0.0f;
+    for (int i = 0; i < DB; ++i)
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) o[rw][i][x] = 0.0f;
-    }
+      for (int x = 0; x < 16; ++x) o[i][x] = 0.0f;
 
     const int64_t head_at = ((int64_t)h << a.page_shift) * (D * E);
     const int mask = (1 << a.page_shift) - 1;
     u32x4_t kr[KL];
     uint32_t vr[VI][8][E];                   // 4 channels of 8 keys
-    // Wavefront w brings in KW keys of a block, those of one 16-key group (or half of it) and so of one page: rows
-    // KW w .. of K, and of V the one or two sets of 8 keys that a 16-byte chunk of a V^T row holds.
-    const int my_group = wave * KW / 16;
+    // Wavefront w brings in the 16-key group w of a block, which lies in one page: rows 16 w .. of K, and of V the two
+    // sets of 8 keys that a 16-byte chunk of a V^T row holds.
+    const int my_group = wave;
     auto my_page = [&](int b) { return b < b1 ? page_of(a, t, (t.block0 + b) * KB + my_group * 16) : -1; };
     auto fetch = [&](int b, int p) {
       const int in = ((t.block0 + b) * KB + my_group * 16) & mask;
-      const uint8_t* kp = a.k + (p >= 0 ? p : 0) * a.k_page + head_at + (in + (wave * KW & 15)) * (D * E);
+      const uint8_t* kp = a.k + (p >= 0 ? p : 0) * a.k_page + head_at + in * (D * E);
       const uint8_t* vp = a.v + (p >= 0 ? p : 0) * a.v_page + head_at + in * (D * E);
 #pragma unroll
       for (int i = 0; i < KL; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(kp + (i * 64 + lane) * 16);
@@ -1008,7 +999,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
     };
     auto stage_unit = [&](int u, int buf) {
       if (u < NK) {
-        const int i = FP8 ? u / 2 : u, at = i * 64 + lane, key = wave * KW + at / CH, ch = at % CH;
+        const int i = FP8 ? u / 2 : u, at = i * 64 + lane, key = wave * 16 + at / CH, ch = at % CH;
         if (FP8) {
           const uint32_t lo = kr[i][(u & 1) * 2], hi = kr[i][(u & 1) * 2 + 1];
           *reinterpret_cast<u32x4_t*>(&ks[buf][k_chunk(key, 2 * ch + (u & 1))]) =
@@ -1085,31 +1076,27 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       if (uniform(bad_block[buf]) == b) {
         // Rare: mark this lane's outputs that see a non-finite value, by reading the block's values again.
         if (!marked)
-          for (int i = 0; i < RW * 2 * MW; ++i) marks[i][tid] = 0;
+          for (int i = 0; i < 2 * MW; ++i) marks[i][tid] = 0;
         marked = true;
 #pragma unroll 1
         for (int kk = 0; kk < KB; ++kk) {
           const int key = key0 + kk, pk = page_of(a, t, key);
           if (pk < 0) continue;
           const uint8_t* vp = a.v + pk * a.v_page + head_at + (key & mask) * (D * E) + half * (4 * E);
-          uint32_t seen = 0;
-#pragma unroll
-          for (int rw = 0; rw < RW; ++rw) seen |= (key >= lo[rw] && key < hi[rw] ? 1u : 0u) << rw;
+          const bool seen = key >= lo && key < hi;
 #pragma unroll 1
           for (int i = 0; i < D / 8 * E; ++i) {          // dwords of this lane's 4-channel groups, 8 channels apart
             constexpr int PER = FP8 ? 4 : 2;
             uint32_t up, down;
             non_finite_signs<FP8>(*reinterpret_cast<const uint32_t*>(vp + (i / E) * (8 * E) + (i % E) * 4), up, down);
             const int bit = i * PER;
-            for (int rw = 0; rw < RW; ++rw) {
-              if (!((seen >> rw) & 1)) continue;
-              marks[(rw * 2) * MW + (bit >> 5)][tid] |= up << (bit & 31);
-              marks[(rw * 2 + 1) * MW + (bit >> 5)][tid] |= down << (bit & 31);
-            }
+            if (!seen) continue;
+            marks[bit >> 5][tid] |= up << (bit & 31);
+            marks[MW + (bit >> 5)][tid] |= down << (bit & 31);
           }
         }
       }
-      f32x16_t s[RW][KB / 32];
+      f32x16_t s[KB / 32];
       {
         constexpr int AHEAD = 4, NS = KB / 32 * ST;
         u32x4_t f[AHEAD];
@@ -1123,13 +1110,10 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 #pragma unroll
         for (int x = 0; x < NS; ++x) {
           const u32x4_t ka = f[x % AHEAD];
+          f32x16_t z;
 #pragma unroll
-          for (int rw = 0; rw < RW; ++rw) {
-            f32x16_t z;
-#pragma unroll
-            for (int y = 0; y < 16; ++y) z[y] = 0.0f;
-            s[rw][x / ST] = mfma32_bf16(ka, q[rw][x % ST], x % ST == 0 ? z : s[rw][x / ST]);
-          }
+          for (int y = 0; y < 16; ++y) z[y] = 0.0f;
+          s[x / ST] = mfma32_bf16(ka, q[x % ST], x % ST == 0 ? z : s[x / ST]);
           if (x + AHEAD < NS) f[x % AHEAD] = read(x + AHEAD);
 #pragma unroll
           for (int u = x * NU / NS; u < (x + 1) * NU / NS; ++u) stage_unit(u, buf ^ 1);
@@ -1139,64 +1123,57 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       __builtin_amdgcn_s_setprio(0);
       stage_end(b + 1, buf ^ 1);
       if (b + 2 < b1) fetch(b + 2, p2);
-      u32x4_t pr[RW][NG] = {};
-      float mc[RW];
-#pragma unroll
-      for (int rw = 0; rw < RW; ++rw) {
-        if (partial_keys) {
-          asm volatile("");        // a branch, not selects paid by every block
-#pragma unroll
-          for (int kb = 0; kb < KB / 32; ++kb)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const int key = key0 + kb * 32 + 8 * (x >> 2) + 4 * half + (x & 3);
-              const bool seen = !((gone >> (kb * 2 + (x >> 3))) & 1) && key >= lo[rw] && key < hi[rw];
-              s[rw][kb][x] = seen ? s[rw][kb][x] : -__builtin_inff();
-            }
-        }
-        float mx = m[rw];
+      u32x4_t pr[NG] = {};
+      if (partial_keys) {
+        asm volatile("");        // a branch, not selects paid by every block
 #pragma unroll
         for (int kb = 0; kb < KB / 32; ++kb)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[rw][kb][x]);
-        mx = max_across_32(mx);
-        if (__builtin_amdgcn_ballot_w64((mx - m[rw]) * c > kLazy) != 0) {
-          const float f0 = rescale<FP8>(m[rw], mx, c);
-          m[rw] = mx;
-          sum[rw] *= f0;
-          // (kAcc: taken out of the accumulation registers here and not ahead of the branch)
-#pragma unroll
-          for (int i = 0; i < DB; ++i) {
-            if constexpr (kAcc) asm volatile("" : "+a"(o[rw][i]));
-            o[rw][i] *= f0;
-            if constexpr (kAcc) asm volatile("" : "+a"(o[rw][i]));
+          for (int x = 0; x < 16; ++x) {
+            const int key = key0 + kb * 32 + 8 * (x >> 2) + 4 * half + (x & 3);
+            const bool seen = !((gone >> (kb * 2 + (x >> 3))) & 1) && key >= lo && key < hi;
+            s[kb][x] = seen ? s[kb][x] : -__builtin_inff();
           }
-        }
-        mc[rw] = exponent_base<FP8>(m[rw], c);
-        if (far_scores(mc[rw])) {
-          asm volatile("");        // a branch, as above
-          const float from = m[rw] == kLowest ? 0.0f : m[rw];
+      }
+      float mx = m;
 #pragma unroll
-          for (int kb = 0; kb < KB / 32; ++kb)
+      for (int kb = 0; kb < KB / 32; ++kb)
 #pragma unroll
-            for (int x = 0; x < 16; ++x) s[rw][kb][x] -= from;
-          mc[rw] = -kLift<FP8>;
+        for (int x = 0; x < 16; ++x) mx = __builtin_fmaxf(mx, s[kb][x]);
+      mx = max_across_32(mx);
+      if (__builtin_amdgcn_ballot_w64((mx - m) * c > kLazy) != 0) {
+        const float f0 = rescale<FP8>(m, mx, c);
+        m = mx;
+        sum *= f0;
+        // (kAcc: taken out of the accumulation registers here and not ahead of the branch)
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          if constexpr (kAcc) asm volatile("" : "+a"(o[i]));
+          o[i] *= f0;
+          if constexpr (kAcc) asm volatile("" : "+a"(o[i]));
         }
+      }
+      float mc = exponent_base<FP8>(m, c);
+      if (far_scores(mc)) {
+        asm volatile("");        // a branch, as above
+        const float from = m == kLowest ? 0.0f : m;
+#pragma unroll
+        for (int kb = 0; kb < KB / 32; ++kb)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) s[kb][x] -= from;
+        mc = -kLift<FP8>;
       }
       // Exponentials of 8 keys (group g) and the product with V, a group behind.
       {
-        float p8[RW][8];
+        float p8[8];
         u32x4_t f[DB];
         auto read = [&](int g, int i) {
           return *reinterpret_cast<const u32x4_t*>(&vt[buf][v_chunk(i * 32 + n, g * 2 + half)]);
         };
         auto exps = [&](int g, int j) {
-#pragma unroll
-          for (int rw = 0; rw < RW; ++rw) {
-            p8[rw][j] = exp2_fast(__builtin_fmaf(s[rw][g >> 1][(g & 1) * 8 + j], c, -mc[rw]));
-            sum[rw] += p8[rw][j];
-            if (j & 1) pr[rw][g][j >> 1] = p_pair<FP8>(p8[rw][j - 1], p8[rw][j]);
-          }
+          p8[j] = exp2_fast(__builtin_fmaf(s[g >> 1][(g & 1) * 8 + j], c, -mc));
+          sum += p8[j];
+          if (j & 1) pr[g][j >> 1] = p_pair<FP8>(p8[j - 1], p8[j]);
         };
 #pragma unroll
         for (int i = 0; i < DB; ++i) f[i] = read(0, i);
@@ -1209,8 +1186,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 #pragma unroll
           for (int i = 0; i < DB; ++i) {
             const u32x4_t va = f[i];
-#pragma unroll
-            for (int rw = 0; rw < RW; ++rw) o[rw][i] = mfma32_pv<FP8>(va, pr[rw][g], o[rw][i]);
+            o[i] = mfma32_pv<FP8>(va, pr[g], o[i]);
             if (g + 1 < NG) {
               f[i] = read(g + 1, i);
 #pragma unroll
@@ -1222,9 +1198,7 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
       }
       if constexpr (kAcc) {
 #pragma unroll
-        for (int rw = 0; rw < RW; ++rw)
-#pragma unroll
-          for (int i = 0; i < DB; ++i) asm volatile("" : "+a"(o[rw][i]));
+        for (int i = 0; i < DB; ++i) asm volatile("" : "+a"(o[i]));
       }
     };
 
@@ -1253,46 +1227,40 @@ __global__ __launch_bounds__(kThreads, RW == 1 && D <= 128 ? 2 : 1) void tile_ke
 
     if (marked) {
 #pragma unroll
-      for (int rw = 0; rw < RW; ++rw)
+      for (int i = 0; i < DB; ++i)
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int bit = i * 16 + x;
-            o[rw][i][x] += non_finite_part((marks[(rw * 2) * MW + (bit >> 5)][tid] >> (bit & 31)) & 1,
-                                           (marks[(rw * 2 + 1) * MW + (bit >> 5)][tid] >> (bit & 31)) & 1);
-          }
+        for (int x = 0; x < 16; ++x) {
+          const int bit = i * 16 + x;
+          o[i][x] += non_finite_part((marks[bit >> 5][tid] >> (bit & 31)) & 1, (marks[MW + (bit >> 5)][tid] >> (bit & 31)) & 1);
+        }
     }
     const float vs = FP8 ? a.v_scale[h * a.scale_stride] : 1.0f;
+    const float ll = sum + __shfl_xor(sum, 32, 64);
+    const float mm = scaled_max<FP8>(m, c, ll);
+    const int tr = wrow + n;
+    if (tr >= t.rows) return;
+    if (partial >= 0) {
+      const int64_t at = (int64_t)partial * BM + tr;
+      if (half == 0) l.ml[at] = make_float2(mm, ll);
 #pragma unroll
-    for (int rw = 0; rw < RW; ++rw) {
-      const float ll = sum[rw] + __shfl_xor(sum[rw], 32, 64);
-      const float mm = scaled_max<FP8>(m[rw], c, ll);
-      const int tr = wrow + rw * 32 + n;
-      if (tr >= t.rows) continue;
-      if (partial >= 0) {
-        const int64_t at = (int64_t)partial * BM + tr;
-        if (half == 0) l.ml[at] = make_float2(mm, ll);
+      for (int i = 0; i < DB; ++i)
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<float4*>(l.po + at * D + i * 32 + 8 * x + 4 * half) =
+              make_float4(o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]);
+    } else {
+      const int r = t.row0 + tr;
+      const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
+      const float f = vs / ll;
+      uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<float4*>(l.po + at * D + i * 32 + 8 * x + 4 * half) =
-                make_float4(o[rw][i][4 * x], o[rw][i][4 * x + 1], o[rw][i][4 * x + 2], o[rw][i][4 * x + 3]);
-      } else {
-        const int r = t.row0 + tr;
-        const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-        const float f = vs / ll;
-        uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head;
+      for (int i = 0; i < DB; ++i)
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint2*>(y + i * 32 + 8 * x + 4 * half) =
-                make_uint2(bf16_pair(normalised(o[rw][i][4 * x], ll, f), normalised(o[rw][i][4 * x + 1], ll, f)),
-                           bf16_pair(normalised(o[rw][i][4 * x + 2], ll, f), normalised(o[rw][i][4 * x + 3], ll, f)));
-        if (a.lse && half == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
-      }
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<uint2*>(y + i * 32 + 8 * x + 4 * half) =
+              make_uint2(bf16_pair(normalised(o[i][4 * x], ll, f), normalised(o[i][4 * x + 1], ll, f)),
+                         bf16_pair(normalised(o[i][4 * x + 2], ll, f), normalised(o[i][4 * x + 3], ll, f)));
+      if (a.lse && half == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
     }
   });
 }
@@ -1502,7 +1470,7 @@ int launch_dim(const AttentionArgs& a, const Choices& c, void* workspace, hipStr
         : launch_one<D, 32, kStreamBlock, true>(stream_kernel<D, FP8, 2>, a, c.stream, 2, workspace, stream);
     if (st != NVFP4_OK) return st;
   }
-  if (c.tile.used) return launch_one<D, 128, tile_block(D), false>(tile_kernel<D, FP8, 1>, a, c.tile, 256 / tile_block(D), workspace, stream);
+  if (c.tile.used) return launch_one<D, 128, kTileBlock, false>(tile_kernel<D, FP8>, a, c.tile, 256 / kTileBlock, workspace, stream);
   return NVFP4_OK;
 }
 

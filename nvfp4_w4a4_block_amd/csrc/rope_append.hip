@@ -31,9 +31,6 @@ constexpr int kThreads = 256;
 template <typename XT>
 constexpr int kGroups = sizeof(XT) == 2 ? 2 : 1;
 
-__device__ __forceinline__ void load8(const uint16_t* x, float (&e)[8]) {
-  widen(*reinterpret_cast<const uint4*>(x), e, x);
-}
 __device__ __forceinline__ void load8(const float* x, float (&e)[8]) {
   const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
   e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
