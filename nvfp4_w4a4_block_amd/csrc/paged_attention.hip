@@ -474,11 +474,18 @@ __device__ __forceinline__ float non_finite_part(uint32_t up, uint32_t down) {
 }
 
 // A part's O times its weight, at most 1.  An infinite or NaN O (from such values, under positive probabilities) stays
-// what it is also where the weight underflows to 0: the answer does not depend on how the keys were divided.
+// what it is also where the weight underflows to 0: the answer does not depend on how the keys were divided.  Joins
+// multiply plainly (KEEP false) and are done again with KEEP where that gives a NaN, which is rare (selecting always: one
+// token over 4096 keys 12.8 us a captured call, so 12.1).
+template <bool KEEP>
 __device__ __forceinline__ float weighted(float o, float w) {
   const float x = o * w;
-  return x != x ? o : x;
+  return KEEP && x != x ? o : x;
 }
+template <bool KEEP>
+struct Keep {
+  static constexpr bool value = KEEP;
+};
 
 // O / l (f is v_scale / l).  A row whose sum is 0 has zeros, selected and not multiplied: its O may be infinite or NaN,
 // from values at keys whose scores are all -inf.
@@ -530,7 +537,9 @@ template <bool FP8>
 __device__ __forceinline__ float rescale(float m, float mx, float c) {
   return exp2_fast(m == kLowest ? __builtin_fminf(-exponent_base<FP8>(mx, c), 0.0f) : (m - mx) * c);
 }
-// Whether any row of the wavefront has to have its scores taken against the maximum first.
+// Whether any row of the wavefront has to have its scores taken against the maximum first.  Looked at in every block:
+// with a flag kept from the maximum's last change, or in one branch with the change, the compiler lays the loop out
+// twice and spills (8192 new tokens, head dim 128: 1030 and 985 us, so 753).
 __device__ __forceinline__ bool far_scores(float base) {
   return __builtin_amdgcn_ballot_w64(__builtin_fabsf(base) > kFar) != 0;
 }
@@ -811,12 +820,18 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
           w[v] = exp2_fast(merge_ml[v][row].x - mm);
           ll += merge_ml[v][row].y * w[v];
         }
+        auto join = [&](auto keep) {
+          float all = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          e[i] = 0.0f;
+          for (int i = 0; i < NT; ++i) {
+            e[i] = 0.0f;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) e[i] += weighted(merge[v][row][d + i], w[v]);
-        }
+            for (int v = 0; v < 4; ++v) e[i] += weighted<decltype(keep)::value>(merge[v][row][d + i], w[v]);
+            all += e[i];
+          }
+          return all != all;
+        };
+        if (join(Keep<false>{})) join(Keep<true>{});
         if (partial >= 0) {
           const int64_t at = (int64_t)partial * BM + rb * 16 + row;
           if (d == 0) l.ml[at] = make_float2(mm, ll);
@@ -1304,9 +1319,29 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
   for (int row0 = (blockIdx.x % l.rows_grid) * ROWS; row0 < t.rows; row0 += l.rows_grid * ROWS) {
     const int row = row0 + g / PARTS;
     const bool live = row < t.rows;
-    float m = kLowest, sum = 0.0f;
-    float4 acc = make_float4(0, 0, 0, 0);
-    if (live) {
+    float m, sum;
+    float4 acc;
+    auto start = [&](float2 ml, float4 v) {
+      m = ml.x;
+      sum = ml.y;
+      acc = v;
+    };
+    auto add = [&](auto keep, float2 ml, float4 v) {
+      constexpr bool KEEP = decltype(keep)::value;
+      const float mx = __builtin_fmaxf(m, ml.x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml.x - mx);
+      m = mx;
+      sum = sum * f0 + ml.y * f1;
+      acc.x = weighted<KEEP>(acc.x, f0) + weighted<KEEP>(v.x, f1);
+      acc.y = weighted<KEEP>(acc.y, f0) + weighted<KEEP>(v.y, f1);
+      acc.z = weighted<KEEP>(acc.z, f0) + weighted<KEEP>(v.z, f1);
+      acc.w = weighted<KEEP>(acc.w, f0) + weighted<KEEP>(v.w, f1);
+    };
+    auto has_nan = [&] {
+      const float x4 = acc.x + acc.y + acc.z + acc.w;
+      return x4 != x4;
+    };
+    auto lane_parts = [&](auto keep) {
+      start(make_float2(kLowest, 0.0f), make_float4(0, 0, 0, 0));
       for (int w = w0 + pg; w <= w1; w += 4 * PARTS) {
         float2 ml[4];
         float4 v[4];
@@ -1316,38 +1351,31 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
           const int64_t at = (wi == w0 ? first : 2 * (int64_t)(wi <= w1 ? wi : w1)) * BM + row;
           ml[i] = l.ml[at];
           v[i] = *reinterpret_cast<const float4*>(l.po + at * D + x * 4);
-          if (wi > w1) ml[i] = make_float2(kLowest, 0.0f);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (w + i * PARTS > w1) continue;
-          const float mx = __builtin_fmaxf(m, ml[i].x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml[i].x - mx);
-          m = mx;
-          sum = sum * f0 + ml[i].y * f1;
-          acc.x = weighted(acc.x, f0) + weighted(v[i].x, f1);
-          acc.y = weighted(acc.y, f0) + weighted(v[i].y, f1);
-          acc.z = weighted(acc.z, f0) + weighted(v[i].z, f1);
-          acc.w = weighted(acc.w, f0) + weighted(v[i].w, f1);
+          add(keep, ml[i], v[i]);
         }
       }
-    }
+      return has_nan();
+    };
+    if (!live)
+      start(make_float2(kLowest, 0.0f), make_float4(0, 0, 0, 0));
+    else if (lane_parts(Keep<false>{}))
+      lane_parts(Keep<true>{});
     if (PARTS > 1) {
       __syncthreads();
       part[g][x] = acc;
       if (x == 0) part_ml[g] = make_float2(m, sum);
       __syncthreads();
       if (pg != 0) continue;
-      for (int i = 1; i < PARTS; ++i) {
-        const float2 ml = part_ml[g + i];
-        const float4 v = part[g + i][x];
-        const float mx = __builtin_fmaxf(m, ml.x), f0 = exp2_fast(m - mx), f1 = exp2_fast(ml.x - mx);
-        m = mx;
-        sum = sum * f0 + ml.y * f1;
-        acc.x = weighted(acc.x, f0) + weighted(v.x, f1);
-        acc.y = weighted(acc.y, f0) + weighted(v.y, f1);
-        acc.z = weighted(acc.z, f0) + weighted(v.z, f1);
-        acc.w = weighted(acc.w, f0) + weighted(v.w, f1);
-      }
+      auto group_parts = [&](auto keep) {
+        start(part_ml[g], part[g][x]);
+        for (int i = 1; i < PARTS; ++i) add(keep, part_ml[g + i], part[g + i][x]);
+        return has_nan();
+      };
+      if (group_parts(Keep<false>{})) group_parts(Keep<true>{});
     }
     if (!live) continue;
     const float vs = a.v_scale ? a.v_scale[h * a.scale_stride] : 1.0f;
