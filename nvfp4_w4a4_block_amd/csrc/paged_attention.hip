@@ -487,9 +487,9 @@ struct Keep {
   static constexpr bool value = KEEP;
 };
 
-// O / l (f is v_scale / l).  A row whose sum is 0 has zeros, selected and not multiplied: its O may be infinite or NaN,
-// from values at keys whose scores are all -inf.
-__device__ __forceinline__ float normalised(float o, float l, float f) { return l == 0.0f ? 0.0f : o * f; }
+// O / l v_scale (f is 1 / l; v_scale / l could underflow where the product does not).  A row whose sum is 0 has zeros,
+// selected and not multiplied: its O may be infinite or NaN, from values at keys whose scores are all -inf.
+__device__ __forceinline__ float normalised(float o, float l, float f, float vs) { return l == 0.0f ? 0.0f : o * f * vs; }
 
 template <int W>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -841,13 +841,13 @@ __global__ __launch_bounds__(kThreads, stream_waves(D, FP8, RB)) void stream_ker
         } else {
           const int r = t.row0 + rb * 16 + row;
           const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-          const float f = vs / ll;
+          const float f = 1.0f / ll;
           uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + d;
 #pragma unroll
           for (int i = 0; i < NT; i += 4)
             *reinterpret_cast<uint2*>(y + i) =
-                make_uint2(bf16_pair(normalised(e[i], ll, f), normalised(e[i + 1], ll, f)),
-                           bf16_pair(normalised(e[i + 2], ll, f), normalised(e[i + 3], ll, f)));
+                make_uint2(bf16_pair(normalised(e[i], ll, f, vs), normalised(e[i + 1], ll, f, vs)),
+                           bf16_pair(normalised(e[i + 2], ll, f, vs), normalised(e[i + 3], ll, f, vs)));
           if (a.lse && d == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
         }
       }
@@ -1266,15 +1266,15 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void tile_kernel(Attent
     } else {
       const int r = t.row0 + tr;
       const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-      const float f = vs / ll;
+      const float f = 1.0f / ll;
       uint16_t* y = a.out + (t.c0 + tok) * a.o_tok + head * a.o_head;
 #pragma unroll
       for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           *reinterpret_cast<uint2*>(y + i * 32 + 8 * x + 4 * half) =
-              make_uint2(bf16_pair(normalised(o[i][4 * x], ll, f), normalised(o[i][4 * x + 1], ll, f)),
-                         bf16_pair(normalised(o[i][4 * x + 2], ll, f), normalised(o[i][4 * x + 3], ll, f)));
+              make_uint2(bf16_pair(normalised(o[i][4 * x], ll, f, vs), normalised(o[i][4 * x + 1], ll, f, vs)),
+                         bf16_pair(normalised(o[i][4 * x + 2], ll, f, vs), normalised(o[i][4 * x + 3], ll, f, vs)));
       if (a.lse && half == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (mm + __builtin_log2f(ll)) * kLn2;
     }
   });
@@ -1381,10 +1381,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttentionArgs a, Laun
     const float vs = a.v_scale ? a.v_scale[h * a.scale_stride] : 1.0f;
     const int r = t.row0 + row;
     const int tok = (int)fastdiv((uint32_t)r, a.div_group), head = h * a.group + r - tok * a.group;
-    const float f = vs / sum;
+    const float f = 1.0f / sum;
     *reinterpret_cast<uint2*>(a.out + (t.c0 + tok) * a.o_tok + head * a.o_head + x * 4) =
-        make_uint2(bf16_pair(normalised(acc.x, sum, f), normalised(acc.y, sum, f)),
-                   bf16_pair(normalised(acc.z, sum, f), normalised(acc.w, sum, f)));
+        make_uint2(bf16_pair(normalised(acc.x, sum, f, vs), normalised(acc.y, sum, f, vs)),
+                   bf16_pair(normalised(acc.z, sum, f, vs), normalised(acc.w, sum, f, vs)));
     if (a.lse && x == 0) a.lse[(int64_t)(t.c0 + tok) * a.q_heads + head] = (m + __builtin_log2f(sum)) * kLn2;
   }
 }

@@ -142,3 +142,22 @@ def test_values_near_the_largest_bf16(n, L):
     out, _ = run(b, scale=1.0)
     assert torch.isfinite(want).all()
     assert_close(out, want, tol)
+
+
+@pytest.mark.parametrize("n,L", [(1, 100), (2, 5000), (100, 600), (300, 9000)])
+@pytest.mark.parametrize("v_scale", [1e-39, 3e-37, 1e36])
+def test_value_scales_of_every_size(n, L, v_scale):
+    # values of 256 to 448, all positive, so the bound of the helpers' derivation is relative: 2^-8 for the output, 2^-11 for
+    # the probabilities, 2 L u for the two sums and 2^-18 for scores and exponentials (scores here are below 40)
+    b = Batch([n], [L], 10, 2, 128, True, seed=L)
+    b.v = torch.randint(0x78, 0x7F, b.v.shape, generator=b.g, dtype=torch.uint8)
+    b.vs = torch.full((1,), v_scale)
+    want = b.attention()[0]
+    tol = want * (2.0 ** -8 + 2.0 ** -11 + L * 2.0 ** -23 + 2.0 ** -18)
+    out, _ = run(b)
+    # 448e36 passes bf16's largest, 2^128 - 2^120, and what is half a step above that rounds to inf: a mean whose
+    # whole tolerance lies there is inf, one whose tolerance reaches across may be
+    edge = 2.0 ** 128 - 2.0 ** 119
+    may = (want - tol < edge) & (want + tol >= edge)
+    want = torch.where((want - tol >= edge) | (may & torch.isinf(out)), math.inf, want)
+    assert_close(out, want, tol)
