@@ -147,13 +147,14 @@ def test_values_near_the_largest_bf16(n, L):
 @pytest.mark.parametrize("n,L", [(1, 100), (2, 5000), (100, 600), (300, 9000)])
 @pytest.mark.parametrize("v_scale", [1e-39, 3e-37, 1e36])
 def test_value_scales_of_every_size(n, L, v_scale):
-    # values of 256 to 448, all positive, so the bound of the helpers' derivation is relative: 2^-8 for the output, 2^-11 for
-    # the probabilities, 2 L u for the two sums and 2^-18 for scores and exponentials (scores here are below 40)
+    # values of 256 to 448; the bound is that of a scale of 1, in units of the scale (outputs and their tolerance
+    # are normal numbers of bf16)
     b = Batch([n], [L], 10, 2, 128, True, seed=L)
     b.v = torch.randint(0x78, 0x7F, b.v.shape, generator=b.g, dtype=torch.uint8)
+    b.vs = torch.ones(1)
+    want, _, tol, _ = b.attention()
     b.vs = torch.full((1,), v_scale)
-    want = b.attention()[0]
-    tol = want * (2.0 ** -8 + 2.0 ** -11 + L * 2.0 ** -23 + 2.0 ** -18)
+    want, tol = want * float(b.vs), tol * float(b.vs)
     out, _ = run(b)
     # 448e36 passes bf16's largest, 2^128 - 2^120, and what is half a step above that rounds to inf: a mean whose
     # whole tolerance lies there is inf, one whose tolerance reaches across may be
