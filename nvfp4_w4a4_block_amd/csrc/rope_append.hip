@@ -74,6 +74,23 @@ __device__ __forceinline__ HeadsView pick(int kind, const HeadsView& q, const He
                    kind == 0 ? q.head : (kind == 1 ? k.head : v.head), kind == 0 ? q.heads : (kind == 1 ? k.heads : v.heads)};
 }
 
+// 1 / sqrt(v) as hi + lo: one Newton step from the hardware's reciprocal root, its residual 1 - v r^2 in twice the
+// precision, kept in two parts, so that x hi + x lo is rounded once.  (Root and quotient each rounded were less exact
+// than the formula step by step: 5.8e-8 against 5.4e-8 of fp32 norms and rotations, this 4.7e-8.)  v outside the range
+// where nothing in the step overflows or loses bits (0 and infinite among it) takes the root and quotient themselves.
+__device__ __forceinline__ void reciprocal_root(float v, float& hi, float& lo) {
+  if (v >= 0x1p-90f && v <= 0x1p90f) {
+    const float r = __builtin_amdgcn_rsqf(v), t = v * r;
+    const float e = __builtin_fmaf(-__builtin_fmaf(v, r, -t), r, __builtin_fmaf(-t, r, 1.0f));
+    const float d = 0.5f * r * e;
+    hi = r + d;
+    lo = d - (hi - r);
+  } else {
+    hi = 1.0f / __builtin_sqrtf(v);
+    lo = 0.0f;
+  }
+}
+
 __device__ __forceinline__ FastQuotient quotient_of(float s) { return FastQuotient{s, 1.0f / s, 440.0f * s}; }
 
 // LPR lanes per head vector (power of two), U groups per wavefront, XT the input type, APPEND: keys and values go
@@ -170,9 +187,10 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeAppendArgs a)
 #pragma unroll
         for (int m = 1; m < LPR; m *= 2) sum += __shfl_xor(sum, m, 64);
         if (live[u]) {
-          const float r = 1.0f / __builtin_sqrtf(sum / (float)a.dim + a.eps);
+          float r, r_lo;
+          reciprocal_root(sum / (float)a.dim + a.eps, r, r_lo);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = v[i] * r * g[i];
+          for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], r, v[i] * r_lo) * g[i];
         }
       }
       if (a.table) {
