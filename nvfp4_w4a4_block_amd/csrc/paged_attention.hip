@@ -53,9 +53,11 @@ constexpr int kMaxSlots = 1024;       // row tiles a split launch can plan
 constexpr int kStreamBlock = 128;     // keys per step of stream_kernel: 32 per wavefront
 constexpr int kTileBlock = 64;        // keys per step of tile_kernel: one 16-key group per wavefront
 // What cutting the key axis costs a tile_kernel launch, in key blocks: the extra prologues, the parts written and
-// joined take about 20 us, a block 0.8 to 2.6 us.  Tiles are kept whole where the longest workgroup's blocks are no
-// more than that above an even share: 1024 new tokens alone 45 us whole and 60 cut, over 32768 keys 970 whole
-// and 760 cut.
+// joined take about 20 us, a block 0.8 to 2.6 us.  Tiles are kept whole where the blocks of a workgroup, by the mean over
+// the launch's slots, are no more than that above an even share: 1024 new tokens alone 45 us whole and 60 cut, over
+// 32768 keys 970 whole and 760 cut.  The mean counts empty slots and says nothing of the longest tile: 4 chunks of 300
+// tokens among 17 sequences (head dim 256, window 2048) stay whole with a longest tile of 34 blocks against an even
+// share of 13, 114 us.
 constexpr int kCutCost = 16;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
@@ -546,14 +548,16 @@ __device__ __forceinline__ bool far_scores(float base) {
 
 // ---- few rows ----------------------------------------------------------------------------------------
 
-// Wavefronts per SIMD of the instances, as their registers (queries, O, one block of K and of V) allow.
+// Wavefronts per SIMD of the instances, by an estimate of their registers (queries, O, one block of K and of V).  It is a
+// little low for two: <64, E4M3, 2 row blocks> at 128 registers and <256, bf16, 2> at 512 keep 52 and 40 bytes a lane in
+// scratch.
 constexpr int stream_waves(int d, bool fp8, int rb) {
   const int regs = rb * (d / 8 + d / 4) + d / 4 * (fp8 ? 1 : 2) + 64;
   return regs <= 128 ? 4 : (regs <= 168 ? 3 : (regs <= 256 ? 2 : 1));
 }
 
-// HBM-bound: 2.2 GB of E4M3 cache in 375 us (5.8 TB/s, above what a copy reaches), 143 MB of bf16 cache in 30 us
-// (4.8 TB/s).  Registers, not LDS, hold the operands because no wavefront shares keys with another; one block of K
+// HBM-bound: 2.2 GB of E4M3 cache in 397 us (379 to 401; 5.5 TB/s, where a plain streaming read of as much reaches 6.3),
+// 143 MB of bf16 cache in 31 us (4.7 TB/s).  Registers, not LDS, hold the operands because no wavefront shares keys with another; one block of K
 // and one of V in flight per wavefront at three wavefronts per SIMD cover the latency (two blocks at two
 // wavefronts: 493 us).  Page numbers come through scalar loads: as vector loads they waited for the keys and values in
 // flight (480 us).
@@ -863,14 +867,16 @@ __device__ __forceinline__ void step() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---- many rows ---------------------------------------------------------------------------------------
 
-// MFMA-bound in principle, by the vector instructions beside it in fact: 8192 new tokens of 40 heads of 128 in 722 to
-// 770 us (890 to 950 TFLOP/s; a large bf16 library product reaches 1215 here).  Per wavefront and block 32 matrix instructions (32
-// cycles each) stand beside about 250 vector instructions, of which softmax's 32 scores a lane take 130 and the
-// staging of the next block 75.  A single wavefront issues a vector instruction every 8 cycles, two every 4 (measured),
-// so two wavefronts per SIMD are needed and everything that can goes between matrix instructions: staging into
-// the score product, exponentials into the second (837 -> 727 us for both).  64 rows a wavefront (half the
-// LDS reads, one wavefront per SIMD) is slower: 814 us; so is output through LDS in whole rows (no gain, more
-// registers).  Head dim 256 has registers for one wavefront per SIMD only: 1674 us, 821 TFLOP/s.
+// MFMA-bound in principle; in fact neither pipe is full: 8192 new tokens of 40 heads of 128 in 745 to 800 us over
+// several runs (860 to 920 TFLOP/s; an 8192^3 bf16 library product reaches 1410 here), the matrix pipe busy 42 % of
+// the time, vector instructions about as much.  A bf16 cache 805 to 830 us (its instance keeps 52 bytes a lane in
+// scratch).  Per wavefront and block 32 matrix instructions (32 cycles each) stand beside about 250 vector instructions,
+// of which softmax's 32 scores a lane take 130 and the staging of the next block 75.  A single wavefront issues a
+// vector instruction every 8 cycles, two every 4 (measured), so two wavefronts per SIMD are needed and everything that
+// can goes between matrix instructions: staging into the score product, exponentials into the second (837 -> 727 us for
+// both).  64 rows a wavefront (half the LDS reads, one wavefront per SIMD) is slower: 814 us; so is output through LDS
+// in whole rows (no gain, more registers).  Head dim 256 has registers for one wavefront per SIMD only: 1710 us, 804
+// TFLOP/s.
 // Four wavefronts of 32 rows each; lane % 32 is the row, half = lane / 32.
 //   scores   S^T (32 keys x 32 rows): register i of a lane is key 8*(i/4) + 4*half + i%4
 //   LDS      K as bf16 [key][D] and V^T as fp16 or bf16 [D][64 keys], both double-buffered, in 16-byte
@@ -1490,8 +1496,8 @@ int launch_one(Kernel kernel, const AttentionArgs& a, const Choice& c, int min_b
 
 template <int D, bool FP8>
 int launch_dim(const AttentionArgs& a, const Choices& c, void* workspace, hipStream_t stream) {
-  // smallest shares: 2 blocks of 128 keys (one token over 4096 keys 12.0 us, 1 block 11.2, 4 blocks 13.4; over
-  // 16384 keys 17.6, 22.7 and 17.0) and 4 of 64 keys
+  // smallest shares: 2 blocks of 128 keys (a captured call of one token over 4096 keys 12.1 us, 1 block 11.2, 4 blocks
+  // 13.4; over 16384 keys 17.6, 22.7 and 17.0) and 4 of 64 keys
   if (c.stream.used) {
     const int st = c.stream.bm == 16
         ? launch_one<D, 16, kStreamBlock, true>(stream_kernel<D, FP8, 1>, a, c.stream, 2, workspace, stream)

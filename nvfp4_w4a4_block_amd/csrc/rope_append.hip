@@ -14,8 +14,8 @@
 // looked up once, all loads go out first, and a lane's angles serve every group (its channels are the same in
 // all).  The partner channel of the half-split rotation is R / 16 lanes away (one cross-lane read per
 // channel); interleaved pairs lie in the lane.  The sum of squares is a butterfly over the vector's lanes.
-// Measured: norms and rotation of 8192 tokens of 48 heads of 128 in 44 us (4.7 TB/s; a copy reaches 5.1), with values
-// and an E4M3 cache in 57 us (3.9 TB/s, limited by the wavefronts in flight: their lookups come before their
+// Measured: norms and rotation of 8192 tokens of 48 heads of 128 in 44 us (4.7 TB/s; a copy reaches 5.0), with values
+// and an E4M3 cache in 56 to 59 us (3.8 to 4.0 TB/s, limited by the wavefronts in flight: their lookups come before their
 // compute).  Two groups a wavefront; four cost occupancy (60 to 63 us), one repeats the lookups (24 against 22 us for
 // 4096 tokens).
 #include "fp8_device.h"
