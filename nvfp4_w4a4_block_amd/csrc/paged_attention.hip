@@ -15,7 +15,7 @@
 //
 // Operands of the matrix instructions.  E4M3 values are exact in bf16 and in fp16.  Scores: bf16 queries
 // (as given) times bf16 keys, exact products.  Output: probabilities are rounded to fp16 next to fp16
-// values for an E4M3 cache (2^-12 relative), to bf16 for a bf16 cache, whose values may exceed
+// values for an E4M3 cache (2^-11 relative), to bf16 for a bf16 cache (2^-8), whose values may exceed
 // fp16's range.
 //
 // The matrix products are taken transposed, S^T = K Q^T and O^T = V^T P^T: a lane then holds scores of
@@ -557,10 +557,10 @@ constexpr int stream_waves(int d, bool fp8, int rb) {
 }
 
 // HBM-bound: 2.2 GB of E4M3 cache in 397 us (379 to 401; 5.5 TB/s, where a plain streaming read of as much reaches 6.3),
-// 143 MB of bf16 cache in 31 us (4.7 TB/s).  Registers, not LDS, hold the operands because no wavefront shares keys with another; one block of K
-// and one of V in flight per wavefront at three wavefronts per SIMD cover the latency (two blocks at two
-// wavefronts: 493 us).  Page numbers come through scalar loads: as vector loads they waited for the keys and values in
-// flight (480 us).
+// 143 MB of bf16 cache in 31 us (4.7 TB/s).  Registers, not LDS, hold the operands because no wavefront shares keys
+// with another; one block of K and one of V in flight per wavefront at three wavefronts per SIMD cover the latency (two
+// blocks at two wavefronts: 493 us).  Page numbers come through scalar loads: as vector loads they waited for the keys
+// and values in flight (480 us).
 // RB blocks of 16 rows; lane n = lane % 16 is the row, quarter = lane / 16.
 //   scores   S^T[g] (16 keys x 16 rows): lane holds keys g*16 + quarter*4 + i of its row
 //   K        A operand, lane = key, quarter = slice of the channels: 16 B loads, two matrix steps each
