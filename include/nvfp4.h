@@ -21,7 +21,11 @@
  *      inside the GEMM kernel;
  *  10. the attention half of the hybrid model around the key-value cache: per-head norms of
  *      queries and keys with the position rotation, appending keys and values to a paged cache
- *      (FP8 as in 5, or bf16), and attention of new tokens over that cache.
+ *      (FP8 as in 5, or bf16), and attention of new tokens over that cache;
+ *  11. the recurrent half behind the projection of 6: the causal convolution, the gated delta rule over
+ *      any mix of prompts and single tokens, and the gated norm behind it;
+ *  12. the residual's addition with a root-mean-square norm, the output quantized on the way for the
+ *      next linear layer.
  *
  * Sources: the element format (E2M1 values, one E4M3 scale per 16-element block) is from
  * "NVFP4 W4A4 Quantization Compresses 27B Hybrid Models" (thevalue.engineering), section
@@ -517,6 +521,125 @@ int nvfp4_paged_attention(const nvfp4_paged_kv* kv, int64_t tokens, int64_t max_
  * results of a key axis split over workgroups.  0 for bad sizes. */
 size_t nvfp4_paged_attention_workspace_size(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t q_heads,
                                             int64_t kv_heads, int64_t head_dim, int dtype);
+
+/*
+ * Operators between the 4-bit linears: norms whose output leaves quantized, and the recurrent half of
+ * the hybrid model (Gated DeltaNet: convolution, gated delta rule, gated norm).
+ */
+
+typedef enum {
+  NVFP4_NORM_PLAIN = 0, /* y only                                                                 */
+  NVFP4_NORM_NVFP4 = 1, /* NVFP4: codes [rows, cols/2], block_scales [rows, cols/16], scale        */
+  NVFP4_NORM_FP8 = 2    /* FP8: E4M3 bytes [rows, cols], scale; value = E4M3(byte) * scale         */
+} nvfp4_norm_format;
+
+/* What a norm writes of its rows y (host struct; device pointers).
+ *   y            [rows, ldy] of y_dtype (NVFP4_BF16: round to nearest even, or NVFP4_F32), or NULL if a
+ *                format is given; 16-byte aligned, ldy * element size a multiple of 16 bytes.
+ *   format       nvfp4_norm_format, of fl32(y).  codes 16-byte aligned.
+ *   mode         NVFP4_SCALE_PER_ROW: scale[rows] is written, max|y| / 2688 (NVFP4) or max|y| / 448 (FP8) of each
+ *                row; a row of zeros has scale 0 and codes of zero.  NVFP4_SCALE_GIVEN: scale[0] is read, finite
+ *                and > 0.  NVFP4 codes and scales are those nvfp4_quantize gives in that mode, FP8 bytes those
+ *                of nvfp4_fp8_kv_quantize. */
+typedef struct {
+  void* y;
+  int64_t ldy;
+  uint8_t* codes;
+  uint8_t* block_scales;
+  float* scale;
+  int32_t y_dtype;
+  int32_t format;
+  int32_t mode;
+} nvfp4_norm_out;
+
+/*
+ * Residual addition and root-mean-square norm over rows, quantized for the next linear layer:
+ *   r' = x + residual in fp32, rounded to the residual's type;  y = r' * w / sqrt(mean(r'^2) + eps)
+ * (r' = x without a residual).  From r' on in 64 bits, y rounded to fp32 once: the codes do not depend on the
+ * order of a sum.
+ *   rows >= 0 (0 is a no-op), at most 2^21 - 1; cols a multiple of 16, 16 to 32768.
+ *   x, residual  [rows, ldx / ldr], NVFP4_BF16 or NVFP4_F32 each; residual may be NULL.
+ *   weight       device fp32 [cols]; eps >= 0.
+ *   residual_out r', of the residual's type, or NULL; may be the residual itself, or x if type and pitch are
+ *                equal, and must not overlap the inputs otherwise.  out->y likewise.
+ *   Pointers 16-byte aligned, pitches times the element size multiples of 16 bytes.
+ */
+int nvfp4_add_rms_norm(int64_t rows, int64_t cols, const void* x, int x_dtype, int64_t ldx, const void* residual,
+                       int residual_dtype, int64_t ldr, const float* weight, float eps, void* residual_out, int64_t ldro,
+                       const nvfp4_norm_out* out, void* stream);
+
+/*
+ * Norm of each head vector times its output gate, the rows of all heads quantized for the next linear:
+ *   y[t, h] = x[t, h] * w / sqrt(mean(x[t, h]^2) + eps) * z[t, h] * sigmoid(z[t, h])
+ * in fp32, or with a quantized output in 64 bits, y rounded to fp32 once.
+ *   head_dim     a power of two, 16 to 1024; heads * head_dim at most 32768 (the cols of the outputs).
+ *   x, z         NVFP4_BF16 or NVFP4_F32 each; weight device fp32 [head_dim]; eps >= 0.
+ *   tokens >= 0 (0 is a no-op), at most 2^21 - 1.  The outputs must not overlap the inputs.
+ */
+int nvfp4_gated_rms_norm(int64_t tokens, int64_t head_dim, const nvfp4_heads* x, int x_dtype, const nvfp4_heads* z, int z_dtype,
+                         const float* weight, float eps, const nvfp4_norm_out* out, void* stream);
+
+/* A pool of per-sequence states and the batch of sequences that uses it (host struct; device pointers).
+ *   data         slot i's state at data + i * slot_stride elements, contiguous; 16-byte aligned, slot_stride
+ *                times the element size a multiple of 16 bytes.
+ *   slots        int32 [num_seqs]: the slot of each sequence, or NULL (sequence s uses slot s).  A slot outside
+ *                [0, num_slots) is none: such a sequence starts from zeros and leaves no state.  No two
+ *                sequences with new tokens may share a slot.
+ *   cu_q         int32 [num_seqs + 1], as in nvfp4_paged_kv: rows cu_q[s] .. cu_q[s+1] - 1 are the new tokens of
+ *                sequence s; rows of nobody are left as they were.
+ *   kv_len       int32 [num_seqs], as in nvfp4_paged_kv: tokens of the sequence with the new ones.  Where all are new
+ *                (kv_len <= number of new tokens) the sequence starts from zeros whatever its slot holds.
+ * A sequence without new tokens keeps its state.  All are read on the device, so a captured graph follows their
+ * contents; values out of range never lead outside the operands. */
+typedef struct {
+  void* data;
+  int64_t num_slots;
+  int64_t slot_stride;
+  const int32_t* slots;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int32_t num_seqs;
+} nvfp4_seq_states;
+
+/*
+ * The causal depthwise convolution with SiLU in front of the gated delta rule:
+ *   y[t, c] = silu(bias[c] + sum_j weight[c, j] * x[t - (width - 1) + j, c])            (fp32)
+ * along each sequence; inputs before its first new token are its state's.
+ *   states       [width - 1, channels] per slot, of x's type: the last inputs, oldest first; replaced by the last
+ *                width - 1 inputs of all (exact copies).
+ *   channels     a multiple of 8, at most 2^24; width 2 to 4; tokens < 2^30.
+ *   x            [tokens, ldx], NVFP4_BF16 or NVFP4_F32; weight device fp32 [channels, width]; bias fp32 [channels] or
+ *                NULL.  All 16-byte aligned, pitches times the element size multiples of 16 bytes.
+ *   y            [tokens, ldy] of y_dtype; must not overlap the inputs.
+ */
+int nvfp4_gdn_conv(const nvfp4_seq_states* states, int64_t tokens, int64_t channels, int width, const void* x, int x_dtype,
+                   int64_t ldx, const float* weight, const float* bias, void* y, int y_dtype, int64_t ldy, void* stream);
+
+/*
+ * The gated delta rule over the new tokens of a batch of sequences.  Per value head, S its state
+ * [k_dim, v_dim], k^ = k / sqrt(k.k + 1e-6), q^ = q / sqrt(q.q + 1e-6), token by token:
+ *   S <- e^g S;  u = beta (v - S^T k^);  S <- S + k^ u^T;  out = scale * S^T q^
+ * with q and k of key head h / (v heads / k heads).  One call takes any mix of single tokens, chunks and
+ * prompts.  A token has no influence on the tokens before it or on other sequences, whatever its values; a
+ * NaN or infinity in it makes its head's state and outputs (in v: those columns) non-finite from it on.
+ *   states       fp32 [v heads, k_dim, v_dim] per slot, replaced by the state behind the last new token.
+ *   q, k         bf16, equal head counts; v, out: bf16, a multiple of q's heads; out must not overlap the inputs.
+ *   g, beta      device fp32 [tokens, v heads] contiguous: log decay and write strength, as
+ *                nvfp4_gemm_fused_gdn_gates writes them.
+ *   k_dim        64 or 128; v_dim a multiple of 32, at most 512; tokens < 2^30 (others: NVFP4_ERR_UNSUPPORTED).
+ *   max_q        the largest number of new tokens of one sequence, or 0 if not known: a hint that picks
+ *                kernels.  Results do not depend on its truth beyond rounding, speed does.
+ *   workspace    device, 16-byte aligned, nvfp4_gated_delta_rule_workspace_size() bytes for the same
+ *                arguments; contents need no initialisation and are clobbered.
+ * States, sums and norms are fp32.  Deterministic.
+ */
+int nvfp4_gated_delta_rule(const nvfp4_seq_states* states, int64_t tokens, int64_t max_q, int64_t k_dim, int64_t v_dim,
+                           const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v, const float* g, const float* beta,
+                           float scale, const nvfp4_heads* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace nvfp4_gated_delta_rule needs for these sizes, whatever the lengths.  0 for bad sizes. */
+size_t nvfp4_gated_delta_rule_workspace_size(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t k_heads, int64_t v_heads,
+                                             int64_t k_dim, int64_t v_dim);
 
 /* Static description of a status code. */
 const char* nvfp4_status_string(int status);

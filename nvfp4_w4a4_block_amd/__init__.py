@@ -32,6 +32,14 @@ Entry points (same names as the C ABI):
                                             cache (PagedKV: FP8 or bf16), queries in the same launch
   paged_attention(q, kv, kv_len, cu_q, ...)
                                          -> attention of new tokens over the paged cache
+  add_rms_norm(x, weight, residual, eps, out_dtype, quant, mode, scale)
+                                         -> (y, y quantized, residual + x): norm in front of a linear,
+                                            its output NVFP4 or FP8
+  gdn_conv(state, x, weight, kv_len, cu_q)
+                                         -> causal convolution + SiLU of new tokens, states updated
+  gated_delta_rule(state, q, k, v, g, beta, kv_len, cu_q)
+                                         -> the recurrence over new tokens, states updated
+  gated_rms_norm(x, z, weight, ...)      -> (y, y quantized): norm of each head times silu(z)
 """
 from __future__ import annotations
 
@@ -46,6 +54,7 @@ __all__ = [
     "NVFP4Tensor", "NVFP4Error", "quantize", "gemm", "gemm_fused_segments", "gemm_nvfp4_out", "gemm_fused_gdn_gates", "MXFP4Tensor", "to_mxfp4", "mxfp4_gemm",
     "fp8_kv_quantize", "fp8_kv_dequantize", "interleave_gate_up", "gemm_swiglu", "decode_linear",
     "PagedKV", "qk_norm_rope", "kv_append", "paged_attention",
+    "FP8Tensor", "add_rms_norm", "gated_rms_norm", "GDNState", "gdn_conv", "gated_delta_rule",
     "library_path", "lib",
     "PER_TENSOR", "PER_ROW", "GIVEN", "MAX_SEGMENTS", "EXPORTED_SYMBOLS",
 ]
@@ -62,7 +71,8 @@ EXPORTED_SYMBOLS = (
     "nvfp4_gemm_nvfp4_out", "nvfp4_gemm_fused_gdn_gates", "nvfp4_to_mxfp4", "nvfp4_mxfp4_gemm",
     "nvfp4_gemm_workspace_size", "nvfp4_fp8_kv_quantize", "nvfp4_fp8_kv_dequantize",
     "nvfp4_interleave_gate_up", "nvfp4_gemm_swiglu", "nvfp4_decode_linear", "nvfp4_qk_norm_rope", "nvfp4_kv_append",
-    "nvfp4_paged_attention", "nvfp4_paged_attention_workspace_size", "nvfp4_status_string",
+    "nvfp4_paged_attention", "nvfp4_paged_attention_workspace_size", "nvfp4_add_rms_norm", "nvfp4_gated_rms_norm",
+    "nvfp4_gdn_conv", "nvfp4_gated_delta_rule", "nvfp4_gated_delta_rule_workspace_size", "nvfp4_status_string",
     "nvfp4_version",
 )
 
@@ -87,6 +97,20 @@ class _PagedKV(ctypes.Structure):
                 ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_seqs", ctypes.c_int32), ("table_width", ctypes.c_int32), ("scale_count", ctypes.c_int32)]
+
+
+class _NormOut(ctypes.Structure):
+    """nvfp4_norm_out"""
+    _fields_ = [("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("block_scales", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("y_dtype", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("mode", ctypes.c_int32)]
+
+
+class _SeqStates(ctypes.Structure):
+    """nvfp4_seq_states"""
+    _fields_ = [("data", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("slots", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("num_seqs", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -136,6 +160,17 @@ def _load() -> ctypes.CDLL:
     L.nvfp4_paged_attention.restype = i32
     L.nvfp4_paged_attention_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i32]
     L.nvfp4_paged_attention_workspace_size.restype = sz
+    norm_out, states = ctypes.POINTER(_NormOut), ctypes.POINTER(_SeqStates)
+    L.nvfp4_add_rms_norm.argtypes = [i64, i64, p, i32, i64, p, i32, i64, p, f32, p, i64, norm_out, p]
+    L.nvfp4_add_rms_norm.restype = i32
+    L.nvfp4_gated_rms_norm.argtypes = [i64, i64, heads, i32, heads, i32, p, f32, norm_out, p]
+    L.nvfp4_gated_rms_norm.restype = i32
+    L.nvfp4_gdn_conv.argtypes = [states, i64, i64, i32, p, i32, i64, p, p, p, i32, i64, p]
+    L.nvfp4_gdn_conv.restype = i32
+    L.nvfp4_gated_delta_rule.argtypes = [states, i64, i64, i64, i64, heads, heads, heads, p, p, f32, heads, p, sz, p]
+    L.nvfp4_gated_delta_rule.restype = i32
+    L.nvfp4_gated_delta_rule_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64]
+    L.nvfp4_gated_delta_rule_workspace_size.restype = sz
     L.nvfp4_gemm_workspace_size.argtypes = [i64, i64, i64]
     L.nvfp4_gemm_workspace_size.restype = sz
     L.nvfp4_status_string.argtypes = [i32]
@@ -830,3 +865,253 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, kv_len: torch.Tensor, cu_q: to
     _run(gpu, "nvfp4_paged_attention", lib.nvfp4_paged_attention, c, T, max_q, qa, D ** -0.5 if scale is None else scale,
          1 if causal else 0, window, oa, _ptr(lse), _ptr(workspace), have)
     return (out, lse) if return_lse else out
+
+
+# ---- between the 4-bit linears: norms with quantized outputs, the recurrent half ------------------------
+
+
+@dataclass
+class FP8Tensor:
+    """codes uint8 [rows, cols] (E4M3FN bytes), scale float32 [1] or [rows]: value = E4M3(code) * scale."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+
+@dataclass
+class GDNState:
+    """The states of a Gated DeltaNet layer's sequences, all on one GPU.
+
+    slots   int32 [sequences]: each sequence's row in the pools below, or None (sequence s has row s); a
+            value outside the pool stands for no state (starts from zeros, nothing kept).
+    conv    [slots, width - 1, channels], of the convolution's input type: the last inputs, oldest first.
+    delta   float32 [slots, v_heads, k_dim, v_dim]: the delta rule's states.
+    Pools are contiguous but for the slot stride; either may be None where it is not used."""
+    slots: torch.Tensor | None = None
+    conv: torch.Tensor | None = None
+    delta: torch.Tensor | None = None
+
+
+_FORMATS = {"none": 0, "nvfp4": 1, "fp8": 2}
+_DT = {torch.float32: _F32, torch.bfloat16: _BF16}
+
+
+def _rows_arg(t: torch.Tensor, name: str, dtypes: tuple, gpu: int, rows: int, cols: int) -> int:
+    """The row pitch of a [rows, cols] operand whose rows are contiguous."""
+    try:
+        n, c = t.shape
+        pitch, step = t.stride()
+        if n == rows and c == cols and (step == 1 or n == 0) and t.dtype in dtypes and t.get_device() == gpu:
+            return pitch
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError(f"{name}: a tensor {_shape_text(rows, cols)}") from None
+    if n != rows or c != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {_shape_text(rows, cols)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(x) for x in dtypes)}")
+    if step != 1 and n > 0:
+        raise ValueError(f"{name}: rows must be contiguous")
+    raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
+
+
+def _norm_out(like: torch.Tensor, gpu: int, rows: int, cols: int, out_dtype, quant: str, mode: str, scale, out, q_out):
+    """(y, quantized y, the C struct) of a norm's outputs over [rows, cols]."""
+    fmt = _FORMATS.get(quant)
+    if fmt is None:
+        raise ValueError(f"quant must be one of {sorted(_FORMATS)}")
+    if out_dtype is None:
+        _require(fmt != 0, "ask for y (out_dtype), a quantized output, or both")
+        _require(out is None, "out without out_dtype")
+        y, ldy, od = None, 0, _BF16
+    else:
+        od = _DT.get(out_dtype)
+        if od is None:
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        y = like.new_empty((rows, cols), dtype=out_dtype) if out is None else out
+        ldy = cols if out is None else _rows_arg(out, "out", (out_dtype,), gpu, rows, cols)
+    if fmt == 0:
+        _require(scale is None and q_out is None, "scale or q_out without quant")
+        return y, None, _NormOut(y.data_ptr(), ldy, None, None, None, od, 0, 0)
+    if mode not in ("per_row", "given"):
+        raise ValueError("mode must be per_row or given")
+    given = mode == "given"
+    _require(not given or scale is not None, "given mode needs scale")
+    _require(given or scale is None, "scale without mode given")
+    _require(cols % 16 == 0, "cols must be a multiple of 16")
+    if given:
+        _vector_arg(scale, "scale", torch.float32, (1,), gpu)
+    wide = cols // 2 if fmt == 1 else cols
+    if q_out is None:
+        codes = like.new_empty((rows, wide), dtype=torch.uint8)
+        s = scale if given else like.new_empty((rows,), dtype=torch.float32)
+        q = NVFP4Tensor(codes, like.new_empty((rows, cols // 16), dtype=torch.uint8), s) if fmt == 1 else FP8Tensor(codes, s)
+    else:
+        q = q_out
+        if not isinstance(q, NVFP4Tensor if fmt == 1 else FP8Tensor):
+            raise ValueError("q_out: an NVFP4Tensor or FP8Tensor, as quant says")
+        _require_bytes(q.codes, (rows, wide), "q_out.codes", like.device)
+        if fmt == 1:
+            _require_bytes(q.scales, (rows, cols // 16), "q_out.scales", like.device)
+            if given:
+                q.global_scale = scale
+            s = q.global_scale
+        else:
+            if given:
+                q.scale = scale
+            s = q.scale
+        _vector_arg(s, "q_out's scale", torch.float32, (1,) if given else (rows,), gpu)
+    return y, q, _NormOut(y.data_ptr() if y is not None else None, ldy, q.codes.data_ptr(), q.scales.data_ptr() if fmt == 1 else None,
+                          s.data_ptr(), od, fmt, GIVEN if given else PER_ROW)
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                 out_dtype: torch.dtype | None = torch.bfloat16, quant: str = "none", mode: str = "per_row",
+                 scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 q_out: NVFP4Tensor | FP8Tensor | None = None, residual_out: torch.Tensor | None = None):
+    """Residual addition and root-mean-square norm of the rows of x [M, N] (bf16 or fp32), the output
+    quantized for the next linear: r = x + residual (rounded to the residual's type; r = x without one),
+    y = r * weight / sqrt(mean(r^2) + eps), weight fp32 [N].  quant "nvfp4" gives an NVFP4Tensor, "fp8" an
+    FP8Tensor, both of fl32(y), their scale one per row (mode "per_row") or the given one (mode "given",
+    scale fp32 [1]).  out_dtype: the type of y itself, or None to leave it out.  residual_out may be the
+    residual.  Returns (y, quantized y, r); what was not asked for is None (r without a residual)."""
+    _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a tensor [rows, cols]")
+    gpu, (M, N) = x.get_device(), x.shape
+    ldx = _rows_arg(x, "x", _X_DTYPES, gpu, M, N)
+    w = _vector_arg(weight, "weight", torch.float32, (N,), gpu)
+    xd = _DT[x.dtype]
+    rp = rop = None
+    ldr = ldro = 0
+    rd = xd
+    if residual is not None:
+        ldr = _rows_arg(residual, "residual", _X_DTYPES, gpu, M, N)
+        rd, rp = _DT[residual.dtype], residual.data_ptr()
+        if residual_out is None:
+            residual_out, ldro = residual.new_empty((M, N)), N
+        else:
+            ldro = _rows_arg(residual_out, "residual_out", (residual.dtype,), gpu, M, N)
+        rop = residual_out.data_ptr()
+    else:
+        _require(residual_out is None, "residual_out without residual")
+    y, q, o = _norm_out(x, gpu, M, N, out_dtype, quant, mode, scale, out, q_out)
+    _run(gpu, "nvfp4_add_rms_norm", lib.nvfp4_add_rms_norm, M, N, x.data_ptr(), xd, ldx, rp, rd, ldr, w, eps, rop, ldro, o)
+    return y, q, residual_out
+
+
+def gated_rms_norm(x: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                   out_dtype: torch.dtype | None = torch.bfloat16, quant: str = "none", mode: str = "per_row",
+                   scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   q_out: NVFP4Tensor | FP8Tensor | None = None):
+    """Norm of each head vector of x [T, H, D] times its output gate z [T, H, D] (bf16 or fp32, strided views
+    welcome): y = x * weight / sqrt(mean(x^2) + eps) * z * sigmoid(z), weight fp32 [D].  The outputs are rows
+    [T, H * D], as of ``add_rms_norm``.  Returns (y, quantized y)."""
+    _require(isinstance(x, torch.Tensor) and x.dim() == 3, "x: a tensor [tokens, heads, dim]")
+    gpu, (T, H, D) = x.get_device(), x.shape
+    xa = _heads_arg(x, "x", _X_DTYPES, gpu)
+    za = _heads_arg(z, "z", _X_DTYPES, gpu, T, H, D)
+    w = _vector_arg(weight, "weight", torch.float32, (D,), gpu)
+    y, q, o = _norm_out(x, gpu, T, H * D, out_dtype, quant, mode, scale, out, q_out)
+    _run(gpu, "nvfp4_gated_rms_norm", lib.nvfp4_gated_rms_norm, T, D, xa, _DT[x.dtype], za, _DT[z.dtype], w, eps, o)
+    return y, q
+
+
+def _states_arg(state: GDNState, pool: torch.Tensor, name: str, dtype: torch.dtype, inner: tuple, kv_len: torch.Tensor,
+                cu_q: torch.Tensor, gpu: int) -> _SeqStates:
+    """A pool [slots, *inner], contiguous but for its slot stride, with the batch's slots and lengths."""
+    try:
+        shape, stride = tuple(pool.shape), pool.stride()
+        good = shape[1:] == inner and len(shape) == 1 + len(inner)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        raise ValueError(f"{name}: a tensor {_shape_text(None, *inner)}")
+    if pool.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {pool.dtype}, expected {dtype}")
+    want = 1
+    for n, s in zip(reversed(inner), reversed(stride)):
+        if n != 1 and s != want and shape[0] > 0:
+            raise ValueError(f"{name}: every slot must be contiguous")
+        want *= n
+    if pool.get_device() != gpu:
+        raise ValueError(f"{name}: on {pool.device}, the other tensors are elsewhere")
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("cu_q: contiguous torch.int32, one dimension")
+    seqs = cu_q.shape[0] - 1
+    slots = None if state.slots is None else _vector_arg(state.slots, "state.slots", torch.int32, (seqs,), gpu)
+    return _SeqStates(pool.data_ptr(), shape[0], stride[0], slots, _vector_arg(cu_q, "cu_q", torch.int32, (seqs + 1,), gpu),
+                      _vector_arg(kv_len, "kv_len", torch.int32, (seqs,), gpu), seqs)
+
+
+def gdn_conv(state: GDNState, x: torch.Tensor, weight: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor,
+             bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+             out: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal depthwise convolution with SiLU of the new tokens x [T, C] (bf16 or fp32, row stride may exceed C):
+    y[t, c] = silu(bias[c] + sum_j weight[c, j] x[t - (W - 1) + j, c]), weight fp32 [C, W], W = 2 to 4.  Rows
+    cu_q[s] .. cu_q[s+1] - 1 are the new tokens of sequence s (int32 [S + 1]) and kv_len[s] its length with them
+    (int32 [S]); the inputs before them come from state.conv, zeros where the sequence begins here, and
+    state.conv is replaced by the last W - 1 inputs.  Returns y [T, C]."""
+    _require(isinstance(state, GDNState), "state: a GDNState")
+    _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a tensor [tokens, channels]")
+    gpu, (T, C) = x.get_device(), x.shape
+    ldx = _rows_arg(x, "x", _X_DTYPES, gpu, T, C)
+    _require(isinstance(weight, torch.Tensor) and weight.dim() == 2 and weight.shape[0] == C, "weight: [channels, width]")
+    W = weight.shape[1]
+    _require(2 <= W <= 4, "weight: a width of 2 to 4")
+    _require(weight.dtype is torch.float32 and weight.is_contiguous() and weight.get_device() == gpu,
+             "weight: contiguous float32 on x's device")
+    b = None if bias is None else _vector_arg(bias, "bias", torch.float32, (C,), gpu)
+    st = _states_arg(state, state.conv, "state.conv", x.dtype, (W - 1, C), kv_len, cu_q, gpu)
+    od = _DT.get(out_dtype)
+    if od is None:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    y = x.new_empty((T, C), dtype=out_dtype) if out is None else out
+    ldy = C if out is None else _rows_arg(out, "out", (out_dtype,), gpu, T, C)
+    _run(gpu, "nvfp4_gdn_conv", lib.nvfp4_gdn_conv, st, T, C, W, x.data_ptr(), _DT[x.dtype], ldx, weight.data_ptr(), b,
+         y.data_ptr(), od, ldy)
+    return y
+
+
+def gated_delta_rule(state: GDNState, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                     beta: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor, scale: float | None = None,
+                     max_q: int = 0, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated delta rule over the new tokens of every sequence, token by token and value head:
+    S <- e^g S;  u = beta (v - S^T k^);  S <- S + k^ u^T;  out = scale S^T q^, with q^ and k^ of unit length.
+    q, k [T, Hk, Dk], v [T, Hv, Dv] (bf16, strided views welcome), Hv a multiple of Hk; g, beta fp32 [T, Hv]
+    as ``gemm_fused_gdn_gates`` returns them; state.delta fp32 [slots, Hv, Dk, Dv], updated; kv_len, cu_q as in
+    ``gdn_conv``.  Dk 64 or 128, Dv a multiple of 32.  scale: Dk ** -0.5 when None.  max_q: the longest chunk, if
+    known; a hint for speed only.  workspace: uint8, at least
+    ``lib.nvfp4_gated_delta_rule_workspace_size(...)`` bytes (allocated when None).  Returns out [T, Hv, Dv] bf16."""
+    _require(isinstance(state, GDNState), "state: a GDNState")
+    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q: a tensor [tokens, heads, dim]")
+    _require(isinstance(v, torch.Tensor) and v.dim() == 3, "v: a tensor [tokens, heads, dim]")
+    gpu, (T, Hk, Dk) = q.get_device(), q.shape
+    Hv, Dv = v.shape[1:]
+    qa = _heads_arg(q, "q", _BF16_ONLY, gpu)
+    ka = _heads_arg(k, "k", _BF16_ONLY, gpu, T, Hk, Dk)
+    va = _heads_arg(v, "v", _BF16_ONLY, gpu, T, Hv, Dv)
+    _require(Hk > 0 and Hv % Hk == 0, "v heads must be a multiple of q's")
+    for name, x in (("g", g), ("beta", beta)):
+        if _rows_arg(x, name, (torch.float32,), gpu, T, Hv) != Hv and T > 1:
+            raise ValueError(f"{name}: contiguous float32 [tokens, v heads]")
+    st = _states_arg(state, state.delta, "state.delta", torch.float32, (Hv, Dk, Dv), kv_len, cu_q, gpu)
+    out, oa = _out_heads(q, out, "out", torch.bfloat16, gpu, T, Hv, Dv)
+    need = lib.nvfp4_gated_delta_rule_workspace_size(T, max_q, st.num_seqs, Hk, Hv, Dk, Dv)
+    have = need
+    if workspace is None:
+        workspace = q.new_empty((need,), dtype=torch.uint8) if need else None
+    else:
+        _require(isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.is_contiguous(),
+                 "workspace: contiguous uint8")
+        have = workspace.numel()
+        if have < need:
+            raise ValueError(f"workspace: {have} bytes, {need} needed")
+        _require(workspace.get_device() == gpu, "workspace: on another device than q")
+    _run(gpu, "nvfp4_gated_delta_rule", lib.nvfp4_gated_delta_rule, st, T, max_q, Dk, Dv, qa, ka, va, g.data_ptr(),
+         beta.data_ptr(), Dk ** -0.5 if scale is None else scale, oa, _ptr(workspace), have)
+    return out

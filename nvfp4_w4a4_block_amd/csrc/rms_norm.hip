@@ -1,0 +1,260 @@
+// Root-mean-square norms in front of and behind the 4-bit linears, with their neighbours fused and the output
+// quantized on the way (gfx950):
+//   add_rms_norm    r' = rnd(x + r), y = r' w / sqrt(mean(r'^2) + eps)           over a row
+//   gated_rms_norm  y = x w / sqrt(mean(x^2) + eps) * z sigmoid(z)                over each head of a row
+// and from y, any of: bf16 or fp32; NVFP4 as the quantizer encodes fl32(y), under a given global scale or one per row
+// (max|y| / 2688); FP8 (E4M3) bytes under a given scale or one per row (max|y| / 448).
+//
+// HBM-bound: every element is read once and written once.  A workgroup takes one row and keeps it in registers, a
+// thread 16 consecutive elements (an NVFP4 block) at a time, so that the statistics, the row's maximum and the
+// encoding need one pass over memory.
+//
+// Arithmetic: in 64 bits from the stored r' (x and z) to y, which is then rounded once to fp32: codes of values next
+// to a rounding border do not depend on the order of a sum, so the NVFP4 and FP8 bytes are the quantizers' of the exactly
+// computed norm.  gated_rms_norm without a quantized output works in fp32, which hides its exponential behind the
+// loads (8192 tokens of 32 heads of 128, bf16 output: 38 us, 58 in 64 bits).
+#include <type_traits>
+
+#include "fp8_device.h"
+#include "gdn_internal.h"
+
+namespace nvfp4 {
+
+namespace {
+
+enum Format { kNone = 0, kNvfp4 = 1, kFp8 = 2 };
+
+template <typename T>
+struct Block16 {
+  uint4 w[sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i)
+    widen(reinterpret_cast<const uint4*>(p)[i], v + i * (16 / sizeof(T)), static_cast<const T*>(nullptr));
+}
+
+__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
+  uint4* o = reinterpret_cast<uint4*>(p);
+  o[0] = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  o[1] = make_uint4(bf16_pair(v[8], v[9]), bf16_pair(v[10], v[11]), bf16_pair(v[12], v[13]), bf16_pair(v[14], v[15]));
+}
+__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
+  float4* o = reinterpret_cast<float4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+__device__ __forceinline__ float rounded(float v, const uint16_t*) { return __uint_as_float((uint32_t)f32_to_bf16_rne(v) << 16); }
+__device__ __forceinline__ float rounded(float v, const float*) { return v; }
+
+// Sum over the workgroup's wavefronts; every thread gets it.
+__device__ __forceinline__ double group_sum(double v, double* lds) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m, 64);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.0;
+  for (int i = 0; i < waves; ++i) s += lds[i];
+  return s;
+}
+
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* lds) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, m, 64));
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  for (int i = 0; i < waves; ++i) v = max(v, lds[i]);
+  return v;
+}
+
+__device__ __forceinline__ uint4 fp8_16(const float (&v)[16], float s, bool zero) {
+  if (zero) {                                  // a row of zeros under its own scale of zero: signed zeros
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i] |= ((__float_as_uint(v[4 * i + j]) >> 24) & 0x80u) << (8 * j);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) nan |= v[i] != v[i];
+  if (fast_scale(s) && !nan) {
+    const FastQuotient f{s, 1.0f / s, 440.0f * s};
+    return make_uint4(fp8x4_fast(v, f), fp8x4_fast(v + 4, f), fp8x4_fast(v + 8, f), fp8x4_fast(v + 12, f));
+  }
+  return make_uint4(fp8x4_exact(v, s), fp8x4_exact(v + 4, s), fp8x4_exact(v + 8, s), fp8x4_exact(v + 12, s));
+}
+
+// z sigmoid(z) to about 2^-45.  e^-z = 2^n 2^f, |f| <= 1/2, 2^f by its Taylor series to the power 11 (the next term is
+// below 2^-46); the quotient by two Newton steps from the hardware's estimate.
+__device__ __forceinline__ double silu(double z) {
+  const double t = __builtin_fmin(__builtin_fmax(z * -1.4426950408889634074, -1000.0), 1000.0);
+  const double n = __builtin_rint(t), f = t - n;
+  double p = 4.4455382718708114976e-10;         // ln(2)^11 / 11!
+  p = __builtin_fma(p, f, 7.0549116208011233299e-9);
+  p = __builtin_fma(p, f, 1.0178086009239699728e-7);
+  p = __builtin_fma(p, f, 1.3215486790144309488e-6);
+  p = __builtin_fma(p, f, 1.5252733804059840280e-5);
+  p = __builtin_fma(p, f, 1.5403530393381609954e-4);
+  p = __builtin_fma(p, f, 1.3333558146428443423e-3);
+  p = __builtin_fma(p, f, 9.6181291076284771619e-3);
+  p = __builtin_fma(p, f, 5.5504108664821579953e-2);
+  p = __builtin_fma(p, f, 2.4022650695910071233e-1);
+  p = __builtin_fma(p, f, 6.9314718055994530942e-1);
+  p = __builtin_fma(p, f, 1.0);
+  const double d = 1.0 + __builtin_ldexp(p, (int)n);
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return z * r;
+}
+
+// In fp32: the exponential's argument is rounded, so |z| 2^-24 relative.
+__device__ __forceinline__ float silu(float z) { return z / (1.0f + __expf(-z)); }
+
+__device__ __forceinline__ double root(double v) { return __builtin_sqrt(v); }
+__device__ __forceinline__ float root(float v) { return __builtin_sqrtf(v); }
+
+// XT: type of x; AT: type of the residual (its output has the same) or of the gates; NB: blocks of a thread.
+template <typename XT, typename AT, int NB, bool GATED, int FORMAT>
+__global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
+  __shared__ double sums[16];
+  __shared__ uint32_t tops[16];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  float v[NB][16];
+  bool live[NB];
+  double sum = 0.0;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int b = tid + n * threads;
+    live[n] = b < a.blocks;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[n][i] = 0.0f;
+    if (GATED) {
+      typedef typename std::conditional<FORMAT == kNone, float, double>::type Real;
+      Real y[16], total = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = 0;
+      if (live[n]) {
+        const int head = b / a.head_blocks, c = (b - head * a.head_blocks) * 16;
+        float z[16], w[16];
+        load16(static_cast<const XT*>(a.x) + row * a.x_row + head * a.x_head + c, v[n]);
+        load16(static_cast<const AT*>(a.aux) + row * a.aux_row + head * a.aux_head + c, z);
+        load16(a.weight + c, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const Real x = v[n][i];
+          total += x * x;
+          y[i] = x * (Real)w[i] * silu((Real)z[i]);
+        }
+      }
+      // a head's blocks lie in neighbouring lanes
+      for (int m = 1; m < a.head_blocks; m *= 2) total += __shfl_xor(total, m, 64);
+      const Real inv = (Real)1 / root(total / (Real)(a.head_blocks * 16) + (Real)a.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[n][i] = (float)(y[i] * inv);
+    } else if (live[n]) {
+      load16(static_cast<const XT*>(a.x) + row * a.x_row + b * 16, v[n]);
+      if (a.aux) {
+        float r[16];
+        load16(static_cast<const AT*>(a.aux) + row * a.aux_row + b * 16, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[n][i] = rounded(v[n][i] + r[i], static_cast<const AT*>(nullptr));
+        if (a.residual_out) store16(static_cast<AT*>(a.residual_out) + row * a.residual_out_row + b * 16, v[n]);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum = __builtin_fma((double)v[n][i], (double)v[n][i], sum);
+    }
+  }
+  if (!GATED) {
+    sum = group_sum(sum, sums);
+    const double inv = 1.0 / __builtin_sqrt(sum / (double)(a.blocks * 16) + (double)a.eps);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (!live[n]) continue;
+      float w[16];
+      load16(a.weight + (tid + n * threads) * 16, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[n][i] = (float)((double)v[n][i] * (double)w[i] * inv);
+    }
+  }
+  if (a.y) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (!live[n]) continue;
+      const int64_t at = row * a.y_row + (tid + n * threads) * 16;
+      if (a.y_bf16)
+        store16(static_cast<uint16_t*>(a.y) + at, v[n]);
+      else
+        store16(static_cast<float*>(a.y) + at, v[n]);
+    }
+  }
+  if (FORMAT == kNone) return;
+  float s;
+  if (a.given) {
+    s = a.global[0];
+  } else {
+    uint32_t top = 0;                          // the largest magnitude's bits: NaN above infinity above the rest
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[n][i]) & 0x7FFFFFFFu);
+    top = group_max(top, tops);
+    s = __uint_as_float(top) / (FORMAT == kNvfp4 ? kGlobalDivisor : 448.0f);
+    if (tid == 0) a.global[row] = s;
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    if (!live[n]) continue;
+    const int64_t b = row * a.blocks + tid + n * threads;
+    if (FORMAT == kNvfp4) {
+      uint32_t scale, lo, hi;
+      encode_block(v[n], s, scale, lo, hi);
+      a.scales[b] = (uint8_t)scale;
+      reinterpret_cast<uint2*>(a.codes)[b] = make_uint2(lo, hi);
+    } else {
+      reinterpret_cast<uint4*>(a.codes)[b] = fp8_16(v[n], s, !a.given && s == 0.0f);
+    }
+  }
+}
+
+template <typename XT, typename AT, bool GATED, int FORMAT>
+int launch_format(const NormArgs& a, hipStream_t stream) {
+  const int waves = (a.blocks + 63) / 64;
+  if (waves <= 16)
+    rms_norm_kernel<XT, AT, 1, GATED, FORMAT><<<a.rows, waves * 64, 0, stream>>>(a);
+  else
+    rms_norm_kernel<XT, AT, 2, GATED, FORMAT><<<a.rows, (waves + 1) / 2 * 64, 0, stream>>>(a);
+  return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+template <typename XT, typename AT, bool GATED>
+int launch_types(const NormArgs& a, int format, hipStream_t stream) {
+  if (format == kNvfp4) return launch_format<XT, AT, GATED, kNvfp4>(a, stream);
+  if (format == kFp8) return launch_format<XT, AT, GATED, kFp8>(a, stream);
+  return launch_format<XT, AT, GATED, kNone>(a, stream);
+}
+
+}  // namespace
+
+int launch_rms_norm(const NormArgs& a, bool gated, int x_dtype, int aux_dtype, int format, hipStream_t stream) {
+  const bool xb = x_dtype == NVFP4_BF16, ab = aux_dtype == NVFP4_BF16;
+  if (gated)
+    return xb ? (ab ? launch_types<uint16_t, uint16_t, true>(a, format, stream) : launch_types<uint16_t, float, true>(a, format, stream))
+              : (ab ? launch_types<float, uint16_t, true>(a, format, stream) : launch_types<float, float, true>(a, format, stream));
+  return xb ? (ab ? launch_types<uint16_t, uint16_t, false>(a, format, stream) : launch_types<uint16_t, float, false>(a, format, stream))
+            : (ab ? launch_types<float, uint16_t, false>(a, format, stream) : launch_types<float, float, false>(a, format, stream));
+}
+
+}  // namespace nvfp4
