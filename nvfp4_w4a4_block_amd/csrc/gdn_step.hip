@@ -6,6 +6,7 @@
 // registers over all the sequence's new tokens, with no barrier.  Both products with the old state are taken in
 // one pass and one reduction, o = scale (e^g S^T q^ + (k^.q^) u).
 // HBM-bound for single tokens: a state is read once and written once.
+#include "gdn_chunk.h"
 #include "seq_device.h"
 
 namespace nvfp4 {
@@ -57,7 +58,7 @@ __device__ __forceinline__ void unit_row(float (&x)[R]) {
 }
 
 template <int DK>
-__global__ __launch_bounds__(kThreads) void delta_step_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads) void delta_step_kernel(DeltaArgs a, int short_len, const uint8_t* flags) {
   constexpr int R = DK / 16;
   const int lane = threadIdx.x & 63;
   const int slices = a.v_dim / 16;
@@ -68,7 +69,8 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(DeltaArgs a) {
   if (seq >= a.s.num_seqs) return;
   const SeqRows rows = seq_rows(a.s, seq);
   const int n = rows.end - rows.first;
-  if (n == 0) return;
+  // longer sequences: only the slices that the blockwise kernel left
+  if (n == 0 || (n > short_len && flags[pair * slices + slice] == 0)) return;
   const int slot = seq_slot(a.s, seq);
   const int k_head = (int)fastdiv((uint32_t)head, a.div_group);
   const int r0 = (lane >> 2) * R, c0 = slice * 16 + (lane & 3) * 4;
@@ -121,16 +123,34 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(DeltaArgs a) {
 
 }  // namespace
 
-size_t gated_delta_rule_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int, int) { return 0; }
+// Where the longest sequence is known to have at most this many new tokens, all go token by token.
+constexpr int kShort = 16;
 
-int launch_gated_delta_rule(const DeltaArgs& a, int64_t, int k_dim, void*, hipStream_t stream) {
+size_t gated_delta_rule_workspace_bytes(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t k_heads, int64_t v_heads,
+                                        int k_dim, int v_dim) {
+  if ((max_q > 0 && max_q <= kShort) || tokens <= kShort) return 0;
+  ChunkWork ws;
+  return chunk_workspace(tokens, num_seqs, k_heads, v_heads, k_dim, v_dim, nullptr, ws);
+}
+
+int launch_gated_delta_rule(const DeltaArgs& a, int64_t max_q, int k_dim, void* workspace, hipStream_t stream) {
   const int64_t jobs = (int64_t)a.s.num_seqs * a.v_heads * (a.v_dim / 16);
   const int64_t grid = (jobs + kThreads / 64 - 1) / (kThreads / 64);
   if (grid * kThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;           // threads of a launch
+  int short_len = INT32_MAX;
+  const uint8_t* flags = nullptr;
+  if (gated_delta_rule_workspace_bytes(a.s.tokens, max_q, a.s.num_seqs, a.k_heads, a.v_heads, k_dim, a.v_dim) > 0) {
+    ChunkWork ws;
+    chunk_workspace(a.s.tokens, a.s.num_seqs, a.k_heads, a.v_heads, k_dim, a.v_dim, workspace, ws);
+    ws.short_len = short_len = kShort;
+    flags = ws.flags;
+    const int st = launch_chunks(a, ws, k_dim, stream);
+    if (st != NVFP4_OK) return st;
+  }
   if (k_dim == 128)
-    delta_step_kernel<128><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+    delta_step_kernel<128><<<(unsigned)grid, kThreads, 0, stream>>>(a, short_len, flags);
   else
-    delta_step_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+    delta_step_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(a, short_len, flags);
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
