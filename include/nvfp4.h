@@ -623,7 +623,8 @@ int nvfp4_gdn_conv(const nvfp4_seq_states* states, int64_t tokens, int64_t chann
  * prompts.  A token has no influence on the tokens before it or on other sequences, whatever its values; a
  * NaN or infinity in it makes its head's state and outputs (in v: those columns) non-finite from it on.
  *   states       fp32 [v heads, k_dim, v_dim] per slot, replaced by the state behind the last new token.
- *   q, k         bf16, equal head counts; v, out: bf16, a multiple of q's heads; out must not overlap the inputs.
+ *   q, k         bf16, equal head counts; v, out: bf16, a multiple of q's heads, token strides below 2^24; out must
+ *                not overlap the inputs.
  *   g, beta      device fp32 [tokens, v heads] contiguous: log decay and write strength, as
  *                nvfp4_gemm_fused_gdn_gates writes them.
  *   k_dim        64 or 128; v_dim a multiple of 32, at most 512; tokens < 2^30 (others: NVFP4_ERR_UNSUPPORTED).

@@ -169,6 +169,7 @@ int nvfp4_gated_delta_rule(const nvfp4_seq_states* states, int64_t tokens, int64
   if (st == NVFP4_OK) st = check_heads(v, tokens, v_dim, 2, vv);
   if (st == NVFP4_OK) st = check_heads(out, tokens, v_dim, 2, ov);
   if (st != NVFP4_OK) return st;
+  if (vv.tok >= 1 << 24 || ov.tok >= 1 << 24) return NVFP4_ERR_UNSUPPORTED;      // 64 rows within 2^31 bytes
   if (!disjoint(ov, tokens, v_dim) || !g || !beta || !aligned(g, 4) || !aligned(beta, 4)) return NVFP4_ERR_INVALID_ARG;
   const size_t need = gated_delta_rule_workspace_bytes(tokens, max_q, states->num_seqs, qv.heads, vv.heads, (int)k_dim, (int)v_dim);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return NVFP4_ERR_WORKSPACE;

@@ -14,6 +14,8 @@
 // That scale rests on the contraction (finite values, g <= 0, 0 <= beta <= 2): a column's 2-norm stays below the
 // running sum B <- e^G B + sum |beta v|.  Where a block breaks that premise the scan gives up its slice with a flag, and
 // the token-by-token kernel, which runs behind it, takes the slice from the sequence's start.
+#include <type_traits>
+
 #include "gdn_chunk.h"
 #include "seq_device.h"
 
@@ -51,12 +53,19 @@ __device__ __forceinline__ half2_t to_half2(float a, float b) {
   return __builtin_convertvector((f32x2_t){a, b}, half2_t);
 }
 
-// Four values in two fp16 parts.
-__device__ __forceinline__ void split4(const f32x4_t x, half4_t& hi, half4_t& lo) {
+// Four values in two fp16 parts.  `one` is 1.0f where the compiler does not see it: x - (float)h is then one mixed
+// multiply-add instead of a conversion and a difference.
+__device__ __forceinline__ void split4(const f32x4_t x, half4_t& hi, half4_t& lo, float one) {
   const half2_t a = to_half2(x[0], x[1]), b = to_half2(x[2], x[3]);
   hi = half4_t{a[0], a[1], b[0], b[1]};
-  const half2_t c = to_half2(x[0] - (float)a[0], x[1] - (float)a[1]), d = to_half2(x[2] - (float)b[0], x[3] - (float)b[1]);
+  const half2_t c = to_half2(__builtin_fmaf((float)a[0], -one, x[0]), __builtin_fmaf((float)a[1], -one, x[1]));
+  const half2_t d = to_half2(__builtin_fmaf((float)b[0], -one, x[2]), __builtin_fmaf((float)b[1], -one, x[3]));
   lo = half4_t{c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ float hidden_one() {
+  uint32_t bits = 0x3F800000u;
+  asm("" : "+s"(bits));
+  return __uint_as_float(bits);
 }
 
 // Sum over the four lanes 16 apart.
@@ -194,9 +203,9 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
       f[kTok + lane] = beta * since * rk[lane];
       f[2 * kTok + lane] = expf((float)(total - sum)) * rk[lane];
       f[3 * kTok + lane] = since * rq[lane];
-      if (lane == 0) {
-        f[4 * kTok] = expf((float)total);
-        f[4 * kTok + 1] = bad_head ? 1.0f : 0.0f;
+      if (lane < 8) {
+        f[4 * kTok + 2 * lane] = expf((float)total);
+        f[4 * kTok + 2 * lane + 1] = bad_head ? 1.0f : 0.0f;
       }
     }
     double row_sum[4];
@@ -287,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
         for (int i = 0; i < 2; ++i) {
           half4_t h, l;
           const float4 x = reinterpret_cast<const float4*>(row)[i];
-          split4(f32x4_t{x.x, x.y, x.z, x.w}, h, l);
+          split4(f32x4_t{x.x, x.y, x.z, x.w}, h, l, 1.0f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             hi[4 * i + j] = h[j];
@@ -303,315 +312,443 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
   }
 }
 
-// What a wavefront needs of one block.
+constexpr int kScanThreads = 512;
+
+// What a wavefront of the solving half needs of one block, and one of the output half.
 template <int KS, int NC>
-struct Stage {
-  half8_t k[KS], q[KS], t_hi[2], t_lo[2], a[2];
-  float4 beta, c, d, e;            // factors of rows 4 g .. 4 g + 3 of its 16 tokens
-  float decay, bad;
-  uint32_t v[NC][2];               // bf16 values of those rows, two to a word
+struct SolveStage {
+  half8_t k[KS], t_hi[2], t_lo[2];
+  float4 beta, c, d;               // factors of rows 4 g .. 4 g + 3 of its 16 tokens
+  float2 whole;                    // the block's decay, and whether it is out of the scale's premise
+  uint32_t v[NC][4];               // bf16 values of those rows
+};
+template <int KS>
+struct OutStage {
+  half8_t q[KS], a[2];
+  float4 e;
+  float2 whole;
 };
 
-// The scan: one workgroup per sequence, value head and slice of 16 NC state columns.  Wavefront w takes tokens
-// 16 w .. 16 w + 15 of each block in the products whose rows are tokens, and Dk / 4 rows of the state, which stay in its
-// registers; S, R and U meet the other wavefronts in LDS, one barrier each.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+template <typename T>
+__device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
+  return *reinterpret_cast<const T*>(static_cast<const char*>(base) + bytes);
+}
+
+// The scan: one workgroup per sequence, value head and slice of 16 NC state columns; eight wavefronts that walk along
+// the sequence together, three barriers a block.  Four solve for the updates (16 tokens each: X = K S, R, U = T R), four
+// make the outputs (Q S while the others do K S, A U while those are at the next block); all update the state, 16 rows
+// of it in the registers of each wavefront that has some.  S, R and U meet the others in LDS.
 template <int DK, int NC>
-__global__ __launch_bounds__(kThreads, 2) void chunk_scan_kernel(DeltaArgs a, ChunkWork ws) {
-  constexpr int KS = DK / 32, RT = DK / 64;
-  __shared__ __attribute__((aligned(16))) _Float16 Ss[2][NC][16][DK + 8];
-  __shared__ __attribute__((aligned(16))) _Float16 Rs[2][NC][16][kTok + 8];
-  __shared__ __attribute__((aligned(16))) _Float16 Us[3][NC][16][kTok + 8];
-  __shared__ __attribute__((aligned(16))) _Float16 Ks[2][kTok][DK + 16];
-  __shared__ float Ms[2][4][NC * 16];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
-  // a key head's workgroups share its K, Q and their value head's T, A: all on one XCD (workgroup i runs on XCD i mod 8)
-  const int group = a.v_heads / a.k_heads, slices = a.v_dim / (16 * NC), per_unit = group * slices;
-  const int j = blockIdx.x >> 3;
-  const int unit = (j / per_unit) * 8 + (blockIdx.x & 7), part = j % per_unit;
-  const int seq = unit / a.k_heads, k_head = unit - seq * a.k_heads;
-  if (seq >= a.s.num_seqs) return;
-  const int head = k_head * group + part / slices, slice = part % slices;
-  const SeqRows rows = seq_rows(a.s, seq);
-  const int n = rows.end - rows.first;
-  if (n <= ws.short_len) return;
-  const int blocks = (n + kTok - 1) / kTok, slot0 = rows.first / kTok + seq;
-  const int slot = seq_slot(a.s, seq);
-  const bool old = slot >= 0 && scalar_load(a.s.kv_len + seq) > n;
-  const int c0 = slice * 16 * NC;
-  uint8_t* flag = ws.flags + ((int64_t)seq * a.v_heads + head) * (a.v_dim / 16) + slice * NC;
-
-  auto load = [&](Stage<KS, NC>& s, int b) {
-    if (b >= blocks) return;
-    const int64_t kq = (((int64_t)(slot0 + b) * a.k_heads + k_head) * 4 + w) * KS * 64 + lane;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      s.k[ks] = reinterpret_cast<const half8_t*>(ws.k)[kq + ks * 64];
-      s.q[ks] = reinterpret_cast<const half8_t*>(ws.q)[kq + ks * 64];
-    }
-    const int64_t pair = (int64_t)(slot0 + b) * a.v_heads + head;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-      if (ks <= (w >> 1)) {
-        const int64_t frag = pair * kTriFrags + tri_frag(w, ks);
-        s.t_hi[ks] = reinterpret_cast<const half8_t*>(ws.t)[(2 * frag) * 64 + lane];
-        s.t_lo[ks] = reinterpret_cast<const half8_t*>(ws.t)[(2 * frag + 1) * 64 + lane];
-        s.a[ks] = reinterpret_cast<const half8_t*>(ws.a)[frag * 64 + lane];
-      }
-    const float* f = ws.factors + pair * kFactors;
-    s.beta = *reinterpret_cast<const float4*>(f + 16 * w + 4 * g);
-    s.c = *reinterpret_cast<const float4*>(f + kTok + 16 * w + 4 * g);
-    s.d = *reinterpret_cast<const float4*>(f + 2 * kTok + 16 * w + 4 * g);
-    s.e = *reinterpret_cast<const float4*>(f + 3 * kTok + 16 * w + 4 * g);
-    s.decay = scalar_load(f + 4 * kTok);
-    s.bad = scalar_load(f + 4 * kTok + 1);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      uint32_t v[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = b * kTok + 16 * w + 4 * g + r;
-        v[r] = t < n ? a.v[(int64_t)(rows.first + t) * a.v_tok + head * a.v_head + c0 + nc * 16 + c] : 0;
-      }
-      s.v[nc][0] = v[0] | v[1] << 16;
-      s.v[nc][1] = v[2] | v[3] << 16;
-    }
-  };
-  auto value = [&](const Stage<KS, NC>& s, int nc, int r) {
-    const uint32_t x = s.v[nc][r >> 1];
-    return __uint_as_float(r & 1 ? x & 0xFFFF0000u : x << 16);
-  };
-  // sum of |beta v| over the wavefront's tokens, by column, for the block's scale
-  auto write_sums = [&](const Stage<KS, NC>& s, int buf) {
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      const float b[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w};
-      float m = 0.0f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) m = __builtin_fmaf(b[r], __builtin_fabsf(value(s, nc, r)), m);
-      m = quad_sum(m);
-      if (g == 0) Ms[buf][w][nc * 16 + c] = m;
-    }
-  };
-  auto read_sums = [&](float (&m)[NC], int buf) {
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      const int i = nc * 16 + c;
-      m[nc] = Ms[buf][0][i] + Ms[buf][1][i] + Ms[buf][2][i] + Ms[buf][3][i];
-    }
+struct Scan {
+  static constexpr int KS = DK / 32, TILES = DK / 16;
+  struct Lds {
+    _Float16 S[2][NC][16][DK + 8];
+    _Float16 R[2][NC][16][kTok + 8];
+    _Float16 U[3][NC][16][kTok + 8];           // U, then its product with the decays to the block's end in two parts
+    _Float16 K[2][kTok][DK + 16];
+    float norm[8][NC * 16];
+    uint32_t top[3][NC * 16];                  // largest |beta v| of a block, as bits
   };
 
-  Stage<KS, NC> s0, s1;
-  load(s0, 0);
-  load(s1, 1);
-  // the state, rows (w RT + rt) 16 + 4 g + r of column c, in units of `unit_of` from here on
-  f32x4_t S[RT][NC];
-  float* state = static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
-                 ((int64_t)head * DK + w * RT * 16 + 4 * g) * a.v_dim + c0 + c;
-  float bound[NC], up[NC], down[NC];           // of a column: its norm's bound, 1 / unit, unit
-#pragma unroll
-  for (int nc = 0; nc < NC; ++nc) {
-    float m = 0.0f;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        S[rt][nc][r] = old ? state[(int64_t)(rt * 16 + r) * a.v_dim + nc * 16] : 0.0f;
-        m += __builtin_fabsf(S[rt][nc][r]);
-      }
-    m = quad_sum(m);
-    if (g == 0) Ms[1][w][nc * 16 + c] = m;
+  const DeltaArgs& a;
+  const ChunkWork& ws;
+  Lds& lds;
+  const int lane, w, c, g, seq, head, k_head, c0;
+  SeqRows rows;
+  int n, blocks, slot0;
+  f32x4_t S[NC];
+  float bound[NC], down[NC];                   // of a column: its norm's bound, the block's unit
+  float state_down[NC], to_state[NC];          // the unit of S between blocks, and the block's in terms of it
+  bool bad = false;
+  const float one = hidden_one();
+
+  __device__ Scan(const DeltaArgs& args, const ChunkWork& work, Lds& shared, int seq_, int head_, int k_head_, int c0_)
+      : a(args), ws(work), lds(shared), lane(threadIdx.x & 63), w(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+        c(lane & 15), g(lane >> 4), seq(seq_), head(head_), k_head(k_head_), c0(c0_) {}
+
+  // The state's tile of this wavefront; the solving half has none if there are only four.
+  __device__ __forceinline__ int tile() const { return TILES == 8 ? w : w - 4; }
+  __device__ __forceinline__ bool owner() const { return tile() >= 0; }
+
+  __device__ __forceinline__ const char* at(const void* base, int block, int heads, int h, int bytes) const {
+    return static_cast<const char*>(base) + ((int64_t)(slot0 + block) * heads + h) * bytes;
   }
-  write_sums(s0, 0);
-  lds_barrier();
-  read_sums(bound, 1);
-  float sums[NC];
-  read_sums(sums, 0);
-  bool bad = s0.bad != 0.0f;
-  // Units: the bound on everything of the block, below 2^13 of them; updates stay below three times that.
-  auto set_unit = [&](int nc) {
-    const float most = bound[nc] + sums[nc];
-    bad |= !(most < 0x1p100f);
-    const uint32_t e = max(__float_as_uint(most) >> 23, 20u);
-    up[nc] = __uint_as_float((266u - e) << 23);
-    down[nc] = __uint_as_float((e - 12u) << 23);
-  };
-  auto write_state = [&](const f32x4_t (&x)[RT][NC]) {
+  __device__ __forceinline__ const char* factors(int block) const {
+    return at(ws.factors, block, a.v_heads, head, kFactors * 4);
+  }
+  // Rows of a block as a buffer: reads past the sequence's end give 0, writes there go nowhere.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint16_t* x, int64_t tok, int64_t h, int block) const {
+    const int row = block * kTok, m = min(n - row, kTok);
+    const uint16_t* p = x + (int64_t)(rows.first + row) * tok + head * h + c0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, (uint32_t)((m - 1) * (uint32_t)tok + 16 * NC) * 2,
+                                             0x00027000);
+  }
+
+  // Loads are straight-line and the same every time (past the end: the last block again), so that the waits in the
+  // loop count on exactly what was issued since.
+  __device__ __forceinline__ void load(SolveStage<KS, NC>& s, int block, const uint32_t (&v_at)[4]) const {
+    const int b = min(block, blocks - 1);
+    const char* kp = at(ws.k, b, a.k_heads, k_head, 4 * KS * 1024);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) s.k[ks] = load_at<half8_t>(kp, ((w * KS + ks) * 64 + lane) * 16);
+    const char* tp = at(ws.t, b, a.v_heads, head, kTriFrags * 2048);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint32_t frag = tri_frag(w, min(ks, w >> 1)) * 2048 + lane * 16;
+      s.t_hi[ks] = load_at<half8_t>(tp, frag);
+      s.t_lo[ks] = load_at<half8_t>(tp, frag + 1024);
+    }
+    const char* f = factors(b);
+    const uint32_t row = (16 * w + 4 * g) * 4;
+    s.beta = load_at<float4>(f, row);
+    s.c = load_at<float4>(f, row + kTok * 4);
+    s.d = load_at<float4>(f, row + 2 * kTok * 4);
+    // one copy for each of eight lanes: as a scalar load, every wait on LDS would wait for it
+    s.whole = load_at<float2>(f, 4 * kTok * 4 + 8 * (lane & 7));
+    const __amdgpu_buffer_rsrc_t v = buffer(a.v, a.v_tok, a.v_head, b);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        half4_t hi, lo;
-        split4(x[rt][nc], hi, lo);
-        *reinterpret_cast<half4_t*>(&Ss[0][nc][c][(w * RT + rt) * 16 + 4 * g]) = hi;
-        *reinterpret_cast<half4_t*>(&Ss[1][nc][c][(w * RT + rt) * 16 + 4 * g]) = lo;
-      }
-  };
-#pragma unroll
-  for (int nc = 0; nc < NC; ++nc) {
-    set_unit(nc);
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) S[rt][nc] *= up[nc];
+      for (int r = 0; r < 4; ++r) s.v[nc][r] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(v, v_at[r], nc * 32, 0);
   }
-  if (__builtin_amdgcn_ballot_w64(bad) != 0) {
-    if (threadIdx.x < NC) flag[threadIdx.x] = 1;
-    return;
+  __device__ __forceinline__ void load(OutStage<KS>& s, int block) const {
+    const int b = min(block, blocks - 1), o = w - 4;
+    const char* qp = at(ws.q, b, a.k_heads, k_head, 4 * KS * 1024);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(qp, ((o * KS + ks) * 64 + lane) * 16);
+    const char* ap = at(ws.a, b, a.v_heads, head, kTriFrags * 1024);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(ap, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
+    const char* f = factors(b);
+    s.e = load_at<float4>(f, 3 * kTok * 4 + (16 * o + 4 * g) * 4);
+    s.whole = load_at<float2>(f, 4 * kTok * 4 + 8 * (lane & 7));
   }
-  write_state(S);
-  lds_barrier();
 
-  const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  // One block; false where the next one breaks the scale's premise.
-  auto block_step = [&](Stage<KS, NC>& s, const Stage<KS, NC>& next, int b) -> bool {
-    const int buf = b & 1;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<half8_t*>(&Ks[buf][16 * w + c][ks * 32 + g * 8]) = s.k[ks];
-    f32x4_t Y[NC], R[NC];
+  __device__ __forceinline__ static float value(const SolveStage<KS, NC>& s, int nc, int r) {
+    return __uint_as_float(s.v[nc][r] << 16);
+  }
+  // The largest |beta v| of the wavefront's tokens, by column, for the block's unit.
+  __device__ __forceinline__ void write_top(const SolveStage<KS, NC>& s, int block) const {
+    const float b[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w};
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      f32x4_t x = zero, xl = zero;
-      Y[nc] = zero;
+      uint32_t m = 0;                          // as bits, so that a NaN is the largest
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(b[r] * value(s, nc, r)) & 0x7FFFFFFFu);
+      atomicMax(&lds.top[block % 3][nc * 16 + c], m);
+    }
+  }
+
+  __device__ __forceinline__ void write_state() const {
+    if (!owner()) return;
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      half4_t hi, lo;
+      split4(S[nc], hi, lo, one);
+      *reinterpret_cast<half4_t*>(&lds.S[0][nc][c][tile() * 16 + 4 * g]) = hi;
+      *reinterpret_cast<half4_t*>(&lds.S[1][nc][c][tile() * 16 + 4 * g]) = lo;
+    }
+  }
+
+  // The power of two that takes x < 2^100 below 2^13, and its inverse.
+  __device__ __forceinline__ static void unit(float x, float& up, float& down) {
+    const uint32_t e = max(min(__float_as_uint(x) >> 23, 226u), 20u);
+    up = __uint_as_float((266u - e) << 23);
+    down = __uint_as_float((e - 12u) << 23);
+  }
+
+  // The units of a block: everything in it is below bound + 64 max|beta v| of a column, updates below three times that.
+  // Between blocks S has a unit of its own, by its bound alone, which follows strong decays.  ratio: from the state's unit
+  // to the block's.
+  __device__ __forceinline__ void open_block(int block, float2 whole, float (&up)[NC], float (&ratio)[NC]) {
+    bad |= whole.y != 0.0f;
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      const float more = 64.0f * __uint_as_float(lds.top[block % 3][nc * 16 + c]);
+      const float most = bound[nc] + more;
+      bad |= !(most < 0x1p100f);
+      unit(most, up[nc], down[nc]);
+      ratio[nc] = state_down[nc] * up[nc];
+      bound[nc] = __builtin_fmaf(whole.x, bound[nc], more) * 1.00001f;
+      float state_up;
+      unit(bound[nc], state_up, state_down[nc]);
+      to_state[nc] = down[nc] * state_up;
+    }
+    if (threadIdx.x >= kScanThreads - NC * 16) lds.top[(block + 2) % 3][threadIdx.x - (kScanThreads - NC * 16)] = 0;
+  }
+
+  // Transposed K: lane i of 16 addresses 4 channels of token i / 4 and gets channel i of 4 tokens.
+  __device__ __forceinline__ void read_kt(half8_t (&kt)[2], int block) const {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      half4_t p[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        p[i] = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4_t*)&lds.K[block & 1][ks * 32 + g * 8 + i * 4 + (c >> 2)][tile() * 16 + (c & 3) * 4]));
+      kt[ks] = half8_t{p[0][0], p[0][1], p[0][2], p[0][3], p[1][0], p[1][1], p[1][2], p[1][3]};
+    }
+  }
+
+  // S <- decay S + K^T U in the block's unit, then in the state's.
+  __device__ __forceinline__ void update(const half8_t (&kt)[2], float decay, const float (&ratio)[NC]) {
+    half8_t hi[NC][2], lo[NC][2];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        hi[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.U[1][nc][c][ks * 32 + g * 8]);
+        lo[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.U[2][nc][c][ks * 32 + g * 8]);
+      }
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) S[nc] *= decay * ratio[nc];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) S[nc] = mfma(kt[ks], lo[nc][ks], S[nc]);
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) S[nc] = mfma(kt[ks], hi[nc][ks], S[nc]);
+    }
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) S[nc] *= to_state[nc];
+  }
+
+  __device__ __forceinline__ void solve_block(const SolveStage<KS, NC>& s, const SolveStage<KS, NC>& next, int b) {
+    float up[NC], ratio[NC];
+    open_block(b, s.whole, up, ratio);
+    half8_t hi[NC][KS], lo[NC][KS];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const half8_t hi = *reinterpret_cast<const half8_t*>(&Ss[0][nc][c][ks * 32 + g * 8]);
-        const half8_t lo = *reinterpret_cast<const half8_t*>(&Ss[1][nc][c][ks * 32 + g * 8]);
-        x = mfma(s.k[ks], hi, x);
-        xl = mfma(s.k[ks], lo, xl);
-        Y[nc] = mfma(s.q[ks], hi, Y[nc]);
+        lo[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.S[1][nc][c][ks * 32 + g * 8]);
+        hi[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.S[0][nc][c][ks * 32 + g * 8]);
       }
-      const float be[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w}, cc[4] = {s.c.x, s.c.y, s.c.z, s.c.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) R[nc][r] = be[r] * (value(s, nc, r) * up[nc]) - cc[r] * (x[r] + xl[r]);
-      half4_t hi, lo;
-      split4(R[nc], hi, lo);
-      *reinterpret_cast<half4_t*>(&Rs[0][nc][c][16 * w + 4 * g]) = hi;
-      *reinterpret_cast<half4_t*>(&Rs[1][nc][c][16 * w + 4 * g]) = lo;
-    }
-    if (b + 1 < blocks) write_sums(next, buf ^ 1);
-    lds_barrier();
+    for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<half8_t*>(&lds.K[b & 1][16 * w + c][ks * 32 + g * 8]) = s.k[ks];
+    const float be[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w}, cc[4] = {s.c.x, s.c.y, s.c.z, s.c.w};
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      f32x4_t u = zero, ul = zero;
+      f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f}, r4;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) x = mfma(s.k[ks], lo[nc][ks], x);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) x = mfma(s.k[ks], hi[nc][ks], x);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) r4[r] = __builtin_fmaf(be[r] * value(s, nc, r), up[nc], -(cc[r] * ratio[nc]) * x[r]);
+      half4_t rh, rl;
+      split4(r4, rh, rl, one);
+      *reinterpret_cast<half4_t*>(&lds.R[0][nc][c][16 * w + 4 * g]) = rh;
+      *reinterpret_cast<half4_t*>(&lds.R[1][nc][c][16 * w + 4 * g]) = rl;
+    }
+    lds_barrier();
+    half8_t kt[2];
+    if (TILES == 8) read_kt(kt, b);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      f32x4_t u = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
         if (ks <= (w >> 1)) {
-          const half8_t hi = *reinterpret_cast<const half8_t*>(&Rs[0][nc][c][ks * 32 + g * 8]);
-          const half8_t lo = *reinterpret_cast<const half8_t*>(&Rs[1][nc][c][ks * 32 + g * 8]);
-          u = mfma(s.t_hi[ks], hi, u);
-          ul = mfma(s.t_hi[ks], lo, ul);
-          ul = mfma(s.t_lo[ks], hi, ul);
+          const half8_t rh = *reinterpret_cast<const half8_t*>(&lds.R[0][nc][c][ks * 32 + g * 8]);
+          const half8_t rl = *reinterpret_cast<const half8_t*>(&lds.R[1][nc][c][ks * 32 + g * 8]);
+          u = mfma(s.t_lo[ks], rh, u);
+          u = mfma(s.t_hi[ks], rl, u);
+          u = mfma(s.t_hi[ks], rh, u);
         }
-      u += ul;
       const float d[4] = {s.d.x, s.d.y, s.d.z, s.d.w};
       const half2_t ua = to_half2(u[0], u[1]), ub = to_half2(u[2], u[3]);
-      half4_t hi, lo;
-      split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, hi, lo);
-      *reinterpret_cast<half4_t*>(&Us[0][nc][c][16 * w + 4 * g]) = half4_t{ua[0], ua[1], ub[0], ub[1]};
-      *reinterpret_cast<half4_t*>(&Us[1][nc][c][16 * w + 4 * g]) = hi;
-      *reinterpret_cast<half4_t*>(&Us[2][nc][c][16 * w + 4 * g]) = lo;
+      half4_t uh, ul;
+      split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, uh, ul, one);
+      *reinterpret_cast<half4_t*>(&lds.U[1][nc][c][16 * w + 4 * g]) = uh;
+      *reinterpret_cast<half4_t*>(&lds.U[2][nc][c][16 * w + 4 * g]) = ul;
+      *reinterpret_cast<half4_t*>(&lds.U[0][nc][c][16 * w + 4 * g]) = half4_t{ua[0], ua[1], ub[0], ub[1]};
     }
     lds_barrier();
-    // the state behind the block
+    if (TILES == 8) {
+      update(kt, s.whole.x, ratio);
+      write_state();
+    }
+    write_top(next, b + 1);
+    lds_barrier();
+  }
+
+  __device__ __forceinline__ void solve() {
+    uint32_t v_at[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v_at[r] = (uint32_t)((16 * w + 4 * g + r) * (uint32_t)a.v_tok + c) * 2;
+    SolveStage<KS, NC> s0, s1, s2;
+    load(s0, 0, v_at);
+    load(s1, 1, v_at);
+    load(s2, 2, v_at);
+    open();
+    write_top(s0, 0);
+    lds_barrier();
+    int b = 0;
+    for (; b + 2 < blocks; b += 3) {
+      solve_block(s0, s1, b);
+      load(s0, b + 3, v_at);
+      solve_block(s1, s2, b + 1);
+      load(s1, b + 4, v_at);
+      solve_block(s2, s0, b + 2);
+      load(s2, b + 5, v_at);
+    }
+    if (b < blocks) solve_block(s0, s1, b);
+    if (b + 1 < blocks) solve_block(s1, s1, b + 1);
+  }
+
+  // The outputs of a block from its Q S and the updates in LDS.
+  __device__ __forceinline__ void store_out(const OutStage<KS>& s, const f32x4_t (&y)[NC], const float (&ratio)[NC], int b,
+                                            const uint32_t (&o_at)[4]) const {
+    const int o = w - 4;
+    const float e[4] = {s.e.x, s.e.y, s.e.z, s.e.w};
+    const __amdgpu_buffer_rsrc_t out = buffer(a.out, a.o_tok, a.o_head, b);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
+      f32x4_t x;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) S[rt][nc] *= s.decay;
-      bound[nc] = __builtin_fmaf(s.decay, bound[nc], sums[nc]) * 1.00001f;
-    }
-    typedef short s16x4_t __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      half8_t kt[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        // transposing read: lane i of 16 addresses 4 channels of token i / 4 and gets channel i of 4 tokens
-        half4_t p[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          p[i] = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4_t*)&Ks[buf][ks * 32 + g * 8 + i * 4 + (c >> 2)][(w * RT + rt) * 16 + (c & 3) * 4]));
-        kt[rt] = half8_t{p[0][0], p[0][1], p[0][2], p[0][3], p[1][0], p[1][1], p[1][2], p[1][3]};
-      }
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const half8_t hi = *reinterpret_cast<const half8_t*>(&Us[1][nc][c][ks * 32 + g * 8]);
-        const half8_t lo = *reinterpret_cast<const half8_t*>(&Us[2][nc][c][ks * 32 + g * 8]);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          S[rt][nc] = mfma(kt[rt], hi, S[rt][nc]);
-          S[rt][nc] = mfma(kt[rt], lo, S[rt][nc]);
-        }
-      }
-    }
-    float down_now[NC];
-    bad = false;
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) down_now[nc] = down[nc];
-    if (b + 1 < blocks) {
-      bad = next.bad != 0.0f;
-      read_sums(sums, buf ^ 1);
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        set_unit(nc);
-        const float ratio = down_now[nc] * up[nc];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) S[rt][nc] *= ratio;
-      }
-      write_state(S);
-    }
-    // the outputs
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      const float e[4] = {s.e.x, s.e.y, s.e.z, s.e.w};
-      f32x4_t o;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = e[r] * Y[nc][r];
+      for (int r = 0; r < 4; ++r) x[r] = e[r] * ratio[nc] * y[nc][r];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks <= (w >> 1)) o = mfma(s.a[ks], *reinterpret_cast<const half8_t*>(&Us[0][nc][c][ks * 32 + g * 8]), o);
+        if (ks <= (o >> 1)) x = mfma(s.a[ks], *reinterpret_cast<const half8_t*>(&lds.U[0][nc][c][ks * 32 + g * 8]), x);
+      const float f = down[nc] * a.scale;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = b * kTok + 16 * w + 4 * g + r;
-        if (t < n)
-          a.out[(int64_t)(rows.first + t) * a.o_tok + head * a.o_head + c0 + nc * 16 + c] =
-              (uint16_t)bf16_pair(o[r] * down_now[nc] * a.scale, 0.0f);
+      for (int r = 0; r < 4; r += 2) {
+        const uint32_t two = bf16_pair(x[r] * f, x[r + 1] * f);
+        __builtin_amdgcn_raw_buffer_store_b16((short)two, out, o_at[r], nc * 32, 0);
+        __builtin_amdgcn_raw_buffer_store_b16((short)(two >> 16), out, o_at[r + 1], nc * 32, 0);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void out_block(const OutStage<KS>& s, int b, const uint32_t (&o_at)[4]) {
+    float up[NC], ratio[NC];
+    open_block(b, s.whole, up, ratio);
+    f32x4_t y[NC];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      y[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        y[nc] = mfma(s.q[ks], *reinterpret_cast<const half8_t*>(&lds.S[0][nc][c][ks * 32 + g * 8]), y[nc]);
+    }
+    lds_barrier();
+    half8_t kt[2];
+    read_kt(kt, b);
+    lds_barrier();
+    update(kt, s.whole.x, ratio);
+    write_state();
+    lds_barrier();
+    store_out(s, y, ratio, b, o_at);           // while the others are at the next block's K S
+  }
+
+  __device__ __forceinline__ void output() {
+    uint32_t o_at[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o_at[r] = (uint32_t)((16 * (w - 4) + 4 * g + r) * (uint32_t)a.o_tok + c) * 2;
+    OutStage<KS> s0, s1, s2;
+    load(s0, 0);
+    load(s1, 1);
+    load(s2, 2);
+    open();
+    lds_barrier();
+    int b = 0;
+    for (; b + 2 < blocks; b += 3) {
+      out_block(s0, b, o_at);
+      load(s0, b + 3);
+      out_block(s1, b + 1, o_at);
+      load(s1, b + 4);
+      out_block(s2, b + 2, o_at);
+      load(s2, b + 5);
+    }
+    if (b < blocks) out_block(s0, b, o_at);
+    if (b + 1 < blocks) out_block(s1, b + 1, o_at);
+  }
+
+  // Reads the state in; one barrier inside, one is due behind it.
+  __device__ __forceinline__ void open() {
+    const int slot = seq_slot(a.s, seq);
+    const bool old = slot >= 0 && scalar_load(a.s.kv_len + seq) > n;
+    if (threadIdx.x < 3 * NC * 16) (&lds.top[0][0])[threadIdx.x] = 0;
+    if (owner()) {
+      const float* p = state(slot);
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        float m = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          S[nc][r] = old ? p[(int64_t)r * a.v_dim + nc * 16] : 0.0f;
+          m += __builtin_fabsf(S[nc][r]);
+        }
+        m = quad_sum(m);
+        if (g == 0) lds.norm[tile()][nc * 16 + c] = m;
       }
     }
     lds_barrier();
-    return __builtin_amdgcn_ballot_w64(bad) == 0;
-  };
-  for (int b = 0; b < blocks; b += 2) {
-    bool good = block_step(s0, s1, b);
-    if (good && b + 1 < blocks) {
-      load(s0, b + 2);
-      good = block_step(s1, s0, b + 1);
-      if (good) load(s1, b + 3);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      bound[nc] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) bound[nc] += lds.norm[i][nc * 16 + c];
+      float up;
+      unit(bound[nc], up, state_down[nc]);
+      S[nc] *= up;
     }
-    if (!good) {
-      if (threadIdx.x < NC) flag[threadIdx.x] = 1;
-      return;
-    }
+    write_state();
   }
-  if (threadIdx.x < NC) flag[threadIdx.x] = 0;
-  if (slot < 0) return;
+  __device__ __forceinline__ float* state(int slot) const {
+    return static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
+           ((int64_t)head * DK + tile() * 16 + 4 * g) * a.v_dim + c0 + c;
+  }
+  __device__ __forceinline__ void close() const {
+    const int slot = seq_slot(a.s, seq), slice = c0 / 16;
+    const bool left = __builtin_amdgcn_ballot_w64(bad) != 0;
+    uint8_t* flag = ws.flags + ((int64_t)seq * a.v_heads + head) * (a.v_dim / 16) + slice;
+    if (threadIdx.x < NC) flag[threadIdx.x] = left;
+    if (slot < 0 || left || !owner()) return;
+    float* p = state(slot);
 #pragma unroll
-  for (int nc = 0; nc < NC; ++nc)
+    for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) state[(int64_t)(rt * 16 + r) * a.v_dim + nc * 16] = S[rt][nc][r] * down[nc];
+      for (int r = 0; r < 4; ++r) p[(int64_t)r * a.v_dim + nc * 16] = S[nc][r] * state_down[nc];
+  }
+};
+
+template <int DK, int NC>
+__global__ __launch_bounds__(kScanThreads) void chunk_scan_kernel(DeltaArgs a, ChunkWork ws) {
+  __shared__ __attribute__((aligned(16))) typename Scan<DK, NC>::Lds lds;
+  // a key head's workgroups share its K, Q and their value head's T, A: all on one XCD (workgroup i runs on XCD i mod 8)
+  const int group = a.v_heads / a.k_heads, slices = a.v_dim / (16 * NC), per_pair = group * slices;
+  const int j = blockIdx.x >> 3;
+  const int pair = (j / per_pair) * 8 + (blockIdx.x & 7), part = j % per_pair;
+  const int seq = pair / a.k_heads, k_head = pair - seq * a.k_heads;
+  if (seq >= a.s.num_seqs) return;
+  Scan<DK, NC> scan(a, ws, lds, seq, k_head * group + part / slices, k_head, part % slices * 16 * NC);
+  scan.rows = seq_rows(a.s, seq);
+  scan.n = scan.rows.end - scan.rows.first;
+  if (scan.n <= ws.short_len) return;
+  scan.blocks = (scan.n + kTok - 1) / kTok;
+  scan.slot0 = scan.rows.first / kTok + seq;
+  if (scan.w < 4)
+    scan.solve();
+  else
+    scan.output();
+  scan.close();
 }
 
 template <int DK>
 int launch_dk(const DeltaArgs& a, const ChunkWork& ws, hipStream_t stream) {
-  constexpr int NC = 2;
+  constexpr int NC = 1;
   const int64_t prepare = ws.blocks * a.k_heads;
   const int64_t units = (int64_t)a.s.num_seqs * a.k_heads;
   const int64_t scan = (units + 7) / 8 * 8 * (a.v_heads / a.k_heads) * (a.v_dim / (16 * NC));
-  if (prepare * kThreads > (int64_t)UINT32_MAX || scan * kThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  if (prepare * kThreads > (int64_t)UINT32_MAX || scan * kScanThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;
   chunk_prepare_kernel<DK><<<(unsigned)prepare, kThreads, 0, stream>>>(a, ws);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-  chunk_scan_kernel<DK, NC><<<(unsigned)scan, kThreads, 0, stream>>>(a, ws);
+  chunk_scan_kernel<DK, NC><<<(unsigned)scan, kScanThreads, 0, stream>>>(a, ws);
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 

@@ -93,6 +93,7 @@ def test_gated_delta_rule_argument_errors(nv):
         assert call(**kw) == 1, kw
     for kw in (dict(dk=32), dict(dk=96), dict(dk=256), dict(dv=48), dict(dv=544), dict(T=1 << 30)):
         assert call(**kw) == 2, kw
+    assert call(v=heads(nv, tok=1 << 24)) == 2 and call(out=heads(nv, tok=1 << 24)) == 2
     assert call(T=0) == 0 and call(states(nv, num_seqs=0, cu_q=None)) == 0
     assert nv.lib.nvfp4_gated_delta_rule(None, 5, 0, 128, 128, heads(nv), heads(nv), heads(nv), A16, A16, 0.1, heads(nv), A16, 1 << 40, None) == 1
 
