@@ -75,13 +75,19 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 
 // One row of q or k as fp16 fragments, scaled by a power of two to a largest element in [2, 4): lane (row, part) holds
-// elements ks * 32 + part * 8 .. + 7.  Returns the factor that makes the scaled row a unit row, 1 / (sc sqrt(x.x + 1e-6)).
+// elements 32 ks + 4 part .. + 3 and 32 ks + 16 + 4 part .. + 3: the rows that a lane holds of two 16-row results, so that
+// the state can be the other operand as it is.  Returns the factor that makes the scaled row a unit row, 1 / (sc sqrt(x.x + 1e-6)).
 template <int KS>
 __device__ __forceinline__ float row_frags(const uint16_t* p, int part, bool live, half8_t (&f)[KS], bool& bad) {
   uint4 raw[KS];
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks)
-    raw[ks] = live ? *reinterpret_cast<const uint4*>(p + ks * 32 + part * 8) : make_uint4(0, 0, 0, 0);
+    if (live) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p + ks * 32 + part * 4), y = *reinterpret_cast<const uint2*>(p + ks * 32 + 16 + part * 4);
+      raw[ks] = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
+      raw[ks] = make_uint4(0, 0, 0, 0);
+    }
   uint32_t top = 0;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) top = max(top, max_abs_bits(raw[ks], static_cast<const uint16_t*>(nullptr)));
@@ -203,10 +209,7 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
       f[kTok + lane] = beta * since * rk[lane];
       f[2 * kTok + lane] = expf((float)(total - sum)) * rk[lane];
       f[3 * kTok + lane] = since * rq[lane];
-      if (lane < 8) {
-        f[4 * kTok + 2 * lane] = expf((float)total);
-        f[4 * kTok + 2 * lane + 1] = bad_head ? 1.0f : 0.0f;
-      }
+      if (lane < 16) f[4 * kTok + lane] = bad_head ? __builtin_nanf("") : expf((float)total);
     }
     double row_sum[4];
     float row_k[4], row_q[4];
@@ -314,23 +317,28 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
 
 constexpr int kScanThreads = 512;
 
-// What a wavefront of the solving half needs of one block, and one of the output half.
-template <int KS, int NC>
-struct SolveStage {
-  half8_t k[KS], t_hi[2], t_lo[2];
-  float4 beta, c, d;               // factors of rows 4 g .. 4 g + 3 of its 16 tokens
-  float2 whole;                    // the block's decay, and whether it is out of the scale's premise
-  uint32_t v[NC][4];               // bf16 values of those rows
+// What a wavefront of the solving half needs of one block: what other workgroups of its XCD read too, and its own rows,
+// which come from farther and are wanted earlier (their largest value a block ahead).
+struct SolveShared {
+  half8_t k[4], t_hi[2], t_lo[2];  // k: 32 channels of all 64 tokens
+  float4 d;                        // factors of rows 4 g .. 4 g + 3 of its 16 tokens
 };
+template <int NC>
+struct SolveRows {
+  float4 beta, c;
+  float decay;                     // of the whole block; NaN where it is out of the scale's premise
+  uint32_t v[NC][4];               // bf16 values of those rows, columns c and its neighbour
+};
+// What one of the output half needs.
 template <int KS>
 struct OutStage {
-  half8_t q[KS], a[2];
-  float4 e;
-  float2 whole;
+  half8_t q[KS], a[2];             // 16 tokens
+  float e;                         // factor of token c
 };
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 template <typename T>
 __device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
@@ -338,19 +346,24 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
 }
 
 // The scan: one workgroup per sequence, value head and slice of 16 NC state columns; eight wavefronts that walk along
-// the sequence together, three barriers a block.  Four solve for the updates (16 tokens each: X = K S, R, U = T R), four
-// make the outputs (Q S while the others do K S, A U while those are at the next block); all update the state, 16 rows
-// of it in the registers of each wavefront that has some.  S, R and U meet the others in LDS.
+// the sequence together, three barriers a block.
+//   Solving half (4 wavefronts): wavefront w keeps rows 32 w .. 32 w + 31 of the state in registers, as the second operand
+//   of K S just as the last update left them.  K S over its channels for all tokens; barrier; the sum over the
+//   wavefronts for tokens 16 w .. 16 w + 15, R; barrier; U = T R; barrier; its rows' update.
+//   Output half: Q S of 16 tokens each while the others solve, A U and the stores while they are at the next block.
 template <int DK, int NC>
 struct Scan {
-  static constexpr int KS = DK / 32, TILES = DK / 16;
+  static constexpr int KS = DK / 32;
   struct Lds {
-    _Float16 S[2][NC][16][DK + 8];
+    f32x4_t X[KS][4][NC][64];                  // K S of a wavefront's channels, 16 tokens each
+    half8_t S[NC][KS][64];                     // the state's upper part, as an operand
     _Float16 R[2][NC][16][kTok + 8];
-    _Float16 U[3][NC][16][kTok + 8];           // U, then its product with the decays to the block's end in two parts
-    _Float16 K[2][kTok][DK + 16];
-    float norm[8][NC * 16];
+    _Float16 U[2][NC][16][kTok + 8];           // U times the decays to the block's end, in two parts
+    _Float16 O[2][NC][16][kTok + 8];           // U for the outputs, of two blocks
+    _Float16 K[KS][kTok][40];                  // a wavefront's channels of K, for their transposition
+    float norm[KS][NC * 16];
     uint32_t top[3][NC * 16];                  // largest |beta v| of a block, as bits
+    float units[2][2][NC * 16];                // for the output half: ratio, and the block's unit times the scale
   };
 
   const DeltaArgs& a;
@@ -359,19 +372,11 @@ struct Scan {
   const int lane, w, c, g, seq, head, k_head, c0;
   SeqRows rows;
   int n, blocks, slot0;
-  f32x4_t S[NC];
-  float bound[NC], down[NC];                   // of a column: its norm's bound, the block's unit
-  float state_down[NC], to_state[NC];          // the unit of S between blocks, and the block's in terms of it
-  bool bad = false;
   const float one = hidden_one();
 
   __device__ Scan(const DeltaArgs& args, const ChunkWork& work, Lds& shared, int seq_, int head_, int k_head_, int c0_)
       : a(args), ws(work), lds(shared), lane(threadIdx.x & 63), w(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
         c(lane & 15), g(lane >> 4), seq(seq_), head(head_), k_head(k_head_), c0(c0_) {}
-
-  // The state's tile of this wavefront; the solving half has none if there are only four.
-  __device__ __forceinline__ int tile() const { return TILES == 8 ? w : w - 4; }
-  __device__ __forceinline__ bool owner() const { return tile() >= 0; }
 
   __device__ __forceinline__ const char* at(const void* base, int block, int heads, int h, int bytes) const {
     return static_cast<const char*>(base) + ((int64_t)(slot0 + block) * heads + h) * bytes;
@@ -387,13 +392,57 @@ struct Scan {
                                              0x00027000);
   }
 
+  // Four values of two results' rows as one operand, in two parts.
+  __device__ __forceinline__ void operand(const f32x4_t& x, const f32x4_t& y, half8_t& hi, half8_t& lo) const {
+    half4_t a0, b0, a1, b1;
+    split4(x, a0, b0, one);
+    split4(y, a1, b1, one);
+    hi = half8_t{a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+    lo = half8_t{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
+  }
+
+  // The power of two that takes x < 2^100 below 2^13, and its inverse.
+  __device__ __forceinline__ static void unit(float x, float& up, float& down) {
+    const uint32_t e = max(min(__float_as_uint(x) >> 23, 226u), 20u);
+    up = __uint_as_float((266u - e) << 23);
+    down = __uint_as_float((e - 12u) << 23);
+  }
+
+  // ---- the solving half
+
+  f32x4_t S[2][NC];                            // rows 32 w + 16 i + 4 g + r of column c
+  // Of a column: its norm's bound and the unit of S behind the block; the block's unit and its inverse, and the ratios
+  // from the state's unit to the block's and back.
+  float bound[NC], state_unit[NC], up[NC], ratio[NC], to_state[NC];
+  float last_unit[NC];                         // of S as it is between blocks
+  bool bad = false;
+  uint32_t v_at[4], v_shift;                   // byte offsets of its values in a block, their place in a word
+
+  __device__ __forceinline__ bool owner() const { return KS == 4 || w < KS; }
+
   // Loads are straight-line and the same every time (past the end: the last block again), so that the waits in the
   // loop count on exactly what was issued since.
-  __device__ __forceinline__ void load(SolveStage<KS, NC>& s, int block, const uint32_t (&v_at)[4]) const {
-    const int b = min(block, blocks - 1);
-    const char* kp = at(ws.k, b, a.k_heads, k_head, 4 * KS * 1024);
+  __device__ __forceinline__ void load_k(SolveShared& s, int block) const {
+    const char* kp = at(ws.k, min(block, blocks - 1), a.k_heads, k_head, 4 * KS * 1024);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) s.k[ks] = load_at<half8_t>(kp, ((w * KS + ks) * 64 + lane) * 16);
+    for (int j = 0; j < 4; ++j) s.k[j] = load_at<half8_t>(kp, ((j * KS + w % KS) * 64 + lane) * 16);
+  }
+  __device__ __forceinline__ void load_rows(SolveRows<NC>& s, int block) const {
+    const int b = min(block, blocks - 1);
+    const char* f = factors(b);
+    const uint32_t row = (16 * w + 4 * g) * 4;
+    s.beta = load_at<float4>(f, row);
+    s.c = load_at<float4>(f, row + kTok * 4);
+    // one copy for each of 16 lanes: as a scalar load, every wait on LDS would wait for it
+    s.decay = load_at<float>(f, 4 * kTok * 4 + 4 * c);
+    const __amdgpu_buffer_rsrc_t v = buffer(a.v, a.v_tok, a.v_head, b);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s.v[nc][r] = __builtin_amdgcn_raw_buffer_load_b32(v, v_at[r], nc * 32, 0);
+  }
+  __device__ __forceinline__ void load_t(SolveShared& s, int block) const {
+    const int b = min(block, blocks - 1);
     const char* tp = at(ws.t, b, a.v_heads, head, kTriFrags * 2048);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
@@ -401,37 +450,14 @@ struct Scan {
       s.t_hi[ks] = load_at<half8_t>(tp, frag);
       s.t_lo[ks] = load_at<half8_t>(tp, frag + 1024);
     }
-    const char* f = factors(b);
-    const uint32_t row = (16 * w + 4 * g) * 4;
-    s.beta = load_at<float4>(f, row);
-    s.c = load_at<float4>(f, row + kTok * 4);
-    s.d = load_at<float4>(f, row + 2 * kTok * 4);
-    // one copy for each of eight lanes: as a scalar load, every wait on LDS would wait for it
-    s.whole = load_at<float2>(f, 4 * kTok * 4 + 8 * (lane & 7));
-    const __amdgpu_buffer_rsrc_t v = buffer(a.v, a.v_tok, a.v_head, b);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s.v[nc][r] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(v, v_at[r], nc * 32, 0);
-  }
-  __device__ __forceinline__ void load(OutStage<KS>& s, int block) const {
-    const int b = min(block, blocks - 1), o = w - 4;
-    const char* qp = at(ws.q, b, a.k_heads, k_head, 4 * KS * 1024);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(qp, ((o * KS + ks) * 64 + lane) * 16);
-    const char* ap = at(ws.a, b, a.v_heads, head, kTriFrags * 1024);
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(ap, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
-    const char* f = factors(b);
-    s.e = load_at<float4>(f, 3 * kTok * 4 + (16 * o + 4 * g) * 4);
-    s.whole = load_at<float2>(f, 4 * kTok * 4 + 8 * (lane & 7));
+    s.d = load_at<float4>(factors(b), 2 * kTok * 4 + (16 * w + 4 * g) * 4);
   }
 
-  __device__ __forceinline__ static float value(const SolveStage<KS, NC>& s, int nc, int r) {
-    return __uint_as_float(s.v[nc][r] << 16);
+  __device__ __forceinline__ float value(const SolveRows<NC>& s, int nc, int r) const {
+    return __uint_as_float((s.v[nc][r] << v_shift) & 0xFFFF0000u);
   }
   // The largest |beta v| of the wavefront's tokens, by column, for the block's unit.
-  __device__ __forceinline__ void write_top(const SolveStage<KS, NC>& s, int block) const {
+  __device__ __forceinline__ void write_top(const SolveRows<NC>& s, int block) const {
     const float b[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w};
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
@@ -442,278 +468,331 @@ struct Scan {
     }
   }
 
-  __device__ __forceinline__ void write_state() const {
-    if (!owner()) return;
+  // Units of a block, by column, from the bound before it (one more block is opened behind the last, which sees what
+  // that one's decay says): everything in the block is below bound + 64 max|beta v|,
+  // updates below three times that.  Between blocks S has a unit by its bound alone, which follows strong decays.
+  __device__ __forceinline__ void open_block(float decay, int b) {
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      half4_t hi, lo;
-      split4(S[nc], hi, lo, one);
-      *reinterpret_cast<half4_t*>(&lds.S[0][nc][c][tile() * 16 + 4 * g]) = hi;
-      *reinterpret_cast<half4_t*>(&lds.S[1][nc][c][tile() * 16 + 4 * g]) = lo;
-    }
-  }
-
-  // The power of two that takes x < 2^100 below 2^13, and its inverse.
-  __device__ __forceinline__ static void unit(float x, float& up, float& down) {
-    const uint32_t e = max(min(__float_as_uint(x) >> 23, 226u), 20u);
-    up = __uint_as_float((266u - e) << 23);
-    down = __uint_as_float((e - 12u) << 23);
-  }
-
-  // The units of a block: everything in it is below bound + 64 max|beta v| of a column, updates below three times that.
-  // Between blocks S has a unit of its own, by its bound alone, which follows strong decays.  ratio: from the state's unit
-  // to the block's.
-  __device__ __forceinline__ void open_block(int block, float2 whole, float (&up)[NC], float (&ratio)[NC]) {
-    bad |= whole.y != 0.0f;
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      const float more = 64.0f * __uint_as_float(lds.top[block % 3][nc * 16 + c]);
-      const float most = bound[nc] + more;
+      const float more = 64.0f * __uint_as_float(lds.top[b % 3][nc * 16 + c]);
+      const float most = bound[nc] + more, was = state_unit[nc];
       bad |= !(most < 0x1p100f);
-      unit(most, up[nc], down[nc]);
-      ratio[nc] = state_down[nc] * up[nc];
-      bound[nc] = __builtin_fmaf(whole.x, bound[nc], more) * 1.00001f;
-      float state_up;
-      unit(bound[nc], state_up, state_down[nc]);
-      to_state[nc] = down[nc] * state_up;
-    }
-    if (threadIdx.x >= kScanThreads - NC * 16) lds.top[(block + 2) % 3][threadIdx.x - (kScanThreads - NC * 16)] = 0;
-  }
-
-  // Transposed K: lane i of 16 addresses 4 channels of token i / 4 and gets channel i of 4 tokens.
-  __device__ __forceinline__ void read_kt(half8_t (&kt)[2], int block) const {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      half4_t p[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        p[i] = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4_t*)&lds.K[block & 1][ks * 32 + g * 8 + i * 4 + (c >> 2)][tile() * 16 + (c & 3) * 4]));
-      kt[ks] = half8_t{p[0][0], p[0][1], p[0][2], p[0][3], p[1][0], p[1][1], p[1][2], p[1][3]};
+      float now, state_up;
+      unit(most, up[nc], now);
+      ratio[nc] = was * up[nc];
+      if (w == 3 && g == 0) {
+        lds.units[b & 1][0][nc * 16 + c] = ratio[nc];
+        lds.units[b & 1][1][nc * 16 + c] = now * a.scale;
+      }
+      bound[nc] = __builtin_fmaf(decay, bound[nc], more) * 1.00001f;
+      unit(bound[nc], state_up, state_unit[nc]);
+      to_state[nc] = now * state_up;
     }
   }
 
-  // S <- decay S + K^T U in the block's unit, then in the state's.
-  __device__ __forceinline__ void update(const half8_t (&kt)[2], float decay, const float (&ratio)[NC]) {
-    half8_t hi[NC][2], lo[NC][2];
+  // The compiler moves nothing across: memory instructions go out where the wavefront waits for LDS anyway, not in a
+  // row that would hold up the next step.
+  __device__ __forceinline__ static void here() { __builtin_amdgcn_sched_barrier(0); }
+
+  __device__ __forceinline__ void solve_block(SolveRows<NC>& s, const SolveRows<NC>& next, SolveShared& sh, int b) {
+    // this wavefront's channels of K S
+    if (owner()) {
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        f32x4_t x[4];
+        half8_t hi, lo;
+        operand(S[0][nc], S[1][nc], hi, lo);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = mfma(sh.k[j], lo, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = mfma(sh.k[j], hi, x[j]);
+        lds.S[nc][w][lane] = hi;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lds.X[w][j][nc][lane] = x[j];
+      }
+    }
+    lds_barrier();
+    f32x4_t part[KS][NC];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        hi[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.U[1][nc][c][ks * 32 + g * 8]);
-        lo[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.U[2][nc][c][ks * 32 + g * 8]);
+      for (int i = 0; i < KS; ++i) part[i][nc] = lds.X[i][w][nc][lane];
+    here();
+    if (owner()) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const half8_t k = sh.k[j];
+        *reinterpret_cast<half4_t*>(&lds.K[w][16 * j + c][4 * g]) = half4_t{k[0], k[1], k[2], k[3]};
+        *reinterpret_cast<half4_t*>(&lds.K[w][16 * j + c][16 + 4 * g]) = half4_t{k[4], k[5], k[6], k[7]};
       }
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) S[nc] *= decay * ratio[nc];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) S[nc] = mfma(kt[ks], lo[nc][ks], S[nc]);
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) S[nc] = mfma(kt[ks], hi[nc][ks], S[nc]);
     }
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) S[nc] *= to_state[nc];
-  }
-
-  __device__ __forceinline__ void solve_block(const SolveStage<KS, NC>& s, const SolveStage<KS, NC>& next, int b) {
-    float up[NC], ratio[NC];
-    open_block(b, s.whole, up, ratio);
-    half8_t hi[NC][KS], lo[NC][KS];
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        lo[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.S[1][nc][c][ks * 32 + g * 8]);
-        hi[nc][ks] = *reinterpret_cast<const half8_t*>(&lds.S[0][nc][c][ks * 32 + g * 8]);
-      }
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<half8_t*>(&lds.K[b & 1][16 * w + c][ks * 32 + g * 8]) = s.k[ks];
+    load_k(sh, b + 2);
+    here();
     const float be[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w}, cc[4] = {s.c.x, s.c.y, s.c.z, s.c.w};
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f}, r4;
+      f32x4_t r4;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) x = mfma(s.k[ks], lo[nc][ks], x);
+      for (int i = 1; i < KS; ++i) part[0][nc] += part[i][nc];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) x = mfma(s.k[ks], hi[nc][ks], x);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) r4[r] = __builtin_fmaf(be[r] * value(s, nc, r), up[nc], -(cc[r] * ratio[nc]) * x[r]);
+      for (int r = 0; r < 4; ++r)
+        r4[r] = __builtin_fmaf(be[r] * value(s, nc, r), up[nc], -(cc[r] * ratio[nc]) * part[0][nc][r]);
       half4_t rh, rl;
       split4(r4, rh, rl, one);
       *reinterpret_cast<half4_t*>(&lds.R[0][nc][c][16 * w + 4 * g]) = rh;
       *reinterpret_cast<half4_t*>(&lds.R[1][nc][c][16 * w + 4 * g]) = rl;
     }
-    lds_barrier();
-    half8_t kt[2];
-    if (TILES == 8) read_kt(kt, b);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      f32x4_t u = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        if (ks <= (w >> 1)) {
-          const half8_t rh = *reinterpret_cast<const half8_t*>(&lds.R[0][nc][c][ks * 32 + g * 8]);
-          const half8_t rl = *reinterpret_cast<const half8_t*>(&lds.R[1][nc][c][ks * 32 + g * 8]);
-          u = mfma(s.t_lo[ks], rh, u);
-          u = mfma(s.t_hi[ks], rl, u);
-          u = mfma(s.t_hi[ks], rh, u);
-        }
-      const float d[4] = {s.d.x, s.d.y, s.d.z, s.d.w};
-      const half2_t ua = to_half2(u[0], u[1]), ub = to_half2(u[2], u[3]);
-      half4_t uh, ul;
-      split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, uh, ul, one);
-      *reinterpret_cast<half4_t*>(&lds.U[1][nc][c][16 * w + 4 * g]) = uh;
-      *reinterpret_cast<half4_t*>(&lds.U[2][nc][c][16 * w + 4 * g]) = ul;
-      *reinterpret_cast<half4_t*>(&lds.U[0][nc][c][16 * w + 4 * g]) = half4_t{ua[0], ua[1], ub[0], ub[1]};
-    }
-    lds_barrier();
-    if (TILES == 8) {
-      update(kt, s.whole.x, ratio);
-      write_state();
-    }
     write_top(next, b + 1);
     lds_barrier();
+    half8_t rh[2][NC], rl[2][NC];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        rh[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.R[0][nc][c][ks * 32 + g * 8]);
+        rl[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.R[1][nc][c][ks * 32 + g * 8]);
+      }
+    if (w == 2 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
+    const float decay = s.decay;
+    here();
+    load_rows(s, b + 3);
+    here();
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4_t u = mfma(sh.t_hi[0], rh[0][nc], zero), ul = mfma(sh.t_lo[0], rh[0][nc], zero);
+      ul = mfma(sh.t_hi[0], rl[0][nc], ul);
+      if (w >= 2) {
+        u = mfma(sh.t_hi[1], rh[1][nc], u);
+        ul = mfma(sh.t_lo[1], rh[1][nc], ul);
+        ul = mfma(sh.t_hi[1], rl[1][nc], ul);
+      }
+      u += ul;
+      const float d[4] = {sh.d.x, sh.d.y, sh.d.z, sh.d.w};
+      half4_t uh, uw;
+      split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, uh, uw, one);
+      *reinterpret_cast<half4_t*>(&lds.U[0][nc][c][16 * w + 4 * g]) = uh;
+      *reinterpret_cast<half4_t*>(&lds.U[1][nc][c][16 * w + 4 * g]) = uw;
+      const half2_t ua = to_half2(u[0], u[1]), ub = to_half2(u[2], u[3]);
+      *reinterpret_cast<half4_t*>(&lds.O[b & 1][nc][c][16 * w + 4 * g]) = half4_t{ua[0], ua[1], ub[0], ub[1]};
+    }
+    half8_t kt[2][2];
+    if (owner()) {
+      // Transposed K: lane i of 16 addresses 4 channels of token i / 4 and gets channel i of 4 tokens.
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          half4_t p[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            p[h] = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4_t*)&lds.K[w][ks * 32 + g * 8 + h * 4 + (c >> 2)][i * 16 + (c & 3) * 4]));
+          kt[ks][i] = half8_t{p[0][0], p[0][1], p[0][2], p[0][3], p[1][0], p[1][1], p[1][2], p[1][3]};
+        }
+    }
+    float back[NC];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      back[nc] = to_state[nc];
+      last_unit[nc] = state_unit[nc];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) S[i][nc] *= decay * ratio[nc];
+    }
+    lds_barrier();
+    // S <- decay S + K^T U in the block's unit, then in the state's
+    half8_t uh[2][NC], ul[2][NC];
+    if (owner()) {
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uh[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.U[0][nc][c][ks * 32 + g * 8]);
+          ul[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.U[1][nc][c][ks * 32 + g * 8]);
+        }
+    }
+    here();
+    load_t(sh, b + 2);
+    open_block(next.decay, b + 1);
+    here();
+    if (owner()) {
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) S[i][nc] = mfma(kt[ks][i], ul[ks][nc], S[i][nc]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) S[i][nc] = mfma(kt[ks][i], uh[ks][nc], S[i][nc]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) S[i][nc] *= back[nc];
+      }
+    }
   }
 
   __device__ __forceinline__ void solve() {
-    uint32_t v_at[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v_at[r] = (uint32_t)((16 * w + 4 * g + r) * (uint32_t)a.v_tok + c) * 2;
-    SolveStage<KS, NC> s0, s1, s2;
-    load(s0, 0, v_at);
-    load(s1, 1, v_at);
-    load(s2, 2, v_at);
-    open();
-    write_top(s0, 0);
-    lds_barrier();
-    int b = 0;
-    for (; b + 2 < blocks; b += 3) {
-      solve_block(s0, s1, b);
-      load(s0, b + 3, v_at);
-      solve_block(s1, s2, b + 1);
-      load(s1, b + 4, v_at);
-      solve_block(s2, s0, b + 2);
-      load(s2, b + 5, v_at);
-    }
-    if (b < blocks) solve_block(s0, s1, b);
-    if (b + 1 < blocks) solve_block(s1, s1, b + 1);
-  }
-
-  // The outputs of a block from its Q S and the updates in LDS.
-  __device__ __forceinline__ void store_out(const OutStage<KS>& s, const f32x4_t (&y)[NC], const float (&ratio)[NC], int b,
-                                            const uint32_t (&o_at)[4]) const {
-    const int o = w - 4;
-    const float e[4] = {s.e.x, s.e.y, s.e.z, s.e.w};
-    const __amdgpu_buffer_rsrc_t out = buffer(a.out, a.o_tok, a.o_head, b);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      f32x4_t x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = e[r] * ratio[nc] * y[nc][r];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        if (ks <= (o >> 1)) x = mfma(s.a[ks], *reinterpret_cast<const half8_t*>(&lds.U[0][nc][c][ks * 32 + g * 8]), x);
-      const float f = down[nc] * a.scale;
-#pragma unroll
-      for (int r = 0; r < 4; r += 2) {
-        const uint32_t two = bf16_pair(x[r] * f, x[r + 1] * f);
-        __builtin_amdgcn_raw_buffer_store_b16((short)two, out, o_at[r], nc * 32, 0);
-        __builtin_amdgcn_raw_buffer_store_b16((short)(two >> 16), out, o_at[r + 1], nc * 32, 0);
-      }
-    }
-  }
-
-  __device__ __forceinline__ void out_block(const OutStage<KS>& s, int b, const uint32_t (&o_at)[4]) {
-    float up[NC], ratio[NC];
-    open_block(b, s.whole, up, ratio);
-    f32x4_t y[NC];
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      y[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        y[nc] = mfma(s.q[ks], *reinterpret_cast<const half8_t*>(&lds.S[0][nc][c][ks * 32 + g * 8]), y[nc]);
-    }
-    lds_barrier();
-    half8_t kt[2];
-    read_kt(kt, b);
-    lds_barrier();
-    update(kt, s.whole.x, ratio);
-    write_state();
-    lds_barrier();
-    store_out(s, y, ratio, b, o_at);           // while the others are at the next block's K S
-  }
-
-  __device__ __forceinline__ void output() {
-    uint32_t o_at[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o_at[r] = (uint32_t)((16 * (w - 4) + 4 * g + r) * (uint32_t)a.o_tok + c) * 2;
-    OutStage<KS> s0, s1, s2;
-    load(s0, 0);
-    load(s1, 1);
-    load(s2, 2);
-    open();
-    lds_barrier();
-    int b = 0;
-    for (; b + 2 < blocks; b += 3) {
-      out_block(s0, b, o_at);
-      load(s0, b + 3);
-      out_block(s1, b + 1, o_at);
-      load(s1, b + 4);
-      out_block(s2, b + 2, o_at);
-      load(s2, b + 5);
-    }
-    if (b < blocks) out_block(s0, b, o_at);
-    if (b + 1 < blocks) out_block(s1, b + 1, o_at);
-  }
-
-  // Reads the state in; one barrier inside, one is due behind it.
-  __device__ __forceinline__ void open() {
+    for (int r = 0; r < 4; ++r) v_at[r] = (uint32_t)((16 * w + 4 * g + r) * (uint32_t)a.v_tok + (c & ~1)) * 2;
+    v_shift = c & 1 ? 0 : 16;
+    SolveRows<NC> s0, s1, s2;
+    SolveShared e, o;
+    load_rows(s0, 0);
+    load_k(e, 0);
+    load_t(e, 0);
+    load_rows(s1, 1);
+    load_k(o, 1);
+    load_t(o, 1);
+    load_rows(s2, 2);
     const int slot = seq_slot(a.s, seq);
     const bool old = slot >= 0 && scalar_load(a.s.kv_len + seq) > n;
-    if (threadIdx.x < 3 * NC * 16) (&lds.top[0][0])[threadIdx.x] = 0;
-    if (owner()) {
-      const float* p = state(slot);
+    float* state = static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
+                   ((int64_t)head * DK + (w % KS) * 32 + 4 * g) * a.v_dim + c0 + c;
+    if (w == 0 && lane < 3 * 16) {
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        float m = 0.0f;
+      for (int nc = 0; nc < NC; ++nc) (&lds.top[0][0])[nc * 48 + lane] = 0;
+    }
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          S[nc][r] = old ? p[(int64_t)r * a.v_dim + nc * 16] : 0.0f;
-          m += __builtin_fabsf(S[nc][r]);
+          S[i][nc][r] = old ? state[(int64_t)(16 * i + r) * a.v_dim + nc * 16] : 0.0f;
+          m += __builtin_fabsf(S[i][nc][r]);
         }
-        m = quad_sum(m);
-        if (g == 0) lds.norm[tile()][nc * 16 + c] = m;
-      }
+      m = quad_sum(m);
+      if (g == 0 && owner()) lds.norm[w][nc * 16 + c] = m;
     }
     lds_barrier();
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       bound[nc] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) bound[nc] += lds.norm[i][nc * 16 + c];
-      float up;
-      unit(bound[nc], up, state_down[nc]);
-      S[nc] *= up;
+      for (int i = 0; i < KS; ++i) bound[nc] += lds.norm[i][nc * 16 + c];
+      float state_up;
+      unit(bound[nc], state_up, state_unit[nc]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) S[i][nc] *= state_up;
     }
-    write_state();
-  }
-  __device__ __forceinline__ float* state(int slot) const {
-    return static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
-           ((int64_t)head * DK + tile() * 16 + 4 * g) * a.v_dim + c0 + c;
-  }
-  __device__ __forceinline__ void close() const {
-    const int slot = seq_slot(a.s, seq), slice = c0 / 16;
+    write_top(s0, 0);
+    lds_barrier();
+    open_block(s0.decay, 0);
+    int b = 0;
+    for (; b + 5 < blocks; b += 6) {
+      solve_block(s0, s1, e, b);
+      solve_block(s1, s2, o, b + 1);
+      solve_block(s2, s0, e, b + 2);
+      solve_block(s0, s1, o, b + 3);
+      solve_block(s1, s2, e, b + 4);
+      solve_block(s2, s0, o, b + 5);
+    }
+    if (b < blocks) solve_block(s0, s1, e, b);
+    if (b + 1 < blocks) solve_block(s1, s2, o, b + 1);
+    if (b + 2 < blocks) solve_block(s2, s0, e, b + 2);
+    if (b + 3 < blocks) solve_block(s0, s1, o, b + 3);
+    if (b + 4 < blocks) solve_block(s1, s2, e, b + 4);
+    // where a block broke the scale's premise, the slice is left as it was to the kernel behind this one
     const bool left = __builtin_amdgcn_ballot_w64(bad) != 0;
-    uint8_t* flag = ws.flags + ((int64_t)seq * a.v_heads + head) * (a.v_dim / 16) + slice;
+    uint8_t* flag = ws.flags + ((int64_t)seq * a.v_heads + head) * (a.v_dim / 16) + c0 / 16;
     if (threadIdx.x < NC) flag[threadIdx.x] = left;
     if (slot < 0 || left || !owner()) return;
-    float* p = state(slot);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) p[(int64_t)r * a.v_dim + nc * 16] = S[nc][r] * state_down[nc];
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) state[(int64_t)(16 * i + r) * a.v_dim + nc * 16] = S[i][nc][r] * last_unit[nc];
+  }
+
+  // ---- the output half: results transposed, a lane holds 4 neighbouring columns of token c
+
+  __device__ __forceinline__ void load(OutStage<KS>& s, int block) const {
+    const int b = min(block, blocks - 1), o = w - 4;
+    const char* qp = at(ws.q, b, a.k_heads, k_head, 4 * KS * 1024);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(qp, ((o * KS + ks) * 64 + lane) * 16);
+    const char* ap = at(ws.a, b, a.v_heads, head, kTriFrags * 1024);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(ap, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
+    s.e = load_at<float>(factors(b), 3 * kTok * 4 + (16 * o + c) * 4);
+  }
+
+  // A U and the stores of a block, its Q S in y.
+  __device__ __forceinline__ void store_out(const OutStage<KS>& s, f32x4_t (&y)[NC], const float4 (&scale)[NC], int b,
+                                            uint32_t o_at) const {
+    const int o = w - 4;
+    const __amdgpu_buffer_rsrc_t out = buffer(a.out, a.o_tok, a.o_head, b);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+        if (ks <= (o >> 1))
+          y[nc] = mfma(*reinterpret_cast<const half8_t*>(&lds.O[b & 1][nc][c][ks * 32 + g * 8]), s.a[ks], y[nc]);
+      const u32x2_t two = {bf16_pair(y[nc][0] * scale[nc].x, y[nc][1] * scale[nc].y),
+                           bf16_pair(y[nc][2] * scale[nc].z, y[nc][3] * scale[nc].w)};
+      __builtin_amdgcn_raw_buffer_store_b64(two, out, o_at, nc * 32, 0);
+    }
+  }
+
+  // Q S of block b beside its K S' exchange; the block before it is finished beside this one's U.
+  __device__ __forceinline__ void out_block(OutStage<KS>& s, OutStage<KS>& last, f32x4_t (&y)[NC], float4 (&scale)[NC], int b,
+                                            uint32_t o_at) const {
+    lds_barrier();
+    f32x4_t q[NC];
+    float4 ratio[NC], now[NC];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      q[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) q[nc] = mfma(lds.S[nc][ks][lane], s.q[ks], q[nc]);
+      ratio[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][0][nc * 16 + 4 * g]);
+      now[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][1][nc * 16 + 4 * g]);
+    }
+    lds_barrier();
+    if (b > 0) {
+      store_out(last, y, scale, b - 1, o_at);
+    }
+    load(last, b + 2);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      y[nc][0] = q[nc][0] * (s.e * ratio[nc].x);
+      y[nc][1] = q[nc][1] * (s.e * ratio[nc].y);
+      y[nc][2] = q[nc][2] * (s.e * ratio[nc].z);
+      y[nc][3] = q[nc][3] * (s.e * ratio[nc].w);
+      scale[nc] = now[nc];
+    }
+    lds_barrier();
+  }
+
+  __device__ __forceinline__ void output() const {
+    const uint32_t o_at = (uint32_t)((16 * (w - 4) + c) * (uint32_t)a.o_tok + 4 * g) * 2;
+    OutStage<KS> s0, s1, s2;
+    f32x4_t y[NC];
+    float4 scale[NC];
+    load(s0, 0);
+    load(s1, 1);
+    load(s2, 2);
+    lds_barrier();
+    lds_barrier();
+    int b = 0;
+    for (; b + 2 < blocks; b += 3) {
+      out_block(s0, s2, y, scale, b, o_at);
+      out_block(s1, s0, y, scale, b + 1, o_at);
+      out_block(s2, s1, y, scale, b + 2, o_at);
+    }
+    if (b == blocks) {
+      store_out(s2, y, scale, b - 1, o_at);
+    } else {
+      out_block(s0, s2, y, scale, b, o_at);
+      if (b + 1 == blocks) {
+        store_out(s0, y, scale, b, o_at);
+      } else {
+        out_block(s1, s0, y, scale, b + 1, o_at);
+        store_out(s1, y, scale, b + 1, o_at);
+      }
+    }
   }
 };
 
@@ -736,7 +815,6 @@ __global__ __launch_bounds__(kScanThreads) void chunk_scan_kernel(DeltaArgs a, C
     scan.solve();
   else
     scan.output();
-  scan.close();
 }
 
 template <int DK>
