@@ -215,10 +215,11 @@ def build(verbose: bool = False) -> str:
     calib_objs = [obj(s) for s in CALIB_SOURCES]
     cmds = [[hipcc(), *HIPCC_FLAGS, *inc, "-c", os.path.join(CSRC, s), "-o", obj(s)]
             for s in SOURCES + CALIB_SOURCES]
-    # The GEMM's device assembly, for the M0 check below.
-    gemm_s = os.path.join(objdir, "gemm.s")
-    cmds.append([hipcc(), *HIPCC_FLAGS, *inc, "--cuda-device-only", "-S", os.path.join(CSRC, "gemm.hip"),
-                 "-o", gemm_s])
+    # The device assembly of the files with direct-to-LDS copies, for the checks below.
+    listings = [os.path.join(objdir, f + ".s") for f in ("gemm", "gdn_chunk")]
+    for s in listings:
+        src = os.path.join(CSRC, os.path.basename(s)[:-2] + ".hip")
+        cmds.append([hipcc(), *HIPCC_FLAGS, *inc, "--cuda-device-only", "-S", src, "-o", s])
     with ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 1)) as pool:
         results = list(pool.map(lambda c: _run(c, verbose), cmds))
     for cmd, res in zip(cmds, results):
@@ -227,10 +228,12 @@ def build(verbose: bool = False) -> str:
             raise RuntimeError(f"hipcc failed ({res.returncode}) on {cmd[-3]}:\n{err}")
         if verbose and err.strip():
             print(err, file=sys.stderr)
-    with open(gemm_s) as f:
-        text = f.read()
-    check_m0(text)
-    check_lds_refills(text)
+    for s in listings:
+        with open(s) as f:
+            text = f.read()
+        check_m0(text)
+        if s == listings[0]:
+            check_lds_refills(text)
     for lib, o in ((LIB, objs), (CALIB_LIB, calib_objs)):
         tmp = lib + ".tmp"
         res = _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *o, "-o", tmp], verbose)

@@ -317,24 +317,34 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
 
 constexpr int kScanThreads = 512;
 
-// What a wavefront of the solving half needs of one block: what other workgroups of its XCD read too, and its own rows,
-// which come from farther and are wanted earlier (their largest value a block ahead).
-struct SolveShared {
+// What a wavefront of the solving half needs of one block in registers, and one of the output half.
+struct SolveStage {
   half8_t k[4], t_hi[2], t_lo[2];  // k: 32 channels of all 64 tokens
-  float4 d;                        // factors of rows 4 g .. 4 g + 3 of its 16 tokens
 };
-template <int NC>
-struct SolveRows {
-  float4 beta, c;
-  float decay;                     // of the whole block; NaN where it is out of the scale's premise
-  uint32_t v[NC][4];               // bf16 values of those rows, columns c and its neighbour
-};
-// What one of the output half needs.
 template <int KS>
 struct OutStage {
   half8_t q[KS], a[2];             // 16 tokens
-  float e;                         // factor of token c
 };
+
+// Values and row factors wait in LDS from six blocks ahead on: they come from memory, not from other workgroups' reads.
+constexpr int kAhead = 6, kRing = 8;
+
+// Copies 16 B (4 B) a lane from memory to LDS, lane l's to dst + 16 l (4 l): base + off, base and dst the same for all
+// lanes.  From inline assembly, so that the compiler does not make every later LDS read wait for it; the copies write
+// no registers, and the kernel orders them itself: they are issued behind a barrier that follows every read of what
+// they overwrite, waited for by count and published with a barrier.  Nothing else in this file uses M0, which the build
+// checks on the generated assembly.
+typedef __attribute__((address_space(3))) void lds_void_t;
+__device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, const void* dst) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t*)dst);
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
+}
+__device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, const void* dst) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t*)dst);
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
+}
+// s_waitcnt immediate that waits for at most n outstanding vector memory operations.
+constexpr int vmcnt_imm(int n) { return (n & 15) | 0x0F70 | ((n >> 4) << 14); }
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
@@ -361,6 +371,10 @@ struct Scan {
     _Float16 U[2][NC][16][kTok + 8];           // U times the decays to the block's end, in two parts
     _Float16 O[2][NC][16][kTok + 8];           // U for the outputs, of two blocks
     _Float16 K[KS][kTok][40];                  // a wavefront's channels of K, for their transposition
+    uint16_t V[kRing][kTok][16 * NC];          // values
+    float rows[kRing][4][kTok];                // row factors: beta, c, d, e
+    float decay[kRing][64];                    // of the whole block, copies; NaN where it is out of the scale's premise
+    float unused[4][64];                       // where copies go that only bring lines near
     float norm[KS][NC * 16];
     uint32_t top[3][NC * 16];                  // largest |beta v| of a block, as bits
     float units[2][2][NC * 16];                // for the output half: ratio, and the block's unit times the scale
@@ -416,62 +430,31 @@ struct Scan {
   float bound[NC], state_unit[NC], up[NC], ratio[NC], to_state[NC];
   float last_unit[NC];                         // of S as it is between blocks
   bool bad = false;
-  uint32_t v_at[4], v_shift;                   // byte offsets of its values in a block, their place in a word
 
   __device__ __forceinline__ bool owner() const { return KS == 4 || w < KS; }
 
   // Loads are straight-line and the same every time (past the end: the last block again), so that the waits in the
   // loop count on exactly what was issued since.
-  __device__ __forceinline__ void load_k(SolveShared& s, int block) const {
+  __device__ __forceinline__ void load_k(SolveStage& s, int block) const {
     const char* kp = at(ws.k, min(block, blocks - 1), a.k_heads, k_head, 4 * KS * 1024);
 #pragma unroll
     for (int j = 0; j < 4; ++j) s.k[j] = load_at<half8_t>(kp, ((j * KS + w % KS) * 64 + lane) * 16);
   }
-  __device__ __forceinline__ void load_rows(SolveRows<NC>& s, int block) const {
-    const int b = min(block, blocks - 1);
-    const char* f = factors(b);
-    const uint32_t row = (16 * w + 4 * g) * 4;
-    s.beta = load_at<float4>(f, row);
-    s.c = load_at<float4>(f, row + kTok * 4);
-    // one copy for each of 16 lanes: as a scalar load, every wait on LDS would wait for it
-    s.decay = load_at<float>(f, 4 * kTok * 4 + 4 * c);
-    const __amdgpu_buffer_rsrc_t v = buffer(a.v, a.v_tok, a.v_head, b);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s.v[nc][r] = __builtin_amdgcn_raw_buffer_load_b32(v, v_at[r], nc * 32, 0);
-  }
-  __device__ __forceinline__ void load_t(SolveShared& s, int block) const {
-    const int b = min(block, blocks - 1);
-    const char* tp = at(ws.t, b, a.v_heads, head, kTriFrags * 2048);
+  __device__ __forceinline__ void load_t(SolveStage& s, int block) const {
+    const char* tp = at(ws.t, min(block, blocks - 1), a.v_heads, head, kTriFrags * 2048);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const uint32_t frag = tri_frag(w, min(ks, w >> 1)) * 2048 + lane * 16;
       s.t_hi[ks] = load_at<half8_t>(tp, frag);
       s.t_lo[ks] = load_at<half8_t>(tp, frag + 1024);
     }
-    s.d = load_at<float4>(factors(b), 2 * kTok * 4 + (16 * w + 4 * g) * 4);
-  }
-
-  __device__ __forceinline__ float value(const SolveRows<NC>& s, int nc, int r) const {
-    return __uint_as_float((s.v[nc][r] << v_shift) & 0xFFFF0000u);
-  }
-  // The largest |beta v| of the wavefront's tokens, by column, for the block's unit.
-  __device__ __forceinline__ void write_top(const SolveRows<NC>& s, int block) const {
-    const float b[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w};
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      uint32_t m = 0;                          // as bits, so that a NaN is the largest
-#pragma unroll
-      for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(b[r] * value(s, nc, r)) & 0x7FFFFFFFu);
-      atomicMax(&lds.top[block % 3][nc * 16 + c], m);
-    }
   }
 
   // Units of a block, by column, from the bound before it (one more block is opened behind the last, which sees what
   // that one's decay says): everything in the block is below bound + 64 max|beta v|,
   // updates below three times that.  Between blocks S has a unit by its bound alone, which follows strong decays.
-  __device__ __forceinline__ void open_block(float decay, int b) {
+  __device__ __forceinline__ void open_block(int b) {
+    const float decay = lds.decay[b % kRing][lane];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       const float more = 64.0f * __uint_as_float(lds.top[b % 3][nc * 16 + c]);
@@ -494,7 +477,16 @@ struct Scan {
   // row that would hold up the next step.
   __device__ __forceinline__ static void here() { __builtin_amdgcn_sched_barrier(0); }
 
-  __device__ __forceinline__ void solve_block(SolveRows<NC>& s, const SolveRows<NC>& next, SolveShared& sh, int b) {
+  __device__ __forceinline__ void solve_block(SolveStage& s, int b) {
+    const int slot = b % kRing, row = 16 * w + 4 * g;
+    const float4 be = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]), cc = *reinterpret_cast<const float4*>(&lds.rows[slot][1][row]);
+    const float4 d4 = *reinterpret_cast<const float4*>(&lds.rows[slot][2][row]);
+    const float decay = lds.decay[slot][lane];
+    uint32_t v[NC][4];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[nc][r] = lds.V[slot][row + r][nc * 16 + c];
     // this wavefront's channels of K S
     if (owner()) {
 #pragma unroll
@@ -503,9 +495,9 @@ struct Scan {
         half8_t hi, lo;
         operand(S[0][nc], S[1][nc], hi, lo);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mfma(sh.k[j], lo, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], lo, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mfma(sh.k[j], hi, x[j]);
+        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], hi, x[j]);
         lds.S[nc][w][lane] = hi;
 #pragma unroll
         for (int j = 0; j < 4; ++j) lds.X[w][j][nc][lane] = x[j];
@@ -521,14 +513,14 @@ struct Scan {
     if (owner()) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const half8_t k = sh.k[j];
+        const half8_t k = s.k[j];
         *reinterpret_cast<half4_t*>(&lds.K[w][16 * j + c][4 * g]) = half4_t{k[0], k[1], k[2], k[3]};
         *reinterpret_cast<half4_t*>(&lds.K[w][16 * j + c][16 + 4 * g]) = half4_t{k[4], k[5], k[6], k[7]};
       }
     }
-    load_k(sh, b + 2);
+    load_k(s, b + 2);
     here();
-    const float be[4] = {s.beta.x, s.beta.y, s.beta.z, s.beta.w}, cc[4] = {s.c.x, s.c.y, s.c.z, s.c.w};
+    const float beta[4] = {be.x, be.y, be.z, be.w}, c4[4] = {cc.x, cc.y, cc.z, cc.w};
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       f32x4_t r4;
@@ -536,13 +528,12 @@ struct Scan {
       for (int i = 1; i < KS; ++i) part[0][nc] += part[i][nc];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        r4[r] = __builtin_fmaf(be[r] * value(s, nc, r), up[nc], -(cc[r] * ratio[nc]) * part[0][nc][r]);
+        r4[r] = __builtin_fmaf(beta[r] * __uint_as_float(v[nc][r] << 16), up[nc], -(c4[r] * ratio[nc]) * part[0][nc][r]);
       half4_t rh, rl;
       split4(r4, rh, rl, one);
       *reinterpret_cast<half4_t*>(&lds.R[0][nc][c][16 * w + 4 * g]) = rh;
       *reinterpret_cast<half4_t*>(&lds.R[1][nc][c][16 * w + 4 * g]) = rl;
     }
-    write_top(next, b + 1);
     lds_barrier();
     half8_t rh[2][NC], rl[2][NC];
 #pragma unroll
@@ -552,23 +543,19 @@ struct Scan {
         rh[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.R[0][nc][c][ks * 32 + g * 8]);
         rl[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.R[1][nc][c][ks * 32 + g * 8]);
       }
-    if (w == 2 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
-    const float decay = s.decay;
-    here();
-    load_rows(s, b + 3);
     here();
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-      f32x4_t u = mfma(sh.t_hi[0], rh[0][nc], zero), ul = mfma(sh.t_lo[0], rh[0][nc], zero);
-      ul = mfma(sh.t_hi[0], rl[0][nc], ul);
+      f32x4_t u = mfma(s.t_hi[0], rh[0][nc], zero), ul = mfma(s.t_lo[0], rh[0][nc], zero);
+      ul = mfma(s.t_hi[0], rl[0][nc], ul);
       if (w >= 2) {
-        u = mfma(sh.t_hi[1], rh[1][nc], u);
-        ul = mfma(sh.t_lo[1], rh[1][nc], ul);
-        ul = mfma(sh.t_hi[1], rl[1][nc], ul);
+        u = mfma(s.t_hi[1], rh[1][nc], u);
+        ul = mfma(s.t_lo[1], rh[1][nc], ul);
+        ul = mfma(s.t_hi[1], rl[1][nc], ul);
       }
       u += ul;
-      const float d[4] = {sh.d.x, sh.d.y, sh.d.z, sh.d.w};
+      const float d[4] = {d4.x, d4.y, d4.z, d4.w};
       half4_t uh, uw;
       split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, uh, uw, one);
       *reinterpret_cast<half4_t*>(&lds.U[0][nc][c][16 * w + 4 * g]) = uh;
@@ -612,8 +599,8 @@ struct Scan {
         }
     }
     here();
-    load_t(sh, b + 2);
-    open_block(next.decay, b + 1);
+    load_t(s, b + 2);
+    open_block(b + 1);
     here();
     if (owner()) {
 #pragma unroll
@@ -632,18 +619,11 @@ struct Scan {
   }
 
   __device__ __forceinline__ void solve() {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v_at[r] = (uint32_t)((16 * w + 4 * g + r) * (uint32_t)a.v_tok + (c & ~1)) * 2;
-    v_shift = c & 1 ? 0 : 16;
-    SolveRows<NC> s0, s1, s2;
-    SolveShared e, o;
-    load_rows(s0, 0);
-    load_k(e, 0);
-    load_t(e, 0);
-    load_rows(s1, 1);
-    load_k(o, 1);
-    load_t(o, 1);
-    load_rows(s2, 2);
+    SolveStage even, odd;
+    load_k(even, 0);
+    load_t(even, 0);
+    load_k(odd, 1);
+    load_t(odd, 1);
     const int slot = seq_slot(a.s, seq);
     const bool old = slot >= 0 && scalar_load(a.s.kv_len + seq) > n;
     float* state = static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
@@ -676,23 +656,14 @@ struct Scan {
 #pragma unroll
       for (int i = 0; i < 2; ++i) S[i][nc] *= state_up;
     }
-    write_top(s0, 0);
     lds_barrier();
-    open_block(s0.decay, 0);
+    open_block(0);
     int b = 0;
-    for (; b + 5 < blocks; b += 6) {
-      solve_block(s0, s1, e, b);
-      solve_block(s1, s2, o, b + 1);
-      solve_block(s2, s0, e, b + 2);
-      solve_block(s0, s1, o, b + 3);
-      solve_block(s1, s2, e, b + 4);
-      solve_block(s2, s0, o, b + 5);
+    for (; b + 1 < blocks; b += 2) {
+      solve_block(even, b);
+      solve_block(odd, b + 1);
     }
-    if (b < blocks) solve_block(s0, s1, e, b);
-    if (b + 1 < blocks) solve_block(s1, s2, o, b + 1);
-    if (b + 2 < blocks) solve_block(s2, s0, e, b + 2);
-    if (b + 3 < blocks) solve_block(s0, s1, o, b + 3);
-    if (b + 4 < blocks) solve_block(s1, s2, e, b + 4);
+    if (b < blocks) solve_block(even, b);
     // where a block broke the scale's premise, the slice is left as it was to the kernel behind this one
     const bool left = __builtin_amdgcn_ballot_w64(bad) != 0;
     uint8_t* flag = ws.flags + ((int64_t)seq * a.v_heads + head) * (a.v_dim / 16) + c0 / 16;
@@ -716,7 +687,40 @@ struct Scan {
     const char* ap = at(ws.a, b, a.v_heads, head, kTriFrags * 1024);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(ap, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
-    s.e = load_at<float>(factors(b), 3 * kTok * 4 + (16 * o + c) * 4);
+  }
+
+  // Starts the copies of a block's values and row factors: one or two of a wavefront.
+  __device__ __forceinline__ void copy_rows(int block) const {
+    const int slot = block % kRing, b = min(block, blocks - 1), row0 = b * kTok;
+    const uint16_t* v = a.v + (int64_t)(rows.first + row0) * a.v_tok + head * a.v_head + c0;
+#pragma unroll
+    for (int i = 0; i < 2 * NC + 2; ++i) {
+      if (i % 4 != w - 4) continue;
+      if (i < 2 * NC) {
+        // rows behind the end repeat the last one; their beta is 0
+        const int l = i * 64 + lane, row = min(l / (2 * NC), n - 1 - row0);
+        copy16_to_lds(v, (uint32_t)row * (uint32_t)a.v_tok * 2 + l % (2 * NC) * 16, reinterpret_cast<const char*>(&lds.V[slot]) + i * 1024);
+      } else if (i == 2 * NC) {
+        copy16_to_lds(factors(b), lane * 16, &lds.rows[slot]);
+      } else {
+        copy4_to_lds(factors(b), 4 * kTok * 4 + 4 * c, &lds.decay[slot]);
+      }
+    }
+  }
+
+  // The largest |beta v| of 16 tokens, by column, for the block's units.
+  __device__ __forceinline__ void write_top(int block) const {
+    const int slot = block % kRing, row = 16 * (w - 4) + 4 * g;
+    const float4 b4 = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]);
+    const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      uint32_t m = 0;                          // as bits, so that a NaN is the largest
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        m = max(m, __float_as_uint(b[r] * __uint_as_float((uint32_t)lds.V[slot][row + r][nc * 16 + c] << 16)) & 0x7FFFFFFFu);
+      atomicMax(&lds.top[block % 3][nc * 16 + c], m);
+    }
   }
 
   // A U and the stores of a block, its Q S in y.
@@ -736,63 +740,52 @@ struct Scan {
     }
   }
 
-  // Q S of block b beside its K S' exchange; the block before it is finished beside this one's U.
-  __device__ __forceinline__ void out_block(OutStage<KS>& s, OutStage<KS>& last, f32x4_t (&y)[NC], float4 (&scale)[NC], int b,
-                                            uint32_t o_at) const {
+  __device__ __forceinline__ void out_block(OutStage<KS>& s, int b, uint32_t o_at) const {
+    copy_rows(b + kAhead);
+    // the next block's copies are in: since its last one, this wavefront issued at least KS + 3 operations for each of
+    // kAhead - 1 blocks (those of the first kAhead blocks were waited for at the start)
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((kAhead - 1) * (KS + 3)));
     lds_barrier();
-    f32x4_t q[NC];
-    float4 ratio[NC], now[NC];
+    f32x4_t y[NC];
+    float4 scale[NC];
+    const float e = lds.rows[b % kRing][3][16 * (w - 4) + c];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      q[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      y[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) q[nc] = mfma(lds.S[nc][ks][lane], s.q[ks], q[nc]);
-      ratio[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][0][nc * 16 + 4 * g]);
-      now[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][1][nc * 16 + 4 * g]);
+      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(lds.S[nc][ks][lane], s.q[ks], y[nc]);
+      const float4 ratio = *reinterpret_cast<const float4*>(&lds.units[b & 1][0][nc * 16 + 4 * g]);
+      scale[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][1][nc * 16 + 4 * g]);
+      y[nc][0] *= e * ratio.x;
+      y[nc][1] *= e * ratio.y;
+      y[nc][2] *= e * ratio.z;
+      y[nc][3] *= e * ratio.w;
     }
     lds_barrier();
-    if (b > 0) {
-      store_out(last, y, scale, b - 1, o_at);
-    }
-    load(last, b + 2);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      y[nc][0] = q[nc][0] * (s.e * ratio[nc].x);
-      y[nc][1] = q[nc][1] * (s.e * ratio[nc].y);
-      y[nc][2] = q[nc][2] * (s.e * ratio[nc].z);
-      y[nc][3] = q[nc][3] * (s.e * ratio[nc].w);
-      scale[nc] = now[nc];
-    }
+    write_top(b + 1);
+    if (w == 7 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
     lds_barrier();
+    store_out(s, y, scale, b, o_at);
+    load(s, b + 2);
   }
 
   __device__ __forceinline__ void output() const {
     const uint32_t o_at = (uint32_t)((16 * (w - 4) + c) * (uint32_t)a.o_tok + 4 * g) * 2;
-    OutStage<KS> s0, s1, s2;
-    f32x4_t y[NC];
-    float4 scale[NC];
-    load(s0, 0);
-    load(s1, 1);
-    load(s2, 2);
+    OutStage<KS> even, odd;
+    for (int b = 0; b < kAhead; ++b) copy_rows(b);
+    load(even, 0);
+    load(odd, 1);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     lds_barrier();
+    write_top(0);
     lds_barrier();
     int b = 0;
-    for (; b + 2 < blocks; b += 3) {
-      out_block(s0, s2, y, scale, b, o_at);
-      out_block(s1, s0, y, scale, b + 1, o_at);
-      out_block(s2, s1, y, scale, b + 2, o_at);
+    for (; b + 1 < blocks; b += 2) {
+      out_block(even, b, o_at);
+      out_block(odd, b + 1, o_at);
     }
-    if (b == blocks) {
-      store_out(s2, y, scale, b - 1, o_at);
-    } else {
-      out_block(s0, s2, y, scale, b, o_at);
-      if (b + 1 == blocks) {
-        store_out(s0, y, scale, b, o_at);
-      } else {
-        out_block(s1, s0, y, scale, b + 1, o_at);
-        store_out(s1, y, scale, b + 1, o_at);
-      }
-    }
+    if (b < blocks) out_block(even, b, o_at);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // no copy outlives the workgroup's LDS
   }
 };
 
