@@ -16,6 +16,6 @@ struct ChunkWork {
 // Lays the workspace out from `base` on and returns its size.
 size_t chunk_workspace(int64_t tokens, int64_t num_seqs, int64_t k_heads, int64_t v_heads, int k_dim, int v_dim, void* base,
                        ChunkWork& ws);
-int launch_chunks(const DeltaArgs& a, const ChunkWork& ws, int k_dim, hipStream_t stream);
+int launch_chunks(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, int k_dim, hipStream_t stream);
 
 }  // namespace nvfp4

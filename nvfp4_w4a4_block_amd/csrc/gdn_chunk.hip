@@ -23,7 +23,6 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kTok = 64;           // tokens of a block
 
 // Workspace of one block: K and Q fragments per key head, T (two parts) and A fragments and row factors per value
@@ -74,67 +73,89 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// One row of q or k as fp16 fragments, scaled by a power of two to a largest element in [2, 4): lane (row, part) holds
-// elements 32 ks + 4 part .. + 3 and 32 ks + 16 + 4 part .. + 3: the rows that a lane holds of two 16-row results, so that
-// the state can be the other operand as it is.  Returns the factor that makes the scaled row a unit row, 1 / (sc sqrt(x.x + 1e-6)).
-template <int KS>
-__device__ __forceinline__ float row_frags(const uint16_t* p, int part, bool live, half8_t (&f)[KS], bool& bad) {
-  uint4 raw[KS];
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks)
-    if (live) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p + ks * 32 + part * 4), y = *reinterpret_cast<const uint2*>(p + ks * 32 + 16 + part * 4);
-      raw[ks] = make_uint4(x.x, x.y, y.x, y.y);
-    } else {
-      raw[ks] = make_uint4(0, 0, 0, 0);
-    }
-  uint32_t top = 0;
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) top = max(top, max_abs_bits(raw[ks], static_cast<const uint16_t*>(nullptr)));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+// The value of the lane 1 and 2 away (by xor), in the other quad of 8 and in the other half of 16: one instruction with
+// what takes it, where a general exchange goes through LDS.
+template <int CONTROL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CONTROL, 0xF, 0xF, true);
+}
+// Sum and largest over the 8 or 16 neighbouring lanes that hold a row.
+template <int LANES>
+__device__ __forceinline__ float row_total(float v) {
+  v += __uint_as_float(moved<0xB1>(__float_as_uint(v)));          // quad_perm 1 0 3 2
+  v += __uint_as_float(moved<0x4E>(__float_as_uint(v)));          // quad_perm 2 3 0 1
+  v += __uint_as_float(moved<0x141>(__float_as_uint(v)));         // mirrored in 8
+  if (LANES == 16) v += __uint_as_float(moved<0x140>(__float_as_uint(v)));   // mirrored in 16
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, moved<0xB1>(v));
+  v = max(v, moved<0x4E>(v));
+  v = max(v, moved<0x141>(v));
+  if (LANES == 16) v = max(v, moved<0x140>(v));
+  return v;
+}
+
+// 8 elements of a row of q or k as fp16, the row (DK / 8 neighbouring lanes) scaled by a power of two `sc` to a largest
+// element in [2, 4).  Returns the scaled row's squares' sum.
+template <int LANES>
+__device__ __forceinline__ float scaled_row(const uint4& raw, half8_t& f, float& sc, bool& bad) {
+  const uint32_t top = row_max<LANES>(max_abs_bits(raw, static_cast<const uint16_t*>(nullptr)));
   bad |= top >= 0x7F800000u;
   const uint32_t e = top >> 23;
-  const float sc = __uint_as_float((e == 0 ? 254u : (e >= 254u ? 1u : 255u - e)) << 23);
-  float s = 0.0f;
+  sc = __uint_as_float((e == 0 ? 254u : 255u - min(e, 254u)) << 23);
+  float s = 0.0f, v[8];
+  widen(raw, v, static_cast<const uint16_t*>(nullptr));
 #pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    float v[8];
-    widen(raw[ks], v, static_cast<const uint16_t*>(nullptr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] *= sc;
-      s = __builtin_fmaf(v[i], v[i], s);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const half2_t h = to_half2(v[2 * i], v[2 * i + 1]);
-      f[ks][2 * i] = h[0];
-      f[ks][2 * i + 1] = h[1];
-    }
+  for (int i = 0; i < 8; ++i) {
+    v[i] *= sc;
+    s = __builtin_fmaf(v[i], v[i], s);
   }
-  s = quad_sum(s);
-  if (!live) return 0.0f;
-  // neither form overflows: the scaled eps for large rows, the unscaled sum for small ones
-  if (sc < 1.0f) return 1.0f / __builtin_sqrtf(s + 1e-6f * sc * sc);
-  const float inv = 1.0f / sc;
-  return inv / __builtin_sqrtf(s * inv * inv + 1e-6f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const half2_t h = to_half2(v[2 * i], v[2 * i + 1]);
+    f[2 * i] = h[0];
+    f[2 * i + 1] = h[1];
+  }
+  return row_total<LANES>(s);
+}
+// The factor that makes a scaled row a unit row, 1 / (sc sqrt(x.x + 1e-6)).  Neither form overflows: the scaled eps for
+// large rows, the unscaled sum for small ones.
+__device__ __forceinline__ float unit_factor(float s, float sc) {
+  const float inv = 1.0f / sc;                 // a power of two
+  return sc < 1.0f ? 1.0f / __builtin_sqrtf(s + 1e-6f * sc * sc) : inv / __builtin_sqrtf(s * inv * inv + 1e-6f);
 }
 
 __device__ __forceinline__ double shfl_double(double v, int lane) { return __shfl(v, lane, 64); }
 
-// T, A and the row factors of one block for the value heads of one key head.
+// 2^x for x <= 0 by the hardware's instruction: what rounding x to fp32 costs, |x| 2^x 2^-25, stays below 2^-25.
+__device__ __forceinline__ float power2(double x) { return __builtin_amdgcn_exp2f((float)x); }
+
+// T, A and the row factors of one block for two value heads of one key head: eight wavefronts, four to a value head;
+// wavefront w of four has rows 16 w .. 16 w + 15.  K K^T and Q K^T are both halves' own work, a tenth of
+// what exchanging them would wait for.  Bound by its bytes (q, k in, fragments out) and the latency of the inverse.
+constexpr int kPrepareThreads = 512;
+
 template <int DK>
-__global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, ChunkWork ws) {
+__global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(DeltaArgs a, ChunkWork ws) {
   constexpr int KS = DK / 32;
-  __shared__ half8_t Kf[4][KS][64];
-  __shared__ float L[kTok][kTok + 4];          // L, then T
-  __shared__ float D[4][16][20];               // inverses of the diagonal blocks
-  __shared__ _Float16 At[kTok][kTok + 8];
-  __shared__ float rk[kTok], rq[kTok];
-  __shared__ int bads[4];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
-  const int block = blockIdx.x / a.k_heads, k_head = blockIdx.x - block * a.k_heads;
+  // K and Q fragments, then A (rows of 72) of both heads
+  __shared__ __attribute__((aligned(16))) char shared[2 * 4 * KS * 1024 > 2 * kTok * 144 ? 2 * 4 * KS * 1024 : 2 * kTok * 144];
+  __shared__ __attribute__((aligned(16))) float Ls[2][kTok][kTok + 4];         // L, then T
+  __shared__ __attribute__((aligned(16))) float Ds[2][4][16][20];              // inverses of the diagonal blocks
+  __shared__ float unit_k[kTok], unit_q[kTok];
+  __shared__ float sums[8][16], scales[8][16];
+  __shared__ int bads[8];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
+  const int half = wave >> 2, w = wave & 3;
+  half8_t(*Kf)[KS][64] = reinterpret_cast<half8_t(*)[KS][64]>(shared);
+  half8_t(*Qf)[KS][64] = Kf + 4;
+  const int group = a.v_heads / a.k_heads, twos = (group + 1) / 2;
+  const int block = blockIdx.x / (a.k_heads * twos), part = blockIdx.x - block * a.k_heads * twos;
+  const int k_head = part / twos, first_head = 2 * (part - k_head * twos);
+  // an odd last head: the second half repeats it and writes the same
+  const int head = k_head * group + min(first_head + half, group - 1);
   // blocks of a sequence start at slot first / 64 + seq, so that no sequence's slots meet another's
   const SeqState& st = a.s;
   const int seq = wave_search(st.num_seqs, [&](int j) {
@@ -146,70 +167,98 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
   if (n <= ws.short_len || index < 0 || index >= (n + kTok - 1) / kTok) return;
   const int m = n - index * kTok < kTok ? n - index * kTok : kTok;
   const int64_t row0 = rows.first + (int64_t)index * kTok;
-
-  half8_t kf[KS], qf[KS];
-  bool bad = false;
+  // decays and strengths come from far, too: out with the rows, used much later
+  const int64_t at = (row0 + (lane < m ? lane : 0)) * a.v_heads + head;
+  const float g_load = a.g[at], beta_load = a.beta[at];
   {
-    const int t = 16 * w + c;
-    const int64_t row = row0 + (t < m ? t : 0);
-    const float fk = row_frags<KS>(a.k + row * a.k_tok + k_head * a.k_head, g, t < m, kf, bad);
-    const float fq = row_frags<KS>(a.q + row * a.q_tok + k_head * a.q_head, g, t < m, qf, bad);
-    if (g == 0) {
-      rk[t] = fk;
-      rq[t] = fq;
-    }
-  }
-  if (lane == 0) bads[w] = 0;
-  if (__builtin_amdgcn_ballot_w64(bad) != 0 && lane == 0) bads[w] = 1;
-  half8_t* wk = reinterpret_cast<half8_t*>(ws.k) + (((int64_t)block * a.k_heads + k_head) * 4 + w) * KS * 64 + lane;
-  half8_t* wq = reinterpret_cast<half8_t*>(ws.q) + (((int64_t)block * a.k_heads + k_head) * 4 + w) * KS * 64 + lane;
+    // One half takes the rows of k, the other those of q, whole rows at a time.  Fragments, K's and Q's alike: lane (row,
+    // part) of 16 x 4 holds channels 32 ks + 4 part .. + 3 and 32 ks + 16 + 4 part .. + 3, the rows that a lane holds of
+    // two 16-row results, so that the state can be the other operand as it is.
+    constexpr int LANES = DK / 8, ROWS = 64 / LANES, LOADS = 16 / ROWS;
+    const uint16_t* x = half == 0 ? a.k + k_head * a.k_head : a.q + k_head * a.q_head;
+    const int64_t pitch = half == 0 ? a.k_tok : a.q_tok;
+    const int d = lane % LANES * 8;
+    uint4 raw[LOADS];
 #pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    Kf[w][ks][lane] = kf[ks];
-    wk[ks * 64] = kf[ks];
-    wq[ks * 64] = qf[ks];
+    for (int i = 0; i < LOADS; ++i) {
+      const int t = 16 * w + i * ROWS + lane / LANES;
+      raw[i] = *reinterpret_cast<const uint4*>(x + (row0 + min(t, m - 1)) * pitch + d);
+    }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int r = i * ROWS + lane / LANES, t = 16 * w + r;
+      half8_t f;
+      float sc;
+      const float s = scaled_row<LANES>(raw[i], f, sc, bad);
+      if (t >= m) f = half8_t{};               // rows behind the end
+      if (lane % LANES == 0) {
+        sums[wave][r] = s;
+        scales[wave][r] = sc;
+      }
+      // channels d .. d + 3 and d + 4 .. d + 7 are parts (d / 4) % 4 and the next of half (d / 16) % 2
+      half4_t* to = reinterpret_cast<half4_t*>(&Kf[half * 4 + w][d / 32][r + d / 4 % 4 * 16]) + d / 16 % 2;
+      to[0] = half4_t{f[0], f[1], f[2], f[3]};
+      to[32] = half4_t{f[4], f[5], f[6], f[7]};
+    }
+    const bool any = __builtin_amdgcn_ballot_w64(bad) != 0;
+    if (lane == 0) bads[wave] = any;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    if (lane < 16) (half == 0 ? unit_k : unit_q)[16 * w + lane] = 16 * w + lane < m ? unit_factor(sums[wave][lane], scales[wave][lane]) : 0.0f;
   }
-  __syncthreads();
+  lds_barrier();
+  if (first_head == 0) {
+    half8_t* out = reinterpret_cast<half8_t*>(half == 0 ? ws.k : ws.q) + (((int64_t)block * a.k_heads + k_head) * 4 + w) * KS * 64 + lane;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) out[ks * 64] = Kf[half * 4 + w][ks][lane];
+  }
 
-  const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4_t kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    kk[j] = zero;
-    qk[j] = zero;
-    if (j <= w) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const half8_t b = Kf[j][ks][lane];
-        kk[j] = mfma(kf[ks], b, kk[j]);
-        qk[j] = mfma(qf[ks], b, qk[j]);
-      }
-    }
+    kk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    qk[j] = kk[j];
   }
-  const bool bad_rows = (bads[0] | bads[1] | bads[2] | bads[3]) != 0;
-  const int group = a.v_heads / a.k_heads;
-  for (int h = 0; h < group; ++h) {
-    const int head = k_head * group + h;
-    // lane t: the sum of the log decays up to token t, in 64 bits: differences of far sums keep their last bits
-    const int64_t at = (row0 + (lane < m ? lane : 0)) * a.v_heads + head;
-    const float gt = lane < m ? a.g[at] : 0.0f, beta = lane < m ? a.beta[at] : 0.0f;
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    const half8_t kf = Kf[w][ks][lane], qf = Qf[w][ks][lane];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= w) {
+        const half8_t b = Kf[j][ks][lane];
+        kk[j] = mfma(kf, b, kk[j]);
+        qk[j] = mfma(qf, b, qk[j]);
+      }
+  }
+  bool bad_rows = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad_rows |= bads[i] != 0;
+  lds_barrier();                               // K and Q are read, A may take their place
+  float(*L)[kTok + 4] = Ls[half];
+  float(*D)[16][20] = Ds[half];
+  _Float16(*At)[kTok + 8] = reinterpret_cast<_Float16(*)[kTok + 8]>(shared) + half * kTok;
+
+  {
+    // lane t: the sum of the log2 decays up to token t, in 64 bits: differences of far sums keep their last bits
+    const float gt = lane < m ? g_load : 0.0f, beta = lane < m ? beta_load : 0.0f;
     const bool off = !(gt <= 0.0f && gt >= -3e38f) || !(beta >= 0.0f && beta <= 2.0f);
     const bool bad_head = bad_rows || __builtin_amdgcn_ballot_w64(off) != 0;
-    double sum = gt;
+    double sum = (double)gt * 1.4426950408889634074;
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) {
       const double other = shfl_double(sum, lane - s);
       if (lane >= s) sum += other;
     }
-    const double total = shfl_double(sum, 63);
     if (w == 0) {
+      const double total = shfl_double(sum, 63);
       float* f = ws.factors + ((int64_t)block * a.v_heads + head) * kFactors;
-      const float since = expf((float)sum);
+      const float since = power2(sum);
       f[lane] = beta;
-      f[kTok + lane] = beta * since * rk[lane];
-      f[2 * kTok + lane] = expf((float)(total - sum)) * rk[lane];
-      f[3 * kTok + lane] = since * rq[lane];
-      if (lane < 16) f[4 * kTok + lane] = bad_head ? __builtin_nanf("") : expf((float)total);
+      f[kTok + lane] = beta * since * unit_k[lane];
+      f[2 * kTok + lane] = power2(total - sum) * unit_k[lane];
+      f[3 * kTok + lane] = since * unit_q[lane];
+      if (lane < 16) f[4 * kTok + lane] = bad_head ? __builtin_nanf("") : power2(total);
     }
     double row_sum[4];
     float row_k[4], row_q[4];
@@ -217,43 +266,61 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
     for (int r = 0; r < 4; ++r) {
       const int i = 16 * w + 4 * g + r;
       row_sum[r] = shfl_double(sum, i);
-      row_k[r] = __shfl(beta, i, 64) * rk[i];
-      row_q[r] = rq[i];
+      row_k[r] = __shfl(beta, i, 64) * unit_k[i];
+      row_q[r] = unit_q[i];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j <= w) {
         const int col = 16 * j + c;
         const double col_sum = shfl_double(sum, col);
-        const float col_k = rk[col];
+        const float col_k = unit_k[col];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * w + 4 * g + r;
-          const float d = expf((float)(row_sum[r] - col_sum)) * col_k;
-          L[i][col] = i > col ? kk[j][r] * row_k[r] * d : 0.0f;
-          At[i][col] = (_Float16)(i >= col ? qk[j][r] * row_q[r] * d : 0.0f);
+          const float d = power2(row_sum[r] - col_sum) * col_k;
+          float l = kk[j][r] * row_k[r] * d, q = qk[j][r] * row_q[r] * d;
+          if (j == w) {
+            l = i > col ? l : 0.0f;
+            q = i >= col ? q : 0.0f;
+          }
+          L[i][col] = l;
+          At[i][col] = (_Float16)q;
         }
       } else if (j == w + 1 && (w & 1) == 0) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) At[16 * w + 4 * g + r][16 * j + c] = (_Float16)0.0f;
       }
     }
-    __syncthreads();
+    // the diagonal block is this wavefront's own: no barrier between its rows and their use
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
     {
-      // forward substitution for column c of this wavefront's diagonal block
+      // forward substitution for column c of the block, four known elements taken out of all later rows at once
       float x[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s = i == c ? 1.0f : 0.0f;
+      for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
 #pragma unroll
-        for (int j = 0; j < i; ++j) s = __builtin_fmaf(-L[16 * w + i][16 * w + j], x[j], s);
-        x[i] = s;
-        if ((i >> 2) == g) D[w][i][c] = s;
+      for (int jb = 0; jb < 4; ++jb) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i <= 4 * jb) continue;
+          const float4 l = *reinterpret_cast<const float4*>(&L[16 * w + i][16 * w + 4 * jb]);
+          x[i] = __builtin_fmaf(-l.x, x[4 * jb], x[i]);
+          if (i > 4 * jb + 1) x[i] = __builtin_fmaf(-l.y, x[4 * jb + 1], x[i]);
+          if (i > 4 * jb + 2) x[i] = __builtin_fmaf(-l.z, x[4 * jb + 2], x[i]);
+          if (i > 4 * jb + 3) x[i] = __builtin_fmaf(-l.w, x[4 * jb + 3], x[i]);
+          if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);         // four rows in flight, not all of them
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((i >> 2) == g) D[w][i][c] = x[i];
     }
-    __syncthreads();
+    lds_barrier();
     // this wavefront's column of blocks: T_ij = -T_ii sum_k L_ik T_kj.  A product's result has rows 4 g + r in register r,
     // which is the next one's operand if its steps take the contracted index in that order.
+    const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
     f32x4_t T[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) T[0][r] = D[w][4 * g + r][c];
@@ -277,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
         T[d] = mfma_f32(-l.w, acc[3], T[d]);
       }
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int d = 0; d < 4; ++d)
       if (w + d < 4) {
@@ -288,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
 #pragma unroll
       for (int r = 0; r < 4; ++r) L[16 * (w - 1) + 4 * g + r][16 * w + c] = 0.0f;
     }
-    __syncthreads();
+    lds_barrier();
     const int64_t frag0 = ((int64_t)block * a.v_heads + head) * kTriFrags;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
@@ -311,7 +378,6 @@ __global__ __launch_bounds__(kThreads) void chunk_prepare_kernel(DeltaArgs a, Ch
         reinterpret_cast<half8_t*>(ws.t)[(2 * frag + 1) * 64 + lane] = lo;
         reinterpret_cast<half8_t*>(ws.a)[frag * 64 + lane] = *reinterpret_cast<const half8_t*>(&At[16 * w + c][ks * 32 + g * 8]);
       }
-    __syncthreads();
   }
 }
 
@@ -810,17 +876,31 @@ __global__ __launch_bounds__(kScanThreads) void chunk_scan_kernel(DeltaArgs a, C
     scan.output();
 }
 
-template <int DK>
-int launch_dk(const DeltaArgs& a, const ChunkWork& ws, hipStream_t stream) {
-  constexpr int NC = 1;
-  const int64_t prepare = ws.blocks * a.k_heads;
-  const int64_t units = (int64_t)a.s.num_seqs * a.k_heads;
-  const int64_t scan = (units + 7) / 8 * 8 * (a.v_heads / a.k_heads) * (a.v_dim / (16 * NC));
-  if (prepare * kThreads > (int64_t)UINT32_MAX || scan * kScanThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;
-  chunk_prepare_kernel<DK><<<(unsigned)prepare, kThreads, 0, stream>>>(a, ws);
-  if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-  chunk_scan_kernel<DK, NC><<<(unsigned)scan, kScanThreads, 0, stream>>>(a, ws);
+template <int DK, int NC>
+int launch_scan(const DeltaArgs& a, const ChunkWork& ws, hipStream_t stream) {
+  const int64_t pairs = (int64_t)a.s.num_seqs * a.k_heads;
+  const int64_t grid = (pairs + 7) / 8 * 8 * (a.v_heads / a.k_heads) * (a.v_dim / (16 * NC));
+  if (grid * kScanThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;           // threads of a launch
+  chunk_scan_kernel<DK, NC><<<(unsigned)grid, kScanThreads, 0, stream>>>(a, ws);
   return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+template <int DK>
+int launch_dk(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, hipStream_t stream) {
+  DeviceInfo dev;
+  const int st = device_info(stream, dev);
+  if (st != NVFP4_OK) return st;
+  const int64_t prepare = ws.blocks * a.k_heads * ((a.v_heads / a.k_heads + 1) / 2);
+  if (prepare * kPrepareThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  chunk_prepare_kernel<DK><<<(unsigned)prepare, kPrepareThreads, 0, stream>>>(a, ws);
+  if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+  // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.3 us
+  // with 16 columns and 1.9 us with 32 (one sequence of 8192 tokens, 256 slices of 16: 165 against 245 us; eight of
+  // 1023, 2048 slices: 199 against 152).  As many sequences as the tokens give of the longest.
+  const int64_t longest = max_q > kTok ? max_q : kTok;
+  const int64_t seqs = (a.s.tokens + longest - 1) / longest;
+  const int64_t slices = (seqs < a.s.num_seqs ? seqs : a.s.num_seqs) * a.v_heads * (a.v_dim / 16);
+  return slices <= dev.cus ? launch_scan<DK, 1>(a, ws, stream) : launch_scan<DK, 2>(a, ws, stream);
 }
 
 int64_t aligned_up(int64_t n) { return (n + 255) & ~(int64_t)255; }
@@ -845,8 +925,8 @@ size_t chunk_workspace(int64_t tokens, int64_t num_seqs, int64_t k_heads, int64_
   return (size_t)(p - static_cast<char*>(base));
 }
 
-int launch_chunks(const DeltaArgs& a, const ChunkWork& ws, int k_dim, hipStream_t stream) {
-  return k_dim == 128 ? launch_dk<128>(a, ws, stream) : launch_dk<64>(a, ws, stream);
+int launch_chunks(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, int k_dim, hipStream_t stream) {
+  return k_dim == 128 ? launch_dk<128>(a, ws, max_q, stream) : launch_dk<64>(a, ws, max_q, stream);
 }
 
 }  // namespace nvfp4

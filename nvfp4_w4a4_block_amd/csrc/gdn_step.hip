@@ -144,7 +144,7 @@ int launch_gated_delta_rule(const DeltaArgs& a, int64_t max_q, int k_dim, void* 
     chunk_workspace(a.s.tokens, a.s.num_seqs, a.k_heads, a.v_heads, k_dim, a.v_dim, workspace, ws);
     ws.short_len = short_len = kShort;
     flags = ws.flags;
-    const int st = launch_chunks(a, ws, k_dim, stream);
+    const int st = launch_chunks(a, ws, max_q, k_dim, stream);
     if (st != NVFP4_OK) return st;
   }
   if (k_dim == 128)

@@ -42,6 +42,13 @@ def test_heads_and_sizes(Hk, Hv, Dk, Dv):
     check(Seqs([70, 1, 5], [3, 2, 0]), Hk, Hv, Dk, Dv, seed=3)
 
 
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv,new", [(2, 40, 128, 128, [300, 130, 1]), (40, 40, 64, 128, [65, 20, 400]), (3, 9, 128, 512, [129, 448]),
+                                             (1, 33, 64, 160, [1000])])
+def test_many_columns(Hk, Hv, Dk, Dv, new):
+    # more slices of 16 columns than compute units: the scan takes 32 at a time
+    check(Seqs(new, [5] * len(new)), Hk, Hv, Dk, Dv, max_q=max(new), seed=4)
+
+
 @pytest.mark.parametrize("new", [[5, 3], [150, 80]])
 def test_strong_decays_and_scale(new):
     check(Seqs(new, [4, 0]), 2, 4, 128, 64, seed=5, strong=True, scale=1.0)
