@@ -395,18 +395,18 @@ struct OutStage {
 // Values and row factors wait in LDS from six blocks ahead on: they come from memory, not from other workgroups' reads.
 constexpr int kAhead = 6, kRing = 8;
 
-// Copies 16 B (4 B) a lane from memory to LDS, lane l's to dst + 16 l (4 l): base + off, base and dst the same for all
-// lanes.  From inline assembly, so that the compiler does not make every later LDS read wait for it; the copies write
+// Copies 16 B (4 B) a lane from memory to LDS, lane l's to dst + 16 l (4 l): base + off, base and dst (an LDS address) the
+// same for all lanes.  From inline assembly, so that the compiler does not make every later LDS read wait for it; the copies write
 // no registers, and the kernel orders them itself: they are issued behind a barrier that follows every read of what
 // they overwrite, waited for by count and published with a barrier.  Nothing else in this file uses M0, which the build
 // checks on the generated assembly.
 typedef __attribute__((address_space(3))) void lds_void_t;
-__device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, const void* dst) {
-  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t*)dst);
+__device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, uint32_t dst) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane(dst);
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
 }
-__device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, const void* dst) {
-  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t*)dst);
+__device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, uint32_t dst) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane(dst);
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
 }
 // s_waitcnt immediate that waits for at most n outstanding vector memory operations.
@@ -436,11 +436,10 @@ struct Scan {
     _Float16 R[2][NC][16][kTok + 8];
     _Float16 U[2][NC][16][kTok + 8];           // U times the decays to the block's end, in two parts
     _Float16 O[2][NC][16][kTok + 8];           // U for the outputs, of two blocks
-    _Float16 K[KS][kTok][40];                  // a wavefront's channels of K, for their transposition
+    half4_t K[KS][2][kTok * 4];                // a wavefront's channels of K in two 16s, for their transposition
     uint16_t V[kRing][kTok][16 * NC];          // values
     float rows[kRing][4][kTok];                // row factors: beta, c, d, e
     float decay[kRing][64];                    // of the whole block, copies; NaN where it is out of the scale's premise
-    float unused[4][64];                       // where copies go that only bring lines near
     float norm[KS][NC * 16];
     uint32_t top[3][NC * 16];                  // largest |beta v| of a block, as bits
     float units[2][2][NC * 16];                // for the output half: ratio, and the block's unit times the scale
@@ -449,27 +448,36 @@ struct Scan {
   const DeltaArgs& a;
   const ChunkWork& ws;
   Lds& lds;
+  const uint32_t lds_base;
   const int lane, w, c, g, seq, head, k_head, c0;
   SeqRows rows;
   int n, blocks, slot0;
   const float one = hidden_one();
 
-  __device__ Scan(const DeltaArgs& args, const ChunkWork& work, Lds& shared, int seq_, int head_, int k_head_, int c0_)
-      : a(args), ws(work), lds(shared), lane(threadIdx.x & 63), w(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+  __device__ Scan(const DeltaArgs& args, const ChunkWork& work, Lds& shared, uint32_t base, int seq_, int head_, int k_head_, int c0_)
+      : a(args), ws(work), lds(shared), lds_base(base), lane(threadIdx.x & 63), w(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
         c(lane & 15), g(lane >> 4), seq(seq_), head(head_), k_head(k_head_), c0(c0_) {}
 
-  __device__ __forceinline__ const char* at(const void* base, int block, int heads, int h, int bytes) const {
-    return static_cast<const char*>(base) + ((int64_t)(slot0 + block) * heads + h) * bytes;
+  __device__ __forceinline__ uint32_t lds_address(const void* p) const {
+    return lds_base + (uint32_t)(static_cast<const char*>(p) - reinterpret_cast<const char*>(&lds));
   }
-  __device__ __forceinline__ const char* factors(int block) const {
-    return at(ws.factors, block, a.v_heads, head, kFactors * 4);
+
+  // A pointer that walks along the blocks, kept in scalar registers; it stays at the last one.
+  struct Walk {
+    const char* p;
+    int64_t step;
+    __device__ __forceinline__ void next(bool more) { p += more ? step : 0; }
+  };
+  __device__ __forceinline__ Walk walk(const void* base, int heads, int h, int bytes) const {
+    return Walk{static_cast<const char*>(base) + ((int64_t)slot0 * heads + h) * bytes, (int64_t)heads * bytes};
   }
-  // Rows of a block as a buffer: reads past the sequence's end give 0, writes there go nowhere.
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint16_t* x, int64_t tok, int64_t h, int block) const {
-    const int row = block * kTok, m = min(n - row, kTok);
-    const uint16_t* p = x + (int64_t)(rows.first + row) * tok + head * h + c0;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, (uint32_t)((m - 1) * (uint32_t)tok + 16 * NC) * 2,
-                                             0x00027000);
+
+  // Where 4 channels (one of four) of a token lie: every second eight tokens with their halves of 32 words and of 4
+  // exchanged, so that neither the writes (16 tokens, 2 parts at a time) nor the transposing reads (4 tokens each of two
+  // eights, all parts) meet in a bank.
+  __device__ __forceinline__ static int place(int token, int part) {
+    const int odd = token >> 3 & 1;
+    return (token * 4 + part) ^ (odd * 18);
   }
 
   // Four values of two results' rows as one operand, in two parts.
@@ -495,25 +503,27 @@ struct Scan {
   // from the state's unit to the block's and back.
   float bound[NC], state_unit[NC], up[NC], ratio[NC], to_state[NC];
   float last_unit[NC];                         // of S as it is between blocks
+  Walk k_at, t_at;
   bool bad = false;
 
   __device__ __forceinline__ bool owner() const { return KS == 4 || w < KS; }
 
   // Loads are straight-line and the same every time (past the end: the last block again), so that the waits in the
   // loop count on exactly what was issued since.
-  __device__ __forceinline__ void load_k(SolveStage& s, int block) const {
-    const char* kp = at(ws.k, min(block, blocks - 1), a.k_heads, k_head, 4 * KS * 1024);
+  // k_at and t_at: the block to load next.
+  __device__ __forceinline__ void load_k(SolveStage& s, bool more) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s.k[j] = load_at<half8_t>(kp, ((j * KS + w % KS) * 64 + lane) * 16);
+    for (int j = 0; j < 4; ++j) s.k[j] = load_at<half8_t>(k_at.p, ((j * KS + w % KS) * 64 + lane) * 16);
+    k_at.next(more);
   }
-  __device__ __forceinline__ void load_t(SolveStage& s, int block) const {
-    const char* tp = at(ws.t, min(block, blocks - 1), a.v_heads, head, kTriFrags * 2048);
+  __device__ __forceinline__ void load_t(SolveStage& s, bool more) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const uint32_t frag = tri_frag(w, min(ks, w >> 1)) * 2048 + lane * 16;
-      s.t_hi[ks] = load_at<half8_t>(tp, frag);
-      s.t_lo[ks] = load_at<half8_t>(tp, frag + 1024);
+      s.t_hi[ks] = load_at<half8_t>(t_at.p, frag);
+      s.t_lo[ks] = load_at<half8_t>(t_at.p, frag + 1024);
     }
+    t_at.next(more);
   }
 
   // Units of a block, by column, from the bound before it (one more block is opened behind the last, which sees what
@@ -580,11 +590,11 @@ struct Scan {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const half8_t k = s.k[j];
-        *reinterpret_cast<half4_t*>(&lds.K[w][16 * j + c][4 * g]) = half4_t{k[0], k[1], k[2], k[3]};
-        *reinterpret_cast<half4_t*>(&lds.K[w][16 * j + c][16 + 4 * g]) = half4_t{k[4], k[5], k[6], k[7]};
+        lds.K[w][0][place(16 * j + c, g)] = half4_t{k[0], k[1], k[2], k[3]};
+        lds.K[w][1][place(16 * j + c, g)] = half4_t{k[4], k[5], k[6], k[7]};
       }
     }
-    load_k(s, b + 2);
+    load_k(s, b + 3 < blocks);
     here();
     const float beta[4] = {be.x, be.y, be.z, be.w}, c4[4] = {cc.x, cc.y, cc.z, cc.w};
 #pragma unroll
@@ -640,7 +650,7 @@ struct Scan {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             p[h] = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t*)&lds.K[w][ks * 32 + g * 8 + h * 4 + (c >> 2)][i * 16 + (c & 3) * 4]));
+                (lds_s16x4_t*)&lds.K[w][i][place(ks * 32 + g * 8 + h * 4 + (c >> 2), c & 3)]));
           kt[ks][i] = half8_t{p[0][0], p[0][1], p[0][2], p[0][3], p[1][0], p[1][1], p[1][2], p[1][3]};
         }
     }
@@ -665,7 +675,7 @@ struct Scan {
         }
     }
     here();
-    load_t(s, b + 2);
+    load_t(s, b + 3 < blocks);
     open_block(b + 1);
     here();
     if (owner()) {
@@ -686,10 +696,12 @@ struct Scan {
 
   __device__ __forceinline__ void solve() {
     SolveStage even, odd;
-    load_k(even, 0);
-    load_t(even, 0);
-    load_k(odd, 1);
-    load_t(odd, 1);
+    k_at = walk(ws.k, a.k_heads, k_head, 4 * KS * 1024);
+    t_at = walk(ws.t, a.v_heads, head, kTriFrags * 2048);
+    load_k(even, blocks > 1);
+    load_t(even, blocks > 1);
+    load_k(odd, blocks > 2);
+    load_t(odd, blocks > 2);
     const int slot = seq_slot(a.s, seq);
     const bool old = slot >= 0 && scalar_load(a.s.kv_len + seq) > n;
     float* state = static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
@@ -745,37 +757,41 @@ struct Scan {
 
   // ---- the output half: results transposed, a lane holds 4 neighbouring columns of token c
 
-  __device__ __forceinline__ void load(OutStage<KS>& s, int block) const {
-    const int b = min(block, blocks - 1), o = w - 4;
-    const char* qp = at(ws.q, b, a.k_heads, k_head, 4 * KS * 1024);
+  Walk q_at, a_at, f_at, v_at, o_at;           // the block to load or copy next, and the one to write
+
+  __device__ __forceinline__ void load(OutStage<KS>& s, bool more) {
+    const int o = w - 4;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(qp, ((o * KS + ks) * 64 + lane) * 16);
-    const char* ap = at(ws.a, b, a.v_heads, head, kTriFrags * 1024);
+    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(q_at.p, ((o * KS + ks) * 64 + lane) * 16);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(ap, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
+    for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(a_at.p, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
+    q_at.next(more);
+    a_at.next(more);
   }
 
   // Starts the copies of a block's values and row factors: one or two of a wavefront.
-  __device__ __forceinline__ void copy_rows(int block) const {
-    const int slot = block % kRing, b = min(block, blocks - 1), row0 = b * kTok;
-    const uint16_t* v = a.v + (int64_t)(rows.first + row0) * a.v_tok + head * a.v_head + c0;
+  __device__ __forceinline__ void copy_rows(int block) {
+    const int slot = block % kRing, last = n - 1 - min(block, blocks - 1) * kTok;
+    const bool more = block + 1 < blocks;
 #pragma unroll
     for (int i = 0; i < 2 * NC + 2; ++i) {
       if (i % 4 != w - 4) continue;
       if (i < 2 * NC) {
         // rows behind the end repeat the last one; their beta is 0
-        const int l = i * 64 + lane, row = min(l / (2 * NC), n - 1 - row0);
-        copy16_to_lds(v, (uint32_t)row * (uint32_t)a.v_tok * 2 + l % (2 * NC) * 16, reinterpret_cast<const char*>(&lds.V[slot]) + i * 1024);
+        const int l = i * 64 + lane, row = min(l / (2 * NC), last);
+        copy16_to_lds(v_at.p, (uint32_t)row * (uint32_t)a.v_tok * 2 + l % (2 * NC) * 16, lds_address(&lds.V[slot]) + i * 1024);
       } else if (i == 2 * NC) {
-        copy16_to_lds(factors(b), lane * 16, &lds.rows[slot]);
+        copy16_to_lds(f_at.p, lane * 16, lds_address(&lds.rows[slot]));
       } else {
-        copy4_to_lds(factors(b), 4 * kTok * 4 + 4 * c, &lds.decay[slot]);
+        copy4_to_lds(f_at.p, 4 * kTok * 4 + 4 * c, lds_address(&lds.decay[slot]));
       }
     }
+    v_at.next(more);
+    f_at.next(more);
   }
 
   // The largest |beta v| of 16 tokens, by column, for the block's units.
-  __device__ __forceinline__ void write_top(int block) const {
+  __device__ __forceinline__ void write_top(int block) {
     const int slot = block % kRing, row = 16 * (w - 4) + 4 * g;
     const float4 b4 = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]);
     const float b[4] = {b4.x, b4.y, b4.z, b4.w};
@@ -791,9 +807,11 @@ struct Scan {
 
   // A U and the stores of a block, its Q S in y.
   __device__ __forceinline__ void store_out(const OutStage<KS>& s, f32x4_t (&y)[NC], const float4 (&scale)[NC], int b,
-                                            uint32_t o_at) const {
-    const int o = w - 4;
-    const __amdgpu_buffer_rsrc_t out = buffer(a.out, a.o_tok, a.o_head, b);
+                                            uint32_t lane_at) {
+    const int o = w - 4, rows_here = min(n - b * kTok, kTok);
+    // a block's rows as a buffer: writes past the sequence's end go nowhere
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(o_at.p), 0, ((uint32_t)(rows_here - 1) * (uint32_t)a.o_tok + 16 * NC) * 2, 0x00027000);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
 #pragma unroll
@@ -802,11 +820,12 @@ struct Scan {
           y[nc] = mfma(*reinterpret_cast<const half8_t*>(&lds.O[b & 1][nc][c][ks * 32 + g * 8]), s.a[ks], y[nc]);
       const u32x2_t two = {bf16_pair(y[nc][0] * scale[nc].x, y[nc][1] * scale[nc].y),
                            bf16_pair(y[nc][2] * scale[nc].z, y[nc][3] * scale[nc].w)};
-      __builtin_amdgcn_raw_buffer_store_b64(two, out, o_at, nc * 32, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(two, out, lane_at, nc * 32, 0);
     }
+    o_at.p += o_at.step;
   }
 
-  __device__ __forceinline__ void out_block(OutStage<KS>& s, int b, uint32_t o_at) const {
+  __device__ __forceinline__ void out_block(OutStage<KS>& s, int b, uint32_t lane_at) {
     copy_rows(b + kAhead);
     // the next block's copies are in: since its last one, this wavefront issued at least KS + 3 operations for each of
     // kAhead - 1 blocks (those of the first kAhead blocks were waited for at the start)
@@ -831,26 +850,31 @@ struct Scan {
     write_top(b + 1);
     if (w == 7 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
     lds_barrier();
-    store_out(s, y, scale, b, o_at);
-    load(s, b + 2);
+    store_out(s, y, scale, b, lane_at);
+    load(s, b + 3 < blocks);
   }
 
-  __device__ __forceinline__ void output() const {
-    const uint32_t o_at = (uint32_t)((16 * (w - 4) + c) * (uint32_t)a.o_tok + 4 * g) * 2;
+  __device__ __forceinline__ void output() {
+    const uint32_t lane_at = (uint32_t)((16 * (w - 4) + c) * (uint32_t)a.o_tok + 4 * g) * 2;
     OutStage<KS> even, odd;
+    q_at = walk(ws.q, a.k_heads, k_head, 4 * KS * 1024);
+    a_at = walk(ws.a, a.v_heads, head, kTriFrags * 1024);
+    f_at = walk(ws.factors, a.v_heads, head, kFactors * 4);
+    v_at = Walk{reinterpret_cast<const char*>(a.v + rows.first * a.v_tok + head * a.v_head + c0), kTok * 2 * a.v_tok};
+    o_at = Walk{reinterpret_cast<const char*>(a.out + rows.first * a.o_tok + head * a.o_head + c0), kTok * 2 * a.o_tok};
     for (int b = 0; b < kAhead; ++b) copy_rows(b);
-    load(even, 0);
-    load(odd, 1);
+    load(even, blocks > 1);
+    load(odd, blocks > 2);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     lds_barrier();
     write_top(0);
     lds_barrier();
     int b = 0;
     for (; b + 1 < blocks; b += 2) {
-      out_block(even, b, o_at);
-      out_block(odd, b + 1, o_at);
+      out_block(even, b, lane_at);
+      out_block(odd, b + 1, lane_at);
     }
-    if (b < blocks) out_block(even, b, o_at);
+    if (b < blocks) out_block(even, b, lane_at);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // no copy outlives the workgroup's LDS
   }
 };
@@ -864,7 +888,7 @@ __global__ __launch_bounds__(kScanThreads) void chunk_scan_kernel(DeltaArgs a, C
   const int pair = (j / per_pair) * 8 + (blockIdx.x & 7), part = j % per_pair;
   const int seq = pair / a.k_heads, k_head = pair - seq * a.k_heads;
   if (seq >= a.s.num_seqs) return;
-  Scan<DK, NC> scan(a, ws, lds, seq, k_head * group + part / slices, k_head, part % slices * 16 * NC);
+  Scan<DK, NC> scan(a, ws, lds, (uint32_t)(uintptr_t)(lds_void_t*)&lds, seq, k_head * group + part / slices, k_head, part % slices * 16 * NC);
   scan.rows = seq_rows(a.s, seq);
   scan.n = scan.rows.end - scan.rows.first;
   if (scan.n <= ws.short_len) return;
