@@ -1025,24 +1025,29 @@ def _states_arg(state: GDNState, pool: torch.Tensor, name: str, dtype: torch.dty
                 cu_q: torch.Tensor, gpu: int) -> _SeqStates:
     """A pool [slots, *inner], contiguous but for its slot stride, with the batch's slots and lengths."""
     try:
-        shape, stride = tuple(pool.shape), pool.stride()
-        good = shape[1:] == inner and len(shape) == 1 + len(inner)
+        shape, stride = pool.shape, pool.stride()
+        good = shape[1:] == inner
     except (AttributeError, TypeError, ValueError):
         good = False
     if not good:
         raise ValueError(f"{name}: a tensor {_shape_text(None, *inner)}")
     if pool.dtype is not dtype:
         raise ValueError(f"{name}: dtype {pool.dtype}, expected {dtype}")
-    want = 1
-    for n, s in zip(reversed(inner), reversed(stride)):
-        if n != 1 and s != want and shape[0] > 0:
-            raise ValueError(f"{name}: every slot must be contiguous")
-        want *= n
+    if not pool.is_contiguous():
+        want = 1
+        for n, s in zip(reversed(inner), reversed(stride)):
+            if n != 1 and s != want and shape[0] > 0:
+                raise ValueError(f"{name}: every slot must be contiguous")
+            want *= n
     if pool.get_device() != gpu:
         raise ValueError(f"{name}: on {pool.device}, the other tensors are elsewhere")
-    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        raise ValueError("cu_q: contiguous torch.int32, one dimension")
-    seqs = cu_q.shape[0] - 1
+    try:
+        (seqs,) = cu_q.shape
+    except (AttributeError, TypeError, ValueError):
+        seqs = 0
+    if seqs < 1:
+        raise ValueError("cu_q: contiguous torch.int32, one dimension, at least one element")
+    seqs -= 1
     slots = None if state.slots is None else _vector_arg(state.slots, "state.slots", torch.int32, (seqs,), gpu)
     return _SeqStates(pool.data_ptr(), shape[0], stride[0], slots, _vector_arg(cu_q, "cu_q", torch.int32, (seqs + 1,), gpu),
                       _vector_arg(kv_len, "kv_len", torch.int32, (seqs,), gpu), seqs)
@@ -1091,7 +1096,7 @@ def gated_delta_rule(state: GDNState, q: torch.Tensor, k: torch.Tensor, v: torch
     _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q: a tensor [tokens, heads, dim]")
     _require(isinstance(v, torch.Tensor) and v.dim() == 3, "v: a tensor [tokens, heads, dim]")
     gpu, (T, Hk, Dk) = q.get_device(), q.shape
-    Hv, Dv = v.shape[1:]
+    _, Hv, Dv = v.shape
     qa = _heads_arg(q, "q", _BF16_ONLY, gpu)
     ka = _heads_arg(k, "k", _BF16_ONLY, gpu, T, Hk, Dk)
     va = _heads_arg(v, "v", _BF16_ONLY, gpu, T, Hv, Dv)

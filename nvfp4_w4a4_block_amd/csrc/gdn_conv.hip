@@ -15,12 +15,29 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTogether = 4;       // tokens loaded at once
 
+// 8 channels as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, Raw<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+template <typename T>
+__device__ __forceinline__ void widen_raw(const Raw<T>& r, float (&v)[8]) {
   constexpr int N = sizeof(T) / 2;
 #pragma unroll
-  for (int i = 0; i < N; ++i) widen(reinterpret_cast<const uint4*>(p)[i], v + i * (8 / N), static_cast<const T*>(nullptr));
+  for (int i = 0; i < N; ++i) widen(r.w[i], v + i * (8 / N), static_cast<const T*>(nullptr));
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  Raw<T> r;
+  load_raw(p, r);
+  widen_raw(r, v);
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
@@ -113,26 +130,43 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) store8(state + j * (int64_t)a.channels, kept[j]);
     }
-    for (; t < end; ++t) {
-      if (live) {
-        float v[8], y[8];
-        load8(x + t * a.x_row + c0, v);
+    if (!live) {
+      t = t < end ? end : t;
+      continue;
+    }
+    auto token = [&](const Raw<XT>& raw, int at) {
+      float v[8], y[8];
+      widen_raw(raw, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float s = bias[i];
+      for (int i = 0; i < 8; ++i) {
+        float s = bias[i];
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) s = __builtin_fmaf(w[j][i], h[j][i], s);
-          s = __builtin_fmaf(w[W - 1][i], v[i], s);
-          y[i] = s / (1.0f + __expf(-s));
+        for (int j = 0; j < W - 1; ++j) s = __builtin_fmaf(w[j][i], h[j][i], s);
+        s = __builtin_fmaf(w[W - 1][i], v[i], s);
+        // the hardware's exponential and reciprocal, a unit in the last place each: the exact quotient's ten
+        // instructions an element made the kernel slower than its bytes
+        y[i] = s * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * -1.44269504088896340736f));
 #pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j) h[j][i] = h[j + 1][i];
-          h[W - 2][i] = v[i];
-        }
-        if (a.out_bf16)
-          store8(static_cast<uint16_t*>(a.y) + t * a.y_row + c0, y);
-        else
-          store8(static_cast<float*>(a.y) + t * a.y_row + c0, y);
+        for (int j = 0; j + 1 < W - 1; ++j) h[j][i] = h[j + 1][i];
+        h[W - 2][i] = v[i];
       }
+      if (a.out_bf16)
+        store8(static_cast<uint16_t*>(a.y) + at * a.y_row + c0, y);
+      else
+        store8(static_cast<float*>(a.y) + at * a.y_row + c0, y);
+    };
+    const XT* p = x + c0;
+    for (; t + kTogether <= end; t += kTogether) {
+      Raw<XT> raw[kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) load_raw(p + (t + i) * a.x_row, raw[i]);
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) token(raw[i], t + i);
+    }
+    for (; t < end; ++t) {
+      Raw<XT> raw;
+      load_raw(p + t * a.x_row, raw);
+      token(raw, t);
     }
   }
 }

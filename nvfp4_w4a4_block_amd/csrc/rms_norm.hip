@@ -119,8 +119,11 @@ __device__ __forceinline__ double silu(double z) {
   return z * r;
 }
 
-// In fp32: the exponential's argument is rounded, so |z| 2^-24 relative.
-__device__ __forceinline__ float silu(float z) { return z / (1.0f + __expf(-z)); }
+// In fp32, by the hardware's exponential and reciprocal (a unit in the last place each); the exponential's argument is
+// rounded, so |z| 2^-24 relative.
+__device__ __forceinline__ float silu(float z) {
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
 
 __device__ __forceinline__ double root(double v) { return __builtin_sqrt(v); }
 __device__ __forceinline__ float root(float v) { return __builtin_sqrtf(v); }
