@@ -65,7 +65,7 @@ def check_m0(asm: str) -> int:
     for i, l in enumerate(code):
         if not re.search(r"\bm0\b", l):
             continue
-        if not re.fullmatch(r"s_mov_b32 m0, s\d+", l):
+        if not re.fullmatch(r"s_mov_b32 m0, (s\d+|vcc_lo|vcc_hi)", l):
             raise RuntimeError(f"M0 used outside the LDS copies: {l}")
         if i + 1 >= len(code) or not code[i + 1].startswith("global_load_lds_dword"):
             raise RuntimeError(f"M0 write not followed by its copy: {l}")

@@ -571,9 +571,9 @@ struct Scan {
         half8_t hi, lo;
         operand(S[0][nc], S[1][nc], hi, lo);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], lo, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], hi, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], hi, x[j]);
+        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], lo, x[j]);
         lds.S[nc][w][lane] = hi;
 #pragma unroll
         for (int j = 0; j < 4; ++j) lds.X[w][j][nc][lane] = x[j];
@@ -601,7 +601,8 @@ struct Scan {
     for (int nc = 0; nc < NC; ++nc) {
       f32x4_t r4;
 #pragma unroll
-      for (int i = 1; i < KS; ++i) part[0][nc] += part[i][nc];
+      for (int i = 1; i < KS; i += 2) part[i - 1][nc] += part[i][nc];
+      if (KS == 4) part[0][nc] += part[2][nc];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         r4[r] = __builtin_fmaf(beta[r] * __uint_as_float(v[nc][r] << 16), up[nc], -(c4[r] * ratio[nc]) * part[0][nc][r]);
@@ -616,6 +617,7 @@ struct Scan {
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
+        if (ks > (w >> 1)) continue;
         rh[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.R[0][nc][c][ks * 32 + g * 8]);
         rl[ks][nc] = *reinterpret_cast<const half8_t*>(&lds.R[1][nc][c][ks * 32 + g * 8]);
       }
@@ -759,13 +761,15 @@ struct Scan {
 
   Walk q_at, a_at, f_at, v_at, o_at;           // the block to load or copy next, and the one to write
 
-  __device__ __forceinline__ void load(OutStage<KS>& s, bool more) {
+  __device__ __forceinline__ void load_q(OutStage<KS>& s, bool more) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(q_at.p, (((w - 4) * KS + ks) * 64 + lane) * 16);
+    q_at.next(more);
+  }
+  __device__ __forceinline__ void load_a(OutStage<KS>& s, bool more) {
     const int o = w - 4;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) s.q[ks] = load_at<half8_t>(q_at.p, ((o * KS + ks) * 64 + lane) * 16);
-#pragma unroll
     for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(a_at.p, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
-    q_at.next(more);
     a_at.next(more);
   }
 
@@ -848,10 +852,11 @@ struct Scan {
     }
     lds_barrier();
     write_top(b + 1);
+    load_q(s, b + 3 < blocks);
     if (w == 7 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
     lds_barrier();
     store_out(s, y, scale, b, lane_at);
-    load(s, b + 3 < blocks);
+    load_a(s, b + 3 < blocks);
   }
 
   __device__ __forceinline__ void output() {
@@ -863,8 +868,10 @@ struct Scan {
     v_at = Walk{reinterpret_cast<const char*>(a.v + rows.first * a.v_tok + head * a.v_head + c0), kTok * 2 * a.v_tok};
     o_at = Walk{reinterpret_cast<const char*>(a.out + rows.first * a.o_tok + head * a.o_head + c0), kTok * 2 * a.o_tok};
     for (int b = 0; b < kAhead; ++b) copy_rows(b);
-    load(even, blocks > 1);
-    load(odd, blocks > 2);
+    load_q(even, blocks > 1);
+    load_a(even, blocks > 1);
+    load_q(odd, blocks > 2);
+    load_a(odd, blocks > 2);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     lds_barrier();
     write_top(0);
