@@ -188,11 +188,14 @@ int launch_gdn_conv(const ConvArgs& args, int x_dtype, int width, hipStream_t st
   ConvArgs a = args;
   a.tiles = (a.channels + 511) / 512;
   a.run = 1;
-  // runs as long as 16 tokens where that leaves enough wavefronts
-  while (a.run < 16 && (int64_t)a.s.tokens * a.tiles / (2 * a.run) >= 8192) a.run *= 2;
+  // Runs share the loads of weights and of the inputs before them, and cost a small call its parallelism: as long as 16
+  // tokens while that leaves four wavefronts a compute unit (8192 channels, runs of 1 / 4 / 16: 256 tokens 7.9 / 5.2 / 8.3
+  // us, 1024 tokens 25.2 / 11.8 / 10.5 us, 4096 tokens 84.4 / 34.2 / 27.4 us; 512 channels, 1024 tokens 4.3 / 4.6 / 7.9 us).
+  while (a.run < 16 && (int64_t)a.s.tokens * a.tiles / (2 * a.run) >= 1024) a.run *= 2;
   const int64_t jobs = (int64_t)((a.s.tokens + a.run - 1) / a.run) * a.tiles;
-  if (jobs > INT32_MAX - kThreads) return NVFP4_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)((jobs + kThreads / 64 - 1) / (kThreads / 64));
+  const int64_t grid64 = (jobs + kThreads / 64 - 1) / (kThreads / 64);
+  if (grid64 * kThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;           // threads of a launch
+  const unsigned grid = (unsigned)grid64;
   return x_dtype == NVFP4_BF16 ? launch_width<uint16_t>(a, width, grid, stream) : launch_width<float>(a, width, grid, stream);
 }
 
