@@ -141,3 +141,38 @@ def test_binding_refusals_sequences(nv):
                       (dict(g=g.bfloat16()), "g:"), (dict(beta=g[:, :2]), "beta"), (dict(g=torch.zeros(5, 8)[:, :4]), "g:"), (dict(kv_len=i32(1)), "kv_len"),
                       (dict(cu_q=g), "cu_q"), (dict(out=v.float()), "out"), (dict(workspace=g), "workspace"), (dict(), "GPU")):
         bad(match, nv.gated_delta_rule, **{**base, **kw})
+
+
+def test_gated_delta_rule_workspace(nv):
+    size = nv.lib.nvfp4_gated_delta_rule_workspace_size
+    need = size(100, 0, 2, 8, 8, 128, 128)
+    assert need > 0 and need % 16 == 0
+    # single tokens and drafts need none; a hint past them does, and more tokens and sequences need more
+    assert size(16, 0, 2, 8, 8, 128, 128) == size(100, 16, 8, 8, 8, 128, 128) == 0
+    assert size(100, 17, 2, 8, 8, 128, 128) == need < size(164, 0, 2, 8, 8, 128, 128) < size(164, 0, 3, 8, 8, 128, 128)
+    for args in ((-1, 0, 2, 8, 8, 128, 128), (100, -1, 2, 8, 8, 128, 128), (100, 0, 0, 8, 8, 128, 128), (100, 0, 2, 0, 8, 128, 128),
+                 (100, 0, 2, 8, 12, 128, 128), (100, 0, 2, 8, 8, 96, 128), (100, 0, 2, 8, 8, 128, 48), (100, 0, 2, 8, 8, 128, 544),
+                 (1 << 30, 0, 2, 8, 8, 128, 128)):
+        assert size(*args) == 0, args
+
+    def call(ws, wsb):
+        return nv.lib.nvfp4_gated_delta_rule(states(nv), 100, 0, 128, 128, heads(nv), heads(nv), heads(nv), A16, A16, 0.1, heads(nv), ws, wsb, None)
+    need = size(100, 0, states(nv).num_seqs, 8, 8, 128, 128)
+    assert call(None, need) == call(A16, need - 1) == call(A16, 0) == call(MIS, need) == 3
+
+
+def test_launches_too_large_are_refused(nv):
+    # 2^26 runs of 16 tokens: a thread more than a launch can have
+    assert nv.lib.nvfp4_gdn_conv(states(nv), (1 << 30) - 1, 8, 4, A16, nv._BF16, 8, A16, None, A16, nv._BF16, 8, None) == 2
+    many = states(nv, num_seqs=1 << 24)
+    assert nv.lib.nvfp4_gated_delta_rule(many, 1, 0, 128, 128, heads(nv), heads(nv), heads(nv), A16, A16, 0.1, heads(nv), None, 0, None) == 2
+
+
+def test_binding_refuses_a_small_workspace(nv):
+    bf = torch.bfloat16
+    q, v, g = torch.zeros(50, 2, 64, dtype=bf), torch.zeros(50, 4, 32, dtype=bf), torch.zeros(50, 4)
+    lens = torch.tensor([30, 20], dtype=torch.int32), torch.tensor([0, 30, 50], dtype=torch.int32)
+    need = nv.lib.nvfp4_gated_delta_rule_workspace_size(50, 0, 2, 2, 4, 64, 32)
+    for ws, match in ((torch.zeros(need - 1, dtype=torch.uint8), "needed"), (torch.zeros(2 * need, dtype=torch.uint8)[::2], "contiguous"),
+                      (torch.zeros(need, dtype=torch.int8), "uint8")):
+        bad(match, nv.gated_delta_rule, nv.GDNState(delta=torch.zeros(2, 4, 64, 32)), q, q, v, g, g, *lens, workspace=ws)
