@@ -17,6 +17,7 @@ struct NormArgs {
   float eps;
   int32_t rows, blocks;
   int32_t head_blocks;             // gated: 16-element blocks per head (a power of two)
+  int32_t row_lanes_log;           // rows that share a workgroup: log2 of a row's threads
   // outputs
   void* y;                         // nullptr: none
   int64_t y_row;

@@ -152,3 +152,28 @@ def test_no_rows():
     assert y.shape == (0, 64) and q.codes.shape == (0, 32) and r.shape == (0, 64)
     y, q = nv().gated_rms_norm(torch.empty(0, 2, 64, device=DEV), torch.empty(0, 2, 64, device=DEV), w, quant="fp8")
     assert y.shape == (0, 128) and q.codes.shape == (0, 128)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 67, 1000])
+@pytest.mark.parametrize("cols", [16, 32, 80, 256, 528, 1008, 1024])
+@pytest.mark.parametrize("eps", [0.0, 1e-3])
+def test_short_rows_share_wavefronts(rows, cols, eps):
+    x, w = rand(rows, cols, seed=10, scale=2.0), 0.5 + uniform(cols, seed=11)
+    _, y32 = add_norm(x, None, w, eps)
+    for quant in ("nvfp4", "fp8"):
+        y, q, _ = nv().add_rms_norm(gpu(x), gpu(w), eps=eps, out_dtype=F32, quant=quant)
+        assert torch.equal(y.cpu(), y32)
+        check_quant(q, y32, quant, "per_row", None)
+    assert torch.equal(nv().add_rms_norm(gpu(x), gpu(w), eps=eps)[0].cpu(), y32.to(BF16))
+
+
+@pytest.mark.parametrize("T,H,D", [(1, 3, 16), (67, 5, 16), (1000, 2, 64), (300, 3, 64), (129, 7, 128), (33, 64, 16), (5, 65, 16), (3, 9, 128)])
+@pytest.mark.parametrize("eps", [0.0, 1e-3])
+def test_short_rows_of_heads(T, H, D, eps):
+    x, z, w = rand(T, H, D, seed=12), rand(T, H, D, seed=13, scale=2.0), 0.5 + uniform(D, seed=14)
+    want, tol32, tol = (t.flatten(1) for t in gated_norm(x, z, w, eps))
+    for quant in ("nvfp4", "fp8"):
+        y, q = nv().gated_rms_norm(gpu(x), gpu(z), gpu(w), eps=eps, out_dtype=F32, quant=quant)
+        assert_within(y, want, tol + HALF[F32] * want.abs())
+        check_quant(q, y.cpu(), quant, "per_row", None)
+    assert_within(nv().gated_rms_norm(gpu(x), gpu(z), gpu(w), eps=eps)[0], want, tol32 + HALF[BF16] * want.abs())
