@@ -127,10 +127,31 @@ __device__ __forceinline__ float unit_factor(float s, float sc) {
   return sc < 1.0f ? 1.0f / __builtin_sqrtf(s + 1e-6f * sc * sc) : inv / __builtin_sqrtf(s * inv * inv + 1e-6f);
 }
 
-__device__ __forceinline__ double shfl_double(double v, int lane) { return __shfl(v, lane, 64); }
+// v + the value of a lane before it, in 64 bits, where CONTROL and ROWS have one.
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ double plus_earlier(double v) {
+  const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)bits, CONTROL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(bits >> 32), CONTROL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Lane l: the sum of lanes 0 .. l.
+__device__ __forceinline__ double running_sum(double v) {
+  v = plus_earlier<0x111, 0xF>(v);             // within rows of 16: the lane 1, 2, 4, 8 before
+  v = plus_earlier<0x112, 0xF>(v);
+  v = plus_earlier<0x114, 0xF>(v);
+  v = plus_earlier<0x118, 0xF>(v);
+  v = plus_earlier<0x142, 0xA>(v);             // a row's last lane to the next row, of rows 1 and 3
+  return plus_earlier<0x143, 0xC>(v);          // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)bits, 63), hi = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 
-// 2^x for x <= 0 by the hardware's instruction: what rounding x to fp32 costs, |x| 2^x 2^-25, stays below 2^-25.
-__device__ __forceinline__ float power2(double x) { return __builtin_amdgcn_exp2f((float)x); }
+// 2^x for x <= 0 by the hardware's instruction: what one rounding of x costs, |x| 2^x 2^-25, stays below 2^-25.
+__device__ __forceinline__ float power2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // T, A and the row factors of one block for two value heads of one key head: eight wavefronts, four to a value head;
 // wavefront w of four has rows 16 w .. 16 w + 15.  K K^T and Q K^T are both halves' own work, a tenth of
@@ -144,7 +165,8 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
   __shared__ __attribute__((aligned(16))) char shared[2 * 4 * KS * 1024 > 2 * kTok * 144 ? 2 * 4 * KS * 1024 : 2 * kTok * 144];
   __shared__ __attribute__((aligned(16))) float Ls[2][kTok][kTok + 4];         // L, then T
   __shared__ __attribute__((aligned(16))) float Ds[2][4][16][20];              // inverses of the diagonal blocks
-  __shared__ float unit_k[kTok], unit_q[kTok];
+  __shared__ __attribute__((aligned(16))) float unit_k[kTok], unit_q[kTok], betas[2][kTok];
+  __shared__ __attribute__((aligned(16))) float decay_hi[2][kTok], decay_lo[2][kTok];      // running sum of a head's log2 decays
   __shared__ float sums[8][16], scales[8][16];
   __shared__ int bads[8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
@@ -167,9 +189,11 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
   if (n <= ws.short_len || index < 0 || index >= (n + kTok - 1) / kTok) return;
   const int m = n - index * kTok < kTok ? n - index * kTok : kTok;
   const int64_t row0 = rows.first + (int64_t)index * kTok;
-  // decays and strengths come from far, too: out with the rows, used much later
+  // decays and strengths come from far, too: out ahead of the rows, their sums taken before those are in
   const int64_t at = (row0 + (lane < m ? lane : 0)) * a.v_heads + head;
   const float g_load = a.g[at], beta_load = a.beta[at];
+  double sum = 0.0;
+  bool off = false;
   {
     // One half takes the rows of k, the other those of q, whole rows at a time.  Fragments, K's and Q's alike: lane (row,
     // part) of 16 x 4 holds channels 32 ks + 4 part .. + 3 and 32 ks + 16 + 4 part .. + 3, the rows that a lane holds of
@@ -183,6 +207,17 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
     for (int i = 0; i < LOADS; ++i) {
       const int t = 16 * w + i * ROWS + lane / LANES;
       raw[i] = *reinterpret_cast<const uint4*>(x + (row0 + min(t, m - 1)) * pitch + d);
+    }
+    if (w == 0) {
+      // lane t: the sum of the log2 decays up to token t, in 64 bits: differences of far sums keep their last bits.  Decays
+      // below 2^-1000 are as good as that one, and sums of it stay finite in fp32.
+      const float gt = lane < m ? g_load : 0.0f, beta = lane < m ? beta_load : 0.0f;
+      off = __builtin_amdgcn_ballot_w64(!(gt <= 0.0f && gt >= -3e38f) || !(beta >= 0.0f && beta <= 2.0f)) != 0;
+      sum = running_sum(__builtin_fmax((double)gt * 1.4426950408889634074, -1000.0));
+      const float hi = (float)sum;
+      decay_hi[half][lane] = hi;
+      decay_lo[half][lane] = (float)(sum - (double)hi);
+      betas[half][lane] = beta;
     }
     bool bad = false;
 #pragma unroll
@@ -240,45 +275,29 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
   _Float16(*At)[kTok + 8] = reinterpret_cast<_Float16(*)[kTok + 8]>(shared) + half * kTok;
 
   {
-    // lane t: the sum of the log2 decays up to token t, in 64 bits: differences of far sums keep their last bits
-    const float gt = lane < m ? g_load : 0.0f, beta = lane < m ? beta_load : 0.0f;
-    const bool off = !(gt <= 0.0f && gt >= -3e38f) || !(beta >= 0.0f && beta <= 2.0f);
-    const bool bad_head = bad_rows || __builtin_amdgcn_ballot_w64(off) != 0;
-    double sum = (double)gt * 1.4426950408889634074;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const double other = shfl_double(sum, lane - s);
-      if (lane >= s) sum += other;
-    }
     if (w == 0) {
-      const double total = shfl_double(sum, 63);
+      const double total = last_lane(sum);
       float* f = ws.factors + ((int64_t)block * a.v_heads + head) * kFactors;
-      const float since = power2(sum);
+      const float since = power2((float)sum), beta = betas[half][lane], uk = unit_k[lane];
       f[lane] = beta;
-      f[kTok + lane] = beta * since * unit_k[lane];
-      f[2 * kTok + lane] = power2(total - sum) * unit_k[lane];
+      f[kTok + lane] = beta * since * uk;
+      f[2 * kTok + lane] = power2((float)(total - sum)) * uk;
       f[3 * kTok + lane] = since * unit_q[lane];
-      if (lane < 16) f[4 * kTok + lane] = bad_head ? __builtin_nanf("") : power2(total);
+      if (lane < 16) f[4 * kTok + lane] = bad_rows || off ? __builtin_nanf("") : power2((float)total);
     }
-    double row_sum[4];
-    float row_k[4], row_q[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * w + 4 * g + r;
-      row_sum[r] = shfl_double(sum, i);
-      row_k[r] = __shfl(beta, i, 64) * unit_k[i];
-      row_q[r] = unit_q[i];
-    }
+    const int row = 16 * w + 4 * g;
+    const f32x4_t row_hi = *reinterpret_cast<const f32x4_t*>(&decay_hi[half][row]), row_lo = *reinterpret_cast<const f32x4_t*>(&decay_lo[half][row]);
+    const f32x4_t row_k = *reinterpret_cast<const f32x4_t*>(&betas[half][row]) * *reinterpret_cast<const f32x4_t*>(&unit_k[row]);
+    const f32x4_t row_q = *reinterpret_cast<const f32x4_t*>(&unit_q[row]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j <= w) {
         const int col = 16 * j + c;
-        const double col_sum = shfl_double(sum, col);
-        const float col_k = unit_k[col];
+        const float col_hi = decay_hi[half][col], col_lo = decay_lo[half][col], col_k = unit_k[col];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * w + 4 * g + r;
-          const float d = power2(row_sum[r] - col_sum) * col_k;
+          const float d = power2((row_hi[r] - col_hi) + (row_lo[r] - col_lo)) * col_k;
           float l = kk[j][r] * row_k[r] * d, q = qk[j][r] * row_q[r] * d;
           if (j == w) {
             l = i > col ? l : 0.0f;
