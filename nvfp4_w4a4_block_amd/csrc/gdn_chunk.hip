@@ -155,7 +155,9 @@ __device__ __forceinline__ float power2(float x) { return __builtin_amdgcn_exp2f
 
 // T, A and the row factors of one block for two value heads of one key head: eight wavefronts, four to a value head;
 // wavefront w of four has rows 16 w .. 16 w + 15.  K K^T and Q K^T are both halves' own work, a tenth of
-// what exchanging them would wait for.  Bound by its bytes (q, k in, fragments out) and the latency of the inverse.
+// what exchanging them would wait for.  Bound by its bytes (q, k in, fragments out) and the latency of the inverse: 8192
+// tokens of 16 and 32 heads of 128, 215 MB, 58 us (3.7 TB/s).  One workgroup that takes block after block with the next
+// one's rows on the way took 70.
 constexpr int kPrepareThreads = 512;
 
 template <int DK>
@@ -413,6 +415,7 @@ struct OutStage {
 
 // Values and row factors wait in LDS from six blocks ahead on: they come from memory, not from other workgroups' reads.
 constexpr int kAhead = 6, kRing = 8;
+static_assert(kAhead == 6, "the first blocks' order and counts in out_block");
 
 // Copies 16 B (4 B) a lane from memory to LDS, lane l's to dst + 16 l (4 l): base + off, base and dst (an LDS address) the
 // same for all lanes.  From inline assembly, so that the compiler does not make every later LDS read wait for it; the copies write
@@ -446,6 +449,8 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
 //   of K S just as the last update left them.  K S over its channels for all tokens; barrier; the sum over the
 //   wavefronts for tokens 16 w .. 16 w + 15, R; barrier; U = T R; barrier; its rows' update.
 //   Output half: Q S of 16 tokens each while the others solve, A U and the stores while they are at the next block.
+// Bound by the chain through the barriers, 2500 cycles a block: 8192 tokens of 32 heads of 128 take 160 us with every
+// compute unit at work (1.3 TB/s, 2 % of the matrix rate for each product) and as long with one head on the machine.
 template <int DK, int NC>
 struct Scan {
   static constexpr int KS = DK / 32;
@@ -471,6 +476,8 @@ struct Scan {
   const int lane, w, c, g, seq, head, k_head, c0;
   SeqRows rows;
   int n, blocks, slot0;
+  int slot;                                    // of the sequence's state, or -1
+  bool old;                                    // it is read
   const float one = hidden_one();
 
   __device__ Scan(const DeltaArgs& args, const ChunkWork& work, Lds& shared, uint32_t base, int seq_, int head_, int k_head_, int c0_)
@@ -719,14 +726,17 @@ struct Scan {
     SolveStage even, odd;
     k_at = walk(ws.k, a.k_heads, k_head, 4 * KS * 1024);
     t_at = walk(ws.t, a.v_heads, head, kTriFrags * 2048);
-    load_k(even, blocks > 1);
-    load_t(even, blocks > 1);
-    load_k(odd, blocks > 2);
-    load_t(odd, blocks > 2);
-    const int slot = seq_slot(a.s, seq);
-    const bool old = slot >= 0 && scalar_load(a.s.kv_len + seq) > n;
     float* state = static_cast<float*>(a.s.state) + (slot >= 0 ? slot : 0) * a.s.slot +
                    ((int64_t)head * DK + (w % KS) * 32 + 4 * g) * a.v_dim + c0 + c;
+    // all CUs begin at once: what the first block needs is asked for first
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[i][nc][r] = old ? state[(int64_t)(16 * i + r) * a.v_dim + nc * 16] : 0.0f;
+    load_k(even, blocks > 1);
+    load_t(even, blocks > 1);
     if (w == 0 && lane < 3 * 16) {
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) (&lds.top[0][0])[nc * 48 + lane] = 0;
@@ -737,10 +747,7 @@ struct Scan {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          S[i][nc][r] = old ? state[(int64_t)(16 * i + r) * a.v_dim + nc * 16] : 0.0f;
-          m += __builtin_fabsf(S[i][nc][r]);
-        }
+        for (int r = 0; r < 4; ++r) m += __builtin_fabsf(S[i][nc][r]);
       m = quad_sum(m);
       if (g == 0 && owner()) lds.norm[w][nc * 16 + c] = m;
     }
@@ -755,6 +762,8 @@ struct Scan {
 #pragma unroll
       for (int i = 0; i < 2; ++i) S[i][nc] *= state_up;
     }
+    load_k(odd, blocks > 2);
+    load_t(odd, blocks > 2);
     lds_barrier();
     open_block(0);
     int b = 0;
@@ -849,10 +858,25 @@ struct Scan {
   }
 
   __device__ __forceinline__ void out_block(OutStage<KS>& s, int b, uint32_t lane_at) {
-    copy_rows(b + kAhead);
-    // the next block's copies are in: since its last one, this wavefront issued at least KS + 3 operations for each of
-    // kAhead - 1 blocks (those of the first kAhead blocks were waited for at the start)
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm((kAhead - 1) * (KS + 3)));
+    // The copies begin with two blocks (all workgroups begin at once, and wait for the first) and go on by two a block,
+    // 2 b + 2 and 2 b + 3, up to a lead of kAhead = 6.  Then this wavefront waits until its part of the next block's are
+    // in, by what it has issued since at least; a block issues its copies, KS + 2 loads and a store.  For block 1 that is
+    // KS + 2 loads and two copies, for 2 more; for 3 two blocks and four copies, for 4 to 8 more; from 9 on kAhead - 1
+    // blocks and copies.
+    int turn = b;
+    asm("" : "+s"(turn));                      // one loop for all of them
+    if (turn < 4) {
+      copy_rows(2 * b + 2);
+      copy_rows(2 * b + 3);
+    } else {
+      copy_rows(b + kAhead);
+    }
+    if (turn < 2)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(KS + 4));
+    else if (turn < 8)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * KS + 10));
+    else
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm((kAhead - 1) * (KS + 3)));
     lds_barrier();
     f32x4_t y[NC];
     float4 scale[NC];
@@ -886,14 +910,15 @@ struct Scan {
     f_at = walk(ws.factors, a.v_heads, head, kFactors * 4);
     v_at = Walk{reinterpret_cast<const char*>(a.v + rows.first * a.v_tok + head * a.v_head + c0), kTok * 2 * a.v_tok};
     o_at = Walk{reinterpret_cast<const char*>(a.out + rows.first * a.o_tok + head * a.o_head + c0), kTok * 2 * a.o_tok};
-    for (int b = 0; b < kAhead; ++b) copy_rows(b);
+    copy_rows(0);
     load_q(even, blocks > 1);
     load_a(even, blocks > 1);
-    load_q(odd, blocks > 2);
-    load_a(odd, blocks > 2);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(KS + 2));       // the first block's copies are in
     lds_barrier();
     write_top(0);
+    copy_rows(1);
+    load_q(odd, blocks > 2);
+    load_a(odd, blocks > 2);
     lds_barrier();
     int b = 0;
     for (; b + 1 < blocks; b += 2) {
@@ -917,6 +942,8 @@ __global__ __launch_bounds__(kScanThreads) void chunk_scan_kernel(DeltaArgs a, C
   Scan<DK, NC> scan(a, ws, lds, (uint32_t)(uintptr_t)(lds_void_t*)&lds, seq, k_head * group + part / slices, k_head, part % slices * 16 * NC);
   scan.rows = seq_rows(a.s, seq);
   scan.n = scan.rows.end - scan.rows.first;
+  scan.slot = seq_slot(a.s, seq);
+  scan.old = scan.slot >= 0 && scalar_load(a.s.kv_len + seq) > scan.n;
   if (scan.n <= ws.short_len) return;
   scan.blocks = (scan.n + kTok - 1) / kTok;
   scan.slot0 = scan.rows.first / kTok + seq;
@@ -944,9 +971,9 @@ int launch_dk(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, hipStream_
   if (prepare * kPrepareThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;
   chunk_prepare_kernel<DK><<<(unsigned)prepare, kPrepareThreads, 0, stream>>>(a, ws);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-  // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.3 us
-  // with 16 columns and 1.9 us with 32 (one sequence of 8192 tokens, 256 slices of 16: 165 against 245 us; eight of
-  // 1023, 2048 slices: 199 against 152).  As many sequences as the tokens give of the longest.
+  // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.2 us
+  // with 16 columns and 1.9 us with 32 (one sequence of 8192 tokens, 256 slices of 16: 160 against 240 us; eight of
+  // 1023, 2048 slices: 186 against 145).  As many sequences as the tokens give of the longest.
   const int64_t longest = max_q > kTok ? max_q : kTok;
   const int64_t seqs = (a.s.tokens + longest - 1) / longest;
   const int64_t slices = (seqs < a.s.num_seqs ? seqs : a.s.num_seqs) * a.v_heads * (a.v_dim / 16);

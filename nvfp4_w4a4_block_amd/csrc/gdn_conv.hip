@@ -3,7 +3,8 @@
 // over the tokens of each sequence; inputs before its first new token come from its state (the last W - 1 inputs),
 // which is replaced by the last W - 1 inputs of all.
 //
-// HBM-bound: every input is read once and written once.  A lane holds 8 channels, a wavefront 512, and walks along a
+// HBM-bound: every input is read once and written once (8192 tokens of 8192 bf16 channels, 268 MB: 56-62 us, 4.3-4.8
+// TB/s).  A lane holds 8 channels, a wavefront 512, and walks along a
 // run of tokens with the last W - 1 inputs in registers; sequences that end inside the run are walked through.  The
 // state is read for the first W - 1 tokens of a sequence only: the wavefront that has a sequence's first token takes
 // those tokens all, even past the end of its run, and then replaces the state, so no other wavefront reads what it
