@@ -536,11 +536,12 @@ typedef enum {
 /* What a norm writes of its rows y (host struct; device pointers).
  *   y            [rows, ldy] of y_dtype (NVFP4_BF16: round to nearest even, or NVFP4_F32), or NULL if a
  *                format is given; 16-byte aligned, ldy * element size a multiple of 16 bytes.
- *   format       nvfp4_norm_format, of fl32(y).  codes 16-byte aligned.
+ *   format       nvfp4_norm_format.  codes 16-byte aligned.
  *   mode         NVFP4_SCALE_PER_ROW: scale[rows] is written, max|y| / 2688 (NVFP4) or max|y| / 448 (FP8) of each
  *                row; a row of zeros has scale 0 and codes of zero.  NVFP4_SCALE_GIVEN: scale[0] is read, finite
- *                and > 0.  NVFP4 codes and scales are those nvfp4_quantize gives in that mode, FP8 bytes those
- *                of nvfp4_fp8_kv_quantize. */
+ *                and > 0.  NVFP4 codes and scales are those nvfp4_quantize gives of fl32(y) in that mode.  FP8 bytes are
+ *                the E4M3 values nearest to y / scale (ties to even, saturating at 448, NaN 0x7F) in one rounding: y
+ *                and a row's max|y| / 448 are held in 64 bits for it. */
 typedef struct {
   void* y;
   int64_t ldy;
@@ -579,7 +580,8 @@ int nvfp4_add_rms_norm(int64_t rows, int64_t cols, const void* x, int x_dtype, i
 int nvfp4_gated_rms_norm(int64_t tokens, int64_t head_dim, const nvfp4_heads* x, int x_dtype, const nvfp4_heads* z, int z_dtype,
                          const float* weight, float eps, const nvfp4_norm_out* out, void* stream);
 
-/* A pool of per-sequence states and the batch of sequences that uses it (host struct; device pointers).
+/* A pool of per-sequence states and the batch of sequences that uses it (host struct; device pointers): fewer than 2^30
+ * sequences, fewer than 2^31 slots.
  *   data         slot i's state at data + i * slot_stride elements, contiguous; 16-byte aligned, slot_stride
  *                times the element size a multiple of 16 bytes.
  *   slots        int32 [num_seqs]: the slot of each sequence, or NULL (sequence s uses slot s).  A slot outside

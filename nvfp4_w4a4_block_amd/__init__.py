@@ -978,7 +978,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     """Residual addition and root-mean-square norm of the rows of x [M, N] (bf16 or fp32), the output
     quantized for the next linear: r = x + residual (rounded to the residual's type; r = x without one),
     y = r * weight / sqrt(mean(r^2) + eps), weight fp32 [N].  quant "nvfp4" gives an NVFP4Tensor, "fp8" an
-    FP8Tensor, both of fl32(y), their scale one per row (mode "per_row") or the given one (mode "given",
+    FP8Tensor, their scale one per row (mode "per_row") or the given one (mode "given",
     scale fp32 [1]).  out_dtype: the type of y itself, or None to leave it out.  residual_out may be the
     residual.  Returns (y, quantized y, r); what was not asked for is None (r without a residual)."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a tensor [rows, cols]")

@@ -38,7 +38,7 @@ int check_norm_out(const nvfp4_norm_out* o, int64_t rows, int64_t cols, NormArgs
 // A pool of states with `per_slot` contiguous elements of `esize` bytes each.
 int check_states(const nvfp4_seq_states* p, int64_t tokens, int64_t per_slot, int64_t esize, SeqState& s) {
   if (!p || p->num_seqs < 0 || p->num_slots < 0) return NVFP4_ERR_INVALID_ARG;
-  if (p->num_slots > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+  if (p->num_slots > INT32_MAX || p->num_seqs > INT32_MAX / 2) return NVFP4_ERR_UNSUPPORTED;
   if (tokens == 0 || p->num_seqs == 0) return NVFP4_OK;
   if (!p->cu_q || !p->kv_len || !aligned(p->cu_q, 4) || !aligned(p->kv_len, 4) || !aligned(p->slots, 4))
     return NVFP4_ERR_INVALID_ARG;

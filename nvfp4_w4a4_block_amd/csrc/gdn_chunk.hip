@@ -450,7 +450,7 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
 //   wavefronts for tokens 16 w .. 16 w + 15, R; barrier; U = T R; barrier; its rows' update.
 //   Output half: Q S of 16 tokens each while the others solve, A U and the stores while they are at the next block.
 // Bound by the chain through the barriers, 2500 cycles a block: 8192 tokens of 32 heads of 128 take 160 us with every
-// compute unit at work (1.3 TB/s, 2 % of the matrix rate for each product) and as long with one head on the machine.
+// compute unit at work and as long with one head on the machine.
 template <int DK, int NC>
 struct Scan {
   static constexpr int KS = DK / 32;
@@ -974,7 +974,7 @@ int launch_dk(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, hipStream_
   // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.2 us
   // with 16 columns and 1.9 us with 32 (one sequence of 8192 tokens, 256 slices of 16: 160 against 240 us; eight of
   // 1023, 2048 slices: 186 against 145).  As many sequences as the tokens give of the longest.
-  const int64_t longest = max_q > kTok ? max_q : kTok;
+  const int64_t longest = max_q > a.s.tokens ? a.s.tokens : max_q > kTok ? max_q : kTok;
   const int64_t seqs = (a.s.tokens + longest - 1) / longest;
   const int64_t slices = (seqs < a.s.num_seqs ? seqs : a.s.num_seqs) * a.v_heads * (a.v_dim / 16);
   return slices <= dev.cus ? launch_scan<DK, 1>(a, ws, stream) : launch_scan<DK, 2>(a, ws, stream);

@@ -5,14 +5,15 @@
 // and from y, any of: bf16 or fp32; NVFP4 as the quantizer encodes fl32(y), under a given global scale or one per row
 // (max|y| / 2688); FP8 (E4M3) bytes under a given scale or one per row (max|y| / 448).
 //
-// HBM-bound: every element is read once and written once (4096 x 5120 bf16 with residual to NVFP4 and bf16, 138 MB: 29-31
-// us, 4.5-4.8 TB/s; gated, 8192 x 4096 to bf16, 201 MB: 37 us, 5.4 TB/s).  A workgroup takes one row and keeps it in registers, a
+// HBM-bound: every element is read once and written once (4096 x 5120 bf16 with residual to NVFP4, 138 MB: 29-31 us,
+// 4.5-4.8 TB/s; gated, 8192 x 4096 to bf16, 201 MB: 37 us, 5.4 TB/s).  A workgroup takes one row and keeps it in registers, a
 // thread 16 consecutive elements (an NVFP4 block) at a time, so that the statistics, the row's maximum and the
 // encoding need one pass over memory.  Rows of at most 64 blocks share workgroups, as many to a wavefront as it holds.
 //
-// Arithmetic: in 64 bits from the stored r' (x and z) to y, which is then rounded once to fp32: codes of values next
-// to a rounding border do not depend on the order of a sum, so the NVFP4 and FP8 bytes are the quantizers' of the exactly
-// computed norm.  gated_rms_norm without a quantized output works in fp32, which hides its exponential behind the
+// Arithmetic: in 64 bits from the stored r' (x and z) to y: codes of values next to a rounding border do not depend on the
+// order of a sum.  The NVFP4 bytes are the quantizer's of fl32(y), the FP8 bytes the values nearest to y / scale, with one
+// rounding and, per row, max|y| / 448 before its own to fp32 (quotients of fl32(y) in fp32 put one byte in about three
+// million on a border's other side; 2049 x 4096 fp32: 12 us, 11 that way).  gated_rms_norm without a quantized output works in fp32, which hides its exponential behind the
 // loads (8192 tokens of 32 heads of 128, bf16 output: 30 us, 58 in 64 bits; NVFP4 output, in 64 bits: 58 us, bound by its
 // 580 64-bit instructions for 16 elements).
 #include <type_traits>
@@ -65,8 +66,10 @@ __device__ __forceinline__ double group_sum(double v, double* lds, int lanes) {
   return s;
 }
 
-__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* lds, int lanes) {
-  for (int m = 1; m < lanes; m *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, m, 64));
+// Largest, likewise: of magnitudes' bits, NaN above infinity above the rest.
+template <typename T>
+__device__ __forceinline__ T group_max(T v, T* lds, int lanes) {
+  for (int m = 1; m < lanes; m *= 2) v = max(v, __shfl_xor(v, m, 64));
   if (!lds) return v;
   const int waves = blockDim.x >> 6;
   if (waves == 1) return v;
@@ -76,25 +79,30 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* lds, int lan
   return v;
 }
 
-__device__ __forceinline__ uint4 fp8_16(const float (&v)[16], float s, bool zero) {
-  if (zero) {                                  // a row of zeros under its own scale of zero: signed zeros
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[i] |= ((__float_as_uint(v[4 * i + j]) >> 24) & 0x80u) << (8 * j);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
+// E4M3 bytes of y f from 64 bits, one rounding: the product's upper 21 bits, the last one set where any below are (so that
+// it lies on no border that the product does not), go through fp32 exactly.
+template <bool MAY_BE_NAN>
+__device__ __forceinline__ uint4 fp8_16(const double (&y)[16], double f) {
+  float t[16];
   bool nan = false;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) nan |= v[i] != v[i];
-  if (fast_scale(s) && !nan) {
-    const FastQuotient f{s, 1.0f / s, 440.0f * s};
-    return make_uint4(fp8x4_fast(v, f), fp8x4_fast(v + 4, f), fp8x4_fast(v + 8, f), fp8x4_fast(v + 12, f));
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t bits = __builtin_bit_cast(uint64_t, y[i] * f);
+    const uint32_t hi = (uint32_t)(bits >> 32) | min((uint32_t)bits, 1u);
+    t[i] = (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
+    if (MAY_BE_NAN) nan |= t[i] != t[i];
   }
-  return make_uint4(fp8x4_exact(v, s), fp8x4_exact(v + 4, s), fp8x4_exact(v + 8, s), fp8x4_exact(v + 12, s));
+  if (MAY_BE_NAN && nan)
+    return make_uint4(fp8x4_exact(t, 1.0f), fp8x4_exact(t + 4, 1.0f), fp8x4_exact(t + 8, 1.0f), fp8x4_exact(t + 12, 1.0f));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = __builtin_amdgcn_fmed3f(t[4 * i + j], -448.0f, 448.0f);
+    w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false), true);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // z sigmoid(z) to about 2^-45.  e^-z = 2^n 2^f, |f| <= 1/2, 2^f by its Taylor series to the power 11 (the next term is
@@ -139,14 +147,17 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
   constexpr bool SHARED = BLOCKS == 0;
   constexpr int NB = SHARED ? 1 : BLOCKS;
   __shared__ double sums_of[16];
-  __shared__ uint32_t tops_of[16];
+  typedef typename std::conditional<FORMAT == kFp8, unsigned long long, unsigned>::type Top;
+  __shared__ Top tops_of[16];
   double* sums = SHARED ? nullptr : sums_of;
-  uint32_t* tops = SHARED ? nullptr : tops_of;
+  Top* tops = SHARED ? nullptr : tops_of;
   const int lanes = SHARED ? 1 << a.row_lanes_log : 64;
   const int64_t row = SHARED ? (int64_t)(blockIdx.x * kSharedThreads + threadIdx.x) >> a.row_lanes_log : (int64_t)blockIdx.x;
   if (SHARED && row >= a.rows) return;
   const int tid = SHARED ? threadIdx.x & (lanes - 1) : threadIdx.x, threads = blockDim.x;
   float v[NB][16];
+  double exact[FORMAT == kFp8 ? NB : 1][16];   // FP8: y is this times inv_of
+  double inv_of[NB];
   bool live[NB];
   double sum = 0.0;
 #pragma unroll
@@ -177,7 +188,13 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
       for (int m = 1; m < a.head_blocks; m *= 2) total += __shfl_xor(total, m, 64);
       const Real inv = (Real)1 / root(total / (Real)(a.head_blocks * 16) + (Real)a.eps);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[n][i] = (float)(y[i] * inv);
+      for (int i = 0; i < 16; ++i) {
+        if (FORMAT == kFp8)
+          exact[n][i] = y[i];
+        else
+          v[n][i] = (float)(y[i] * inv);
+      }
+      inv_of[n] = inv;
     } else if (live[n]) {
       load16(static_cast<const XT*>(a.x) + row * a.x_row + b * 16, v[n]);
       if (a.aux) {
@@ -200,7 +217,14 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
       float w[16];
       load16(a.weight + (tid + n * threads) * 16, w);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[n][i] = (float)((double)v[n][i] * (double)w[i] * inv);
+      for (int i = 0; i < 16; ++i) {
+        const double y = (double)v[n][i] * (double)w[i];
+        if (FORMAT == kFp8)
+          exact[n][i] = y;
+        else
+          v[n][i] = (float)(y * inv);
+      }
+      inv_of[n] = inv;
     }
   }
   if (a.y) {
@@ -208,37 +232,74 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
     for (int n = 0; n < NB; ++n) {
       if (!live[n]) continue;
       const int64_t at = row * a.y_row + (tid + n * threads) * 16;
+      if (FORMAT == kFp8) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[n][i] = (float)(exact[n][i] * inv_of[n]);
+      }
       if (a.y_bf16)
         store16(static_cast<uint16_t*>(a.y) + at, v[n]);
       else
         store16(static_cast<float*>(a.y) + at, v[n]);
     }
   }
-  if (FORMAT == kNone) return;
-  float s;
-  if (a.given) {
-    s = a.global[0];
-  } else {
-    uint32_t top = 0;                          // the largest magnitude's bits: NaN above infinity above the rest
+  if (FORMAT == kNvfp4) {
+    float s;
+    if (a.given) {
+      s = a.global[0];
+    } else {
+      unsigned top = 0;
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = !live[n] ? top : max(top, __float_as_uint(v[n][i]) & 0x7FFFFFFFu);
-    top = group_max(top, tops, lanes);
-    s = __uint_as_float(top) / (FORMAT == kNvfp4 ? kGlobalDivisor : 448.0f);
-    if (tid == 0) a.global[row] = s;
-  }
+        for (int i = 0; i < 16; ++i) top = !live[n] ? top : max(top, __float_as_uint(v[n][i]) & 0x7FFFFFFFu);
+      top = group_max(top, reinterpret_cast<unsigned*>(tops), lanes);
+      s = __uint_as_float(top) / kGlobalDivisor;
+      if (tid == 0) a.global[row] = s;
+    }
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    if (!live[n]) continue;
-    const int64_t b = row * a.blocks + tid + n * threads;
-    if (FORMAT == kNvfp4) {
+    for (int n = 0; n < NB; ++n) {
+      if (!live[n]) continue;
+      const int64_t b = row * a.blocks + tid + n * threads;
       uint32_t scale, lo, hi;
       encode_block(v[n], s, scale, lo, hi);
       a.scales[b] = (uint8_t)scale;
       reinterpret_cast<uint2*>(a.codes)[b] = make_uint2(lo, hi);
+    }
+  }
+  if (FORMAT == kFp8) {
+    double r;                                  // 1 / scale
+    bool finite = false;                       // known of the whole row
+    if (a.given) {
+      r = 1.0 / (double)a.global[0];
     } else {
-      reinterpret_cast<uint4*>(a.codes)[b] = fp8_16(v[n], s, !a.given && s == 0.0f);
+      double most = 0.0;
+      bool nan = false;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (!live[n]) continue;
+        double m = 0.0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          nan |= exact[n][i] != exact[n][i];
+          m = __builtin_fmax(m, __builtin_fabs(exact[n][i]));
+        }
+        m *= inv_of[n];
+        nan |= m != m;
+        most = __builtin_fmax(most, m);
+      }
+      unsigned long long top = nan ? 0x7FF8000000000000ull : __builtin_bit_cast(unsigned long long, most);
+      top = group_max(top, reinterpret_cast<unsigned long long*>(tops), lanes);
+      const double s = __builtin_bit_cast(double, top) / 448.0;
+      if (tid == 0) a.global[row] = (float)s;
+      finite = top < 0x7FF0000000000000ull;
+      r = s == 0.0 ? 0.0 : 1.0 / s;            // a row of zeros has scale 0: signed zeros
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (!live[n]) continue;
+      const int64_t b = row * a.blocks + tid + n * threads;
+      const double f = inv_of[n] * r;
+      reinterpret_cast<uint4*>(a.codes)[b] = finite ? fp8_16<false>(exact[n], f) : fp8_16<true>(exact[n], f);
     }
   }
 }

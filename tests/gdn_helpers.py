@@ -5,7 +5,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from tests.gpu_helpers import DEV
+from oracle import nvfp4_ref as ref
+from tests.gpu_helpers import DEV, assert_quant_equal
 
 BF16, F32 = torch.bfloat16, torch.float32
 U = 2.0 ** -24                     # half a step of fp32, relative
@@ -39,12 +40,31 @@ def silu(x: torch.Tensor) -> torch.Tensor:
 # ---- norms ---------------------------------------------------------------------------------------
 
 
-def add_norm(x, residual, w, eps):
-    """(r', fl32(y)) of add_rms_norm: from the rounded sum on in 64 bits, y rounded to fp32 once."""
+def add_norm64(x, residual, w, eps):
+    """(r', y) of add_rms_norm, from the rounded sum on in 64 bits."""
     r = x if residual is None else (x.float() + residual.float()).to(residual.dtype)
     d = r.double()
-    inv = 1.0 / torch.sqrt((d * d).mean(1, keepdim=True) + float(np.float32(eps)))
-    return r, (d * w.double() * inv).float()
+    return r, d * w.double() * (1.0 / torch.sqrt((d * d).mean(1, keepdim=True) + float(np.float32(eps))))
+
+
+def add_norm(x, residual, w, eps):
+    """(r', fl32(y))."""
+    r, y = add_norm64(x, residual, w, eps)
+    return r, y.float()
+
+
+def check_quant(q, y: torch.Tensor, quant, mode, given):
+    """The quantized output's bytes are those of y, 64 bits: NVFP4 as the oracle has it from fl32(y), FP8 the nearest."""
+    if quant == "nvfp4":
+        y = y.float().numpy()
+        assert_quant_equal(q, ref.quantize(y, ref.PER_ROW) if mode == "per_row" else ref.quantize(y, ref.GIVEN, np.float32(given)))
+        return
+    y = y.double().numpy()
+    scale = np.abs(y).max(1) / 448 if mode == "per_row" else np.full(len(y), np.float32(given), np.float64)
+    if mode == "per_row":
+        assert np.array_equal(q.scale.cpu().numpy(), scale.astype(np.float32))
+    t = y / scale[:, None]
+    assert np.array_equal(q.codes.cpu().numpy(), ref.e4m3_rne_sat(np.abs(t)) | np.where(np.signbit(t), 0x80, 0).astype(np.uint8))
 
 
 def gated_norm(x, z, w, eps):

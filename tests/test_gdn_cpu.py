@@ -164,6 +164,7 @@ def test_gated_delta_rule_workspace(nv):
 def test_launches_too_large_are_refused(nv):
     # 2^26 runs of 16 tokens: a thread more than a launch can have
     assert nv.lib.nvfp4_gdn_conv(states(nv), (1 << 30) - 1, 8, 4, A16, nv._BF16, 8, A16, None, A16, nv._BF16, 8, None) == 2
+    assert nv.lib.nvfp4_gdn_conv(states(nv, num_seqs=(1 << 31) - 1), 8, 8, 4, A16, nv._BF16, 8, A16, None, A16, nv._BF16, 8, None) == 2
     many = states(nv, num_seqs=1 << 24)
     assert nv.lib.nvfp4_gated_delta_rule(many, 1, 0, 128, 128, heads(nv), heads(nv), heads(nv), A16, A16, 0.1, heads(nv), None, 0, None) == 2
 

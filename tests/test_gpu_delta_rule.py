@@ -37,6 +37,10 @@ def test_lengths(new, past, Hk, Hv, Dk, Dv, hint):
     check(Seqs(new, past, front=1, behind=2), Hk, Hv, Dk, Dv, max_q={"none": 0, "true": max(new), "small": 1}[hint])
 
 
+def test_a_hint_far_past_the_batch():
+    check(Seqs([70, 3], [0, 2]), 1, 2, 64, 64, max_q=2 ** 63 - 1)
+
+
 @pytest.mark.parametrize("Hk,Hv,Dk,Dv", [(1, 1, 128, 32), (1, 1, 64, 512), (3, 3, 128, 96), (2, 10, 128, 160), (16, 32, 128, 128), (16, 48, 64, 64)])
 def test_heads_and_sizes(Hk, Hv, Dk, Dv):
     check(Seqs([70, 1, 5], [3, 2, 0]), Hk, Hv, Dk, Dv, seed=3)

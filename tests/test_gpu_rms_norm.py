@@ -1,11 +1,10 @@
 """Norms with quantized outputs against the 64-bit formula and the quantizer's oracle: types, widths from one block to
 the largest, strides, in-place residuals, rows of zeros, infinities and NaN."""
-import numpy as np
 import pytest
 import torch
 
 from oracle import nvfp4_ref as ref
-from tests.gdn_helpers import BF16, F32, HALF, add_norm, assert_within, gated_norm, rand, uniform
+from tests.gdn_helpers import BF16, F32, HALF, add_norm, add_norm64, assert_within, check_quant, gated_norm, rand, uniform
 from tests.gpu_helpers import DEV, assert_quant_equal, nv
 
 pytestmark = pytest.mark.gpu
@@ -15,39 +14,23 @@ def gpu(x):
     return None if x is None else x.to(DEV)
 
 
-def fp8_bytes(y: np.ndarray, scale: np.ndarray) -> np.ndarray:
-    return np.stack([ref.fp8_kv_quantize(r, s) for r, s in zip(y, scale)])
-
-
-def check_quant(q, y32, quant, mode, given):
-    """The quantized output's bytes are the oracle's of fl32(y)."""
-    y = y32.numpy()
-    if quant == "nvfp4":
-        want = ref.quantize(y, ref.PER_ROW) if mode == "per_row" else ref.quantize(y, ref.GIVEN, np.float32(given))
-        assert_quant_equal(q, want)
-    else:
-        top = np.abs(y).max(1)
-        scale = (top / np.float32(448)).astype(np.float32) if mode == "per_row" else np.full(len(y), given, np.float32)
-        if mode == "per_row":
-            assert np.array_equal(q.scale.cpu().numpy(), scale)
-        assert np.array_equal(q.codes.cpu().numpy(), fp8_bytes(y, scale))
-
-
 @pytest.mark.parametrize("rows,cols", [(1, 16), (3, 48), (1, 5120), (5, 1040), (2, 16384), (2, 16400), (1, 32768), (300, 256)])
 @pytest.mark.parametrize("xt,rt", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16), (BF16, None), (F32, None)])
 def test_add_rms_norm(rows, cols, xt, rt):
     x = rand(rows, cols, seed=1, dtype=xt, scale=1.5)
     r = None if rt is None else rand(rows, cols, seed=2, dtype=rt, scale=3.0)
     w = 0.5 + uniform(cols, seed=3)
-    r_want, y32 = add_norm(x, r, w, 1e-6)
+    r_want, y64 = add_norm64(x, r, w, 1e-6)
+    y32 = y64.float()
     for quant, mode in (("nvfp4", "per_row"), ("nvfp4", "given"), ("fp8", "per_row"), ("fp8", "given")):
         given = 0.013
         s = torch.full((1,), given, device=DEV) if mode == "given" else None
         y, q, r_out = nv().add_rms_norm(gpu(x), gpu(w), gpu(r), out_dtype=F32, quant=quant, mode=mode, scale=s)
         assert_within(y, y32.double(), U_ONE * y32.double().abs())
         assert (r_out is None) if r is None else torch.equal(r_out.cpu(), r_want)
-        check_quant(q, y.cpu(), quant, mode, given)              # of the same launch's fp32 output
-        check_quant(q, y32, quant, mode, given)                  # and of the formula's
+        if quant == "nvfp4":
+            check_quant(q, y.cpu(), quant, mode, given)          # of the same launch's fp32 output
+        check_quant(q, y64, quant, mode, given)                  # and of the formula's
         alone = nv().add_rms_norm(gpu(x), gpu(w), gpu(r), out_dtype=None, quant=quant, mode=mode, scale=s)
         assert alone[0] is None and torch.equal(alone[1].codes, q.codes)
     yb, none, _ = nv().add_rms_norm(gpu(x), gpu(w), gpu(r))
@@ -92,7 +75,7 @@ def test_rows_of_zeros_and_tiny_rows(quant):
     w = torch.ones(64)
     y, q, _ = nv().add_rms_norm(gpu(x), gpu(w), eps=1e-6, out_dtype=F32, quant=quant)
     assert (y[:2] == 0).all() and torch.isfinite(y).all()
-    check_quant(some_rows(q, quant, slice(2, 4)), y[2:].cpu(), quant, "per_row", None)
+    check_quant(some_rows(q, quant, slice(2, 4)), add_norm64(x[2:], None, w, 1e-6)[1], quant, "per_row", None)
     if quant == "nvfp4":
         assert_quant_equal(q, ref.quantize(y.cpu().numpy(), ref.PER_ROW))
         assert (q.scales[:2] == 0).all() and (q.codes[0] == 0).all() and q.global_scale[0] == 0
@@ -130,7 +113,7 @@ def test_gated_rms_norm(T, H, D, xt, zt):
         s = torch.full((1,), 0.02, device=DEV) if mode == "given" else None
         none, q = nv().gated_rms_norm(gpu(x), zg, gpu(w), out_dtype=None, quant=quant, mode=mode, scale=s)
         assert none is None
-        check_quant(q, y.cpu(), quant, mode, 0.02)
+        check_quant(q, want, quant, mode, 0.02)
     for dtype in (BF16, F32):
         y, none = nv().gated_rms_norm(gpu(x), zg, gpu(w), out_dtype=dtype)
         assert none is None
@@ -159,11 +142,12 @@ def test_no_rows():
 @pytest.mark.parametrize("eps", [0.0, 1e-3])
 def test_short_rows_share_wavefronts(rows, cols, eps):
     x, w = rand(rows, cols, seed=10, scale=2.0), 0.5 + uniform(cols, seed=11)
-    _, y32 = add_norm(x, None, w, eps)
+    _, y64 = add_norm64(x, None, w, eps)
+    y32 = y64.float()
     for quant in ("nvfp4", "fp8"):
         y, q, _ = nv().add_rms_norm(gpu(x), gpu(w), eps=eps, out_dtype=F32, quant=quant)
         assert torch.equal(y.cpu(), y32)
-        check_quant(q, y32, quant, "per_row", None)
+        check_quant(q, y64, quant, "per_row", None)
     assert torch.equal(nv().add_rms_norm(gpu(x), gpu(w), eps=eps)[0].cpu(), y32.to(BF16))
 
 
@@ -175,5 +159,24 @@ def test_short_rows_of_heads(T, H, D, eps):
     for quant in ("nvfp4", "fp8"):
         y, q = nv().gated_rms_norm(gpu(x), gpu(z), gpu(w), eps=eps, out_dtype=F32, quant=quant)
         assert_within(y, want, tol + HALF[F32] * want.abs())
-        check_quant(q, y.cpu(), quant, "per_row", None)
+        check_quant(q, want, quant, "per_row", None)
     assert_within(nv().gated_rms_norm(gpu(x), gpu(z), gpu(w), eps=eps)[0], want, tol32 + HALF[BF16] * want.abs())
+
+
+@pytest.mark.parametrize("given", [None, 2.0 ** -6, 0.013])
+def test_fp8_bytes_next_to_borders(given):
+    # quotients that lie on a border between two E4M3 values, or a rounding in fp32 away from it
+    x = torch.full((64, 256), 0.5, dtype=F32)
+    steps = torch.arange(256, dtype=torch.float64)
+    border = (1 + (2 * (steps % 8) + 1) / 16) * 2.0 ** (steps // 8 % 12 - 6)
+    w = (border * (1 + 2.0 ** -23 * (steps // 96 - 1))).float()
+    x[:, 0] = 1.0 + torch.arange(64) * 2.0 ** -18              # norms that differ in their last bits
+    _, y64 = add_norm64(x, None, w, 0.0)
+    s = None if given is None else torch.full((1,), given, device=DEV)
+    _, q, _ = nv().add_rms_norm(gpu(x), gpu(w), eps=0.0, out_dtype=None, quant="fp8", mode="per_row" if given is None else "given", scale=s)
+    check_quant(q, y64, "fp8", "per_row" if given is None else "given", given)
+    z = gpu(torch.full((64, 4, 64), 1.5))
+    _, q = nv().gated_rms_norm(gpu(x).unflatten(1, (4, 64)), z, gpu(w[:64]), eps=0.0, out_dtype=None, quant="fp8",
+                               mode="per_row" if given is None else "given", scale=s)
+    want = gated_norm(x.unflatten(1, (4, 64)), z.cpu(), w[:64], 0.0)[0].flatten(1)
+    check_quant(q, want, "fp8", "per_row" if given is None else "given", given)
