@@ -822,17 +822,26 @@ struct Scan {
     f_at.next(more);
   }
 
-  // The largest |beta v| of 16 tokens, by column, for the block's units.
-  __device__ __forceinline__ void write_top(int block) {
+  // The largest |beta v| of 16 tokens, by column, for the block's units: read, then written.
+  struct TopRows {
+    float4 beta;
+    uint32_t v[NC][4];
+  };
+  __device__ __forceinline__ void read_top(TopRows& t, int block) {
     const int slot = block % kRing, row = 16 * (w - 4) + 4 * g;
-    const float4 b4 = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]);
-    const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+    t.beta = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) t.v[nc][r] = lds.V[slot][row + r][nc * 16 + c];
+  }
+  __device__ __forceinline__ void write_top(const TopRows& t, int block) {
+    const float b[4] = {t.beta.x, t.beta.y, t.beta.z, t.beta.w};
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       uint32_t m = 0;                          // as bits, so that a NaN is the largest
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        m = max(m, __float_as_uint(b[r] * __uint_as_float((uint32_t)lds.V[slot][row + r][nc * 16 + c] << 16)) & 0x7FFFFFFFu);
+      for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(b[r] * __uint_as_float(t.v[nc][r] << 16)) & 0x7FFFFFFFu);
       atomicMax(&lds.top[block % 3][nc * 16 + c], m);
     }
   }
@@ -880,12 +889,21 @@ struct Scan {
     lds_barrier();
     f32x4_t y[NC];
     float4 scale[NC];
+    half8_t state[NC][KS];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) state[nc][ks] = lds.S[nc][ks][lane];
     const float e = lds.rows[b % kRing][3][16 * (w - 4) + c];
+    here();
+    TopRows top;                               // used behind the next barrier
+    read_top(top, b + 1);
+    here();
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       y[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(lds.S[nc][ks][lane], s.q[ks], y[nc]);
+      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(state[nc][ks], s.q[ks], y[nc]);
       const float4 ratio = *reinterpret_cast<const float4*>(&lds.units[b & 1][0][nc * 16 + 4 * g]);
       scale[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][1][nc * 16 + 4 * g]);
       y[nc][0] *= e * ratio.x;
@@ -894,7 +912,7 @@ struct Scan {
       y[nc][3] *= e * ratio.w;
     }
     lds_barrier();
-    write_top(b + 1);
+    write_top(top, b + 1);
     load_q(s, b + 3 < blocks);
     if (w == 7 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
     lds_barrier();
@@ -915,7 +933,9 @@ struct Scan {
     load_a(even, blocks > 1);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(KS + 2));       // the first block's copies are in
     lds_barrier();
-    write_top(0);
+    TopRows top;
+    read_top(top, 0);
+    write_top(top, 0);
     copy_rows(1);
     load_q(odd, blocks > 2);
     load_a(odd, blocks > 2);
