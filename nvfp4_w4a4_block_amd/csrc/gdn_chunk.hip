@@ -993,7 +993,7 @@ int launch_dk(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, hipStream_
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
   // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.2 us
   // with 16 columns and 1.9 us with 32 (one sequence of 8192 tokens, 256 slices of 16: 160 against 240 us; eight of
-  // 1023, 2048 slices: 186 against 145).  As many sequences as the tokens give of the longest.
+  // 1023, 2048 slices: 186 against 142).  As many sequences as the tokens give of the longest.
   const int64_t longest = max_q > a.s.tokens ? a.s.tokens : max_q > kTok ? max_q : kTok;
   const int64_t seqs = (a.s.tokens + longest - 1) / longest;
   const int64_t slices = (seqs < a.s.num_seqs ? seqs : a.s.num_seqs) * a.v_heads * (a.v_dim / 16);
