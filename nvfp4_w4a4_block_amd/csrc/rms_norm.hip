@@ -14,8 +14,8 @@
 // order of a sum.  The NVFP4 bytes are the quantizer's of fl32(y), the FP8 bytes the values nearest to y / scale, with one
 // rounding and, per row, max|y| / 448 before its own to fp32 (quotients of fl32(y) in fp32 put one byte in about three
 // million on a border's other side; 2049 x 4096 fp32: 12 us, 11 that way).  gated_rms_norm without a quantized output works in fp32, which hides its exponential behind the
-// loads (8192 tokens of 32 heads of 128, bf16 output: 30 us, 58 in 64 bits; NVFP4 output, in 64 bits: 58 us, bound by its
-// 580 64-bit instructions for 16 elements).
+// loads (8192 tokens of 32 heads of 128, bf16 output: 30 us, 58 in 64 bits; NVFP4 output, in 64 bits: 55 us, FP8 63 us,
+// bound by their thousand instructions, half of them of 64 bits, for 16 elements).
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -105,28 +105,25 @@ __device__ __forceinline__ uint4 fp8_16(const double (&y)[16], double f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// z sigmoid(z) to about 2^-45.  e^-z = 2^n 2^f, |f| <= 1/2, 2^f by its Taylor series to the power 11 (the next term is
-// below 2^-46); the quotient by two Newton steps from the hardware's estimate.
+// z sigmoid(z) to about 2^-44.  e^-z = 2^n 2^f, |f| <= 1/2, n by adding 1.5 * 2^52, whose last bits are then n; 2^f by the
+// polynomial of degree 9 through its values at ten Chebyshev nodes (off by 2^-46); the quotient by a Newton step from the
+// hardware's estimate (2^-24 or better).
 __device__ __forceinline__ double silu(double z) {
-  const double t = __builtin_fmin(__builtin_fmax(z * -1.4426950408889634074, -1000.0), 1000.0);
-  const double n = __builtin_rint(t), f = t - n;
-  double p = 4.4455382718708114976e-10;         // ln(2)^11 / 11!
-  p = __builtin_fma(p, f, 7.0549116208011233299e-9);
-  p = __builtin_fma(p, f, 1.0178086009239699728e-7);
-  p = __builtin_fma(p, f, 1.3215486790144309488e-6);
-  p = __builtin_fma(p, f, 1.5252733804059840280e-5);
-  p = __builtin_fma(p, f, 1.5403530393381609954e-4);
-  p = __builtin_fma(p, f, 1.3333558146428443423e-3);
-  p = __builtin_fma(p, f, 9.6181291076284771619e-3);
-  p = __builtin_fma(p, f, 5.5504108664821579953e-2);
-  p = __builtin_fma(p, f, 2.4022650695910071233e-1);
-  p = __builtin_fma(p, f, 6.9314718055994530942e-1);
-  p = __builtin_fma(p, f, 1.0);
-  const double d = 1.0 + __builtin_ldexp(p, (int)n);
-  double r = __builtin_amdgcn_rcp(d);
-  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-  return z * r;
+  const double t = (double)__builtin_amdgcn_fmed3f((float)z, -700.0f, 700.0f) * -1.4426950408889634074;
+  const double m = t + 0x1.8p52, f = t - (m - 0x1.8p52);
+  double p = 1.0205905413765595e-07;
+  p = __builtin_fma(p, f, 1.325964524488711e-06);
+  p = __builtin_fma(p, f, 1.5252672924850737e-05);
+  p = __builtin_fma(p, f, 0.0001540343375125101);
+  p = __builtin_fma(p, f, 0.0013333558200794592);
+  p = __builtin_fma(p, f, 0.009618129193934313);
+  p = __builtin_fma(p, f, 0.05550410866465167);
+  p = __builtin_fma(p, f, 0.2402265069564034);
+  p = __builtin_fma(p, f, 0.6931471805599462);
+  p = __builtin_fma(p, f, 1.0000000000000135);
+  const double d = 1.0 + __builtin_ldexp(p, (int)(uint32_t)__builtin_bit_cast(uint64_t, m));
+  const double r = __builtin_amdgcn_rcp(d);
+  return z * __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
 // In fp32, by the hardware's exponential and reciprocal (a unit in the last place each); the exponential's argument is
