@@ -126,8 +126,8 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(DeltaArgs a, int s
 
 // Sequences of at most this many new tokens go token by token, the whole call where the longest is known to be no longer.
 // A token's step is 1.4 us where the states fill the machine once, a block about the same for one token as for 64.  By
-// steps against in blocks, us, with 32 heads of 128 x 128: one sequence of 8 tokens 14 / 16, of 17 27 / 17; eight of 17
-// 31 / 35, of 24 42 / 36; 64 of 16 147 / 194, of 24 212 / 197.
+// steps against in blocks, us, with 32 heads of 128 x 128: one sequence of 8 tokens 14 / 15, of 17 27 / 16; eight of 16
+// 30 / 34, of 24 42 / 34; 64 of 16 142 / 175, of 24 208 / 179.
 constexpr int kShort = 16;
 
 size_t gated_delta_rule_workspace_bytes(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t k_heads, int64_t v_heads,
