@@ -9,8 +9,9 @@
 // sequence, one workgroup per value head and slice of state columns (the columns do not meet).
 //
 // Precision.  State, sums, T and statistics are fp32.  Matrix operands are fp16: k and q rows scaled by powers of two
-// (exact but for elements below 2^-16 of a row's largest); S, R, T, U in two parts (2^-22), R and U and S in units of a
-// power of two per column that keeps them in range; what only reaches the bf16 output (S and U there, A) in one (2^-11).
+// (exact but for elements below 2^-16 of a row's largest); S, R, T, U, A in two parts (2^-22), R and U and S in units of a
+// power of two per column that keeps them in range.  (With S, U and A in one part where they only reach the bf16 output the
+// outputs were off by 2^-11 of what the state holds, many steps of an output far below that.)
 // That scale rests on the contraction (finite values, g <= 0, 0 <= beta <= 2): a column's 2-norm stays below the
 // running sum B <- e^G B + sum |beta v|.  Where a block breaks that premise the scan gives up its slice with a flag, and
 // the token-by-token kernel, which runs behind it, takes the slice from the sequence's start.
@@ -25,7 +26,7 @@ namespace {
 
 constexpr int kTok = 64;           // tokens of a block
 
-// Workspace of one block: K and Q fragments per key head, T (two parts) and A fragments and row factors per value
+// Workspace of one block: K and Q fragments per key head, T and A fragments (two parts each) and row factors per value
 // head.  A fragment is the 64 lanes' 16 B of one matrix operand; of a lower triangular 64 x 64 operand only the six
 // (row block, half) pairs that are not all zero are kept.
 constexpr int kTriFrags = 6;
@@ -52,13 +53,19 @@ __device__ __forceinline__ half2_t to_half2(float a, float b) {
   return __builtin_convertvector((f32x2_t){a, b}, half2_t);
 }
 
-// Four values in two fp16 parts.  `one` is 1.0f where the compiler does not see it: x - (float)h is then one mixed
-// multiply-add instead of a conversion and a difference.
-__device__ __forceinline__ void split4(const f32x4_t x, half4_t& hi, half4_t& lo, float one) {
+// The second of two parts, times kPart where it says so: it is no larger than the first one then, and as small values
+// keep their bits.
+constexpr float kPart = 0x1p11f;
+// T and A (at most 2) are multiplied by kTri: both parts of elements down to 2^-28 are normal numbers.
+constexpr float kTri = 0x1p14f;
+
+// Four values in two fp16 parts, x = hi + lo / part.  `one` is 1.0f where the compiler does not see it: x - (float)h is then
+// one mixed multiply-add instead of a conversion and a difference.
+__device__ __forceinline__ void split4(const f32x4_t x, half4_t& hi, half4_t& lo, float one, float part = kPart) {
   const half2_t a = to_half2(x[0], x[1]), b = to_half2(x[2], x[3]);
   hi = half4_t{a[0], a[1], b[0], b[1]};
-  const half2_t c = to_half2(__builtin_fmaf((float)a[0], -one, x[0]), __builtin_fmaf((float)a[1], -one, x[1]));
-  const half2_t d = to_half2(__builtin_fmaf((float)b[0], -one, x[2]), __builtin_fmaf((float)b[1], -one, x[3]));
+  const half2_t c = to_half2(part * __builtin_fmaf((float)a[0], -one, x[0]), part * __builtin_fmaf((float)a[1], -one, x[1]));
+  const half2_t d = to_half2(part * __builtin_fmaf((float)b[0], -one, x[2]), part * __builtin_fmaf((float)b[1], -one, x[3]));
   lo = half4_t{c[0], c[1], d[0], d[1]};
 }
 __device__ __forceinline__ float hidden_one() {
@@ -291,6 +298,7 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
     const f32x4_t row_hi = *reinterpret_cast<const f32x4_t*>(&decay_hi[half][row]), row_lo = *reinterpret_cast<const f32x4_t*>(&decay_lo[half][row]);
     const f32x4_t row_k = *reinterpret_cast<const f32x4_t*>(&betas[half][row]) * *reinterpret_cast<const f32x4_t*>(&unit_k[row]);
     const f32x4_t row_q = *reinterpret_cast<const f32x4_t*>(&unit_q[row]);
+    half4_t a_low[4];                          // the second parts of A
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j <= w) {
@@ -306,16 +314,31 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
             q = i >= col ? q : 0.0f;
           }
           L[i][col] = l;
+          q *= kTri;
           At[i][col] = (_Float16)q;
+          a_low[j][r] = (_Float16)(kPart * (q - (float)(_Float16)q));
         }
       } else if (j == w + 1 && (w & 1) == 0) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) At[16 * w + 4 * g + r][16 * j + c] = (_Float16)0.0f;
       }
     }
-    // the diagonal block is this wavefront's own: no barrier between its rows and their use
+    // the diagonal block and the rows of A are this wavefront's own: no barrier between them and their use
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
+    half8_t* a_out = reinterpret_cast<half8_t*>(ws.a) + 2 * ((int64_t)block * a.v_heads + head) * kTriFrags * 64;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      if (ks <= (w >> 1)) (a_out + 2 * tri_frag(w, ks) * 64)[threadIdx.x & 63] = *reinterpret_cast<const half8_t*>(&At[16 * w + c][ks * 32 + g * 8]);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    // they take the first ones' place
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= w) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) At[16 * w + 4 * g + r][16 * j + c] = a_low[j][r];
+      }
     {
       // forward substitution for column c of the block, four known elements taken out of all later rows at once
       float x[16];
@@ -387,7 +410,7 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
         for (int i = 0; i < 2; ++i) {
           half4_t h, l;
           const float4 x = reinterpret_cast<const float4*>(row)[i];
-          split4(f32x4_t{x.x, x.y, x.z, x.w}, h, l, 1.0f);
+          split4(f32x4_t{kTri * x.x, kTri * x.y, kTri * x.z, kTri * x.w}, h, l, 1.0f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             hi[4 * i + j] = h[j];
@@ -397,7 +420,7 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
         const int64_t frag = frag0 + tri_frag(w, ks);
         reinterpret_cast<half8_t*>(ws.t)[(2 * frag) * 64 + lane] = hi;
         reinterpret_cast<half8_t*>(ws.t)[(2 * frag + 1) * 64 + lane] = lo;
-        reinterpret_cast<half8_t*>(ws.a)[frag * 64 + lane] = *reinterpret_cast<const half8_t*>(&At[16 * w + c][ks * 32 + g * 8]);
+        reinterpret_cast<half8_t*>(ws.a)[(2 * frag + 1) * 64 + lane] = *reinterpret_cast<const half8_t*>(&At[16 * w + c][ks * 32 + g * 8]);
       }
   }
 }
@@ -410,7 +433,7 @@ struct SolveStage {
 };
 template <int KS>
 struct OutStage {
-  half8_t q[KS], a[2];             // 16 tokens
+  half8_t q[KS], a_hi[2], a_lo[2]; // 16 tokens
 };
 
 // Values and row factors wait in LDS from six blocks ahead on: they come from memory, not from other workgroups' reads.
@@ -456,10 +479,10 @@ struct Scan {
   static constexpr int KS = DK / 32;
   struct Lds {
     f32x4_t X[KS][4][NC][64];                  // K S of a wavefront's channels, 16 tokens each
-    half8_t S[NC][KS][64];                     // the state's upper part, as an operand
+    half8_t S[2][NC][KS][64];                  // the state in two parts, as an operand
     _Float16 R[2][NC][16][kTok + 8];
     _Float16 U[2][NC][16][kTok + 8];           // U times the decays to the block's end, in two parts
-    _Float16 O[2][NC][16][kTok + 8];           // U for the outputs, of two blocks
+    _Float16 O[2][2][NC][16][kTok + 8];        // U for the outputs, of two blocks, in two parts
     half4_t K[KS][2][kTok * 4];                // a wavefront's channels of K in two 16s, for their transposition
     uint16_t V[kRing][kTok][16 * NC];          // values
     float rows[kRing][4][kTok];                // row factors: beta, c, d, e
@@ -506,11 +529,11 @@ struct Scan {
     return (token * 4 + part) ^ (odd * 18);
   }
 
-  // Four values of two results' rows as one operand, in two parts.
+  // Four values of two results' rows as one operand, in two parts of one unit: both go into one sum.
   __device__ __forceinline__ void operand(const f32x4_t& x, const f32x4_t& y, half8_t& hi, half8_t& lo) const {
     half4_t a0, b0, a1, b1;
-    split4(x, a0, b0, one);
-    split4(y, a1, b1, one);
+    split4(x, a0, b0, one, 1.0f);
+    split4(y, a1, b1, one, 1.0f);
     hi = half8_t{a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
     lo = half8_t{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
   }
@@ -566,8 +589,8 @@ struct Scan {
       unit(most, up[nc], now);
       ratio[nc] = was * up[nc];
       if (w == 3 && g == 0) {
-        lds.units[b & 1][0][nc * 16 + c] = ratio[nc];
-        lds.units[b & 1][1][nc * 16 + c] = now * a.scale;
+        lds.units[b & 1][0][nc * 16 + c] = kTri * ratio[nc];
+        lds.units[b & 1][1][nc * 16 + c] = now * (a.scale / kTri);
       }
       bound[nc] = __builtin_fmaf(decay, bound[nc], more) * 1.00001f;
       unit(bound[nc], state_up, state_unit[nc]);
@@ -600,7 +623,8 @@ struct Scan {
         for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], hi, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], lo, x[j]);
-        lds.S[nc][w][lane] = hi;
+        lds.S[0][nc][w][lane] = hi;
+        lds.S[1][nc][w][lane] = lo;
 #pragma unroll
         for (int j = 0; j < 4; ++j) lds.X[w][j][nc][lane] = x[j];
       }
@@ -658,14 +682,16 @@ struct Scan {
         ul = mfma(s.t_lo[1], rh[1][nc], ul);
         ul = mfma(s.t_hi[1], rl[1][nc], ul);
       }
-      u += ul;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) u[r] = __builtin_fmaf(ul[r], 1.0f / kPart, u[r]) * (1.0f / kTri);
       const float d[4] = {d4.x, d4.y, d4.z, d4.w};
-      half4_t uh, uw;
+      half4_t uh, uw, oh, ow;
       split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, uh, uw, one);
       *reinterpret_cast<half4_t*>(&lds.U[0][nc][c][16 * w + 4 * g]) = uh;
       *reinterpret_cast<half4_t*>(&lds.U[1][nc][c][16 * w + 4 * g]) = uw;
-      const half2_t ua = to_half2(u[0], u[1]), ub = to_half2(u[2], u[3]);
-      *reinterpret_cast<half4_t*>(&lds.O[b & 1][nc][c][16 * w + 4 * g]) = half4_t{ua[0], ua[1], ub[0], ub[1]};
+      split4(u, oh, ow, one);
+      *reinterpret_cast<half4_t*>(&lds.O[b & 1][0][nc][c][16 * w + 4 * g]) = oh;
+      *reinterpret_cast<half4_t*>(&lds.O[b & 1][1][nc][c][16 * w + 4 * g]) = ow;
     }
     half8_t kt[2][2];
     if (owner()) {
@@ -709,15 +735,18 @@ struct Scan {
     if (owner()) {
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) {
+        f32x4_t low[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) S[i][nc] = mfma(kt[ks][i], ul[ks][nc], S[i][nc]);
+          for (int i = 0; i < 2; ++i) low[i] = mfma(kt[ks][i], ul[ks][nc], low[i]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) S[i][nc] = mfma(kt[ks][i], uh[ks][nc], S[i][nc]);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) S[i][nc] *= back[nc];
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[i][nc][r] = __builtin_fmaf(low[i][r], 1.0f / kPart, S[i][nc][r]) * back[nc];
       }
     }
   }
@@ -787,6 +816,8 @@ struct Scan {
 
   // ---- the output half: results transposed, a lane holds 4 neighbouring columns of token c
 
+  static constexpr int kLoads = KS + 4;        // of a block: Q's and A's fragments
+
   Walk q_at, a_at, f_at, v_at, o_at;           // the block to load or copy next, and the one to write
 
   __device__ __forceinline__ void load_q(OutStage<KS>& s, bool more) {
@@ -797,7 +828,11 @@ struct Scan {
   __device__ __forceinline__ void load_a(OutStage<KS>& s, bool more) {
     const int o = w - 4;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) s.a[ks] = load_at<half8_t>(a_at.p, tri_frag(o, min(ks, o >> 1)) * 1024 + lane * 16);
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint32_t frag = tri_frag(o, min(ks, o >> 1)) * 2048 + lane * 16;
+      s.a_hi[ks] = load_at<half8_t>(a_at.p, frag);
+      s.a_lo[ks] = load_at<half8_t>(a_at.p, frag + 1024);
+    }
     a_at.next(more);
   }
 
@@ -855,10 +890,18 @@ struct Scan {
         const_cast<char*>(o_at.p), 0, ((uint32_t)(rows_here - 1) * (uint32_t)a.o_tok + 16 * NC) * 2, 0x00027000);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
+      f32x4_t low = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        if (ks <= (o >> 1))
-          y[nc] = mfma(*reinterpret_cast<const half8_t*>(&lds.O[b & 1][nc][c][ks * 32 + g * 8]), s.a[ks], y[nc]);
+      for (int ks = 0; ks < 2; ++ks) {
+        if (ks > (o >> 1)) continue;
+        const half8_t hi = *reinterpret_cast<const half8_t*>(&lds.O[b & 1][0][nc][c][ks * 32 + g * 8]);
+        const half8_t lo = *reinterpret_cast<const half8_t*>(&lds.O[b & 1][1][nc][c][ks * 32 + g * 8]);
+        y[nc] = mfma(hi, s.a_hi[ks], y[nc]);
+        low = mfma(hi, s.a_lo[ks], low);
+        low = mfma(lo, s.a_hi[ks], low);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[nc][r] = __builtin_fmaf(low[r], 1.0f / kPart, y[nc][r]);
       const u32x2_t two = {bf16_pair(y[nc][0] * scale[nc].x, y[nc][1] * scale[nc].y),
                            bf16_pair(y[nc][2] * scale[nc].z, y[nc][3] * scale[nc].w)};
       __builtin_amdgcn_raw_buffer_store_b64(two, out, lane_at, nc * 32, 0);
@@ -869,8 +912,8 @@ struct Scan {
   __device__ __forceinline__ void out_block(OutStage<KS>& s, int b, uint32_t lane_at) {
     // The copies begin with two blocks (all workgroups begin at once, and wait for the first) and go on by two a block,
     // 2 b + 2 and 2 b + 3, up to a lead of kAhead = 6.  Then this wavefront waits until its part of the next block's are
-    // in, by what it has issued since at least; a block issues its copies, KS + 2 loads and a store.  For block 1 that is
-    // KS + 2 loads and two copies, for 2 more; for 3 two blocks and four copies, for 4 to 8 more; from 9 on kAhead - 1
+    // in, by what it has issued since at least; a block issues its copies, kLoads loads and a store.  For block 1 that is
+    // kLoads loads and two copies, for 2 more; for 3 two blocks and four copies, for 4 to 8 more; from 9 on kAhead - 1
     // blocks and copies.
     int turn = b;
     asm("" : "+s"(turn));                      // one loop for all of them
@@ -881,19 +924,21 @@ struct Scan {
       copy_rows(b + kAhead);
     }
     if (turn < 2)
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(KS + 4));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads + 2));
     else if (turn < 8)
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * KS + 10));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * (kLoads + 1) + 4));
     else
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm((kAhead - 1) * (KS + 3)));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm((kAhead - 1) * (kLoads + 1)));
     lds_barrier();
     f32x4_t y[NC];
     float4 scale[NC];
-    half8_t state[NC][KS];
+    half8_t state[2][NC][KS];
 #pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
+    for (int part = 0; part < 2; ++part)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) state[nc][ks] = lds.S[nc][ks][lane];
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) state[part][nc][ks] = lds.S[part][nc][ks][lane];
     const float e = lds.rows[b % kRing][3][16 * (w - 4) + c];
     here();
     TopRows top;                               // used behind the next barrier
@@ -903,7 +948,9 @@ struct Scan {
     for (int nc = 0; nc < NC; ++nc) {
       y[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(state[nc][ks], s.q[ks], y[nc]);
+      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(state[0][nc][ks], s.q[ks], y[nc]);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(state[1][nc][ks], s.q[ks], y[nc]);
       const float4 ratio = *reinterpret_cast<const float4*>(&lds.units[b & 1][0][nc * 16 + 4 * g]);
       scale[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][1][nc * 16 + 4 * g]);
       y[nc][0] *= e * ratio.x;
@@ -924,14 +971,14 @@ struct Scan {
     const uint32_t lane_at = (uint32_t)((16 * (w - 4) + c) * (uint32_t)a.o_tok + 4 * g) * 2;
     OutStage<KS> even, odd;
     q_at = walk(ws.q, a.k_heads, k_head, 4 * KS * 1024);
-    a_at = walk(ws.a, a.v_heads, head, kTriFrags * 1024);
+    a_at = walk(ws.a, a.v_heads, head, kTriFrags * 2048);
     f_at = walk(ws.factors, a.v_heads, head, kFactors * 4);
     v_at = Walk{reinterpret_cast<const char*>(a.v + rows.first * a.v_tok + head * a.v_head + c0), kTok * 2 * a.v_tok};
     o_at = Walk{reinterpret_cast<const char*>(a.out + rows.first * a.o_tok + head * a.o_head + c0), kTok * 2 * a.o_tok};
     copy_rows(0);
     load_q(even, blocks > 1);
     load_a(even, blocks > 1);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(KS + 2));       // the first block's copies are in
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads));       // the first block's copies are in
     lds_barrier();
     TopRows top;
     read_top(top, 0);
@@ -1016,7 +1063,7 @@ size_t chunk_workspace(int64_t tokens, int64_t num_seqs, int64_t k_heads, int64_
   ws.k = reinterpret_cast<_Float16*>(take(ws.blocks * k_heads * kTok * k_dim * 2));
   ws.q = reinterpret_cast<_Float16*>(take(ws.blocks * k_heads * kTok * k_dim * 2));
   ws.t = reinterpret_cast<_Float16*>(take(ws.blocks * v_heads * kTriFrags * 2 * 1024));
-  ws.a = reinterpret_cast<_Float16*>(take(ws.blocks * v_heads * kTriFrags * 1024));
+  ws.a = reinterpret_cast<_Float16*>(take(ws.blocks * v_heads * kTriFrags * 2 * 1024));
   ws.factors = reinterpret_cast<float*>(take(ws.blocks * v_heads * kFactors * 4));
   ws.flags = reinterpret_cast<uint8_t*>(take(num_seqs * v_heads * (v_dim / 16)));
   return (size_t)(p - static_cast<char*>(base));
