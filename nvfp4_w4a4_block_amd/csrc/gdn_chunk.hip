@@ -481,7 +481,7 @@ struct Scan {
     f32x4_t X[KS][4][NC][64];                  // K S of a wavefront's channels, 16 tokens each
     half8_t S[2][NC][KS][64];                  // the state in two parts, as an operand
     _Float16 R[2][NC][16][kTok + 8];
-    _Float16 U[2][NC][16][kTok + 8];           // U times the decays to the block's end, in two parts
+    _Float16 U[2][NC][16][kTok + 8];           // U times the decays to the block's end, in the state's unit, in two parts
     _Float16 O[2][2][NC][16][kTok + 8];        // U for the outputs, of two blocks, in two parts
     half4_t K[KS][2][kTok * 4];                // a wavefront's channels of K in two 16s, for their transposition
     uint16_t V[kRing][kTok][16 * NC];          // values
@@ -548,9 +548,9 @@ struct Scan {
   // ---- the solving half
 
   f32x4_t S[2][NC];                            // rows 32 w + 16 i + 4 g + r of column c
-  // Of a column: its norm's bound and the unit of S behind the block; the block's unit and its inverse, and the ratios
-  // from the state's unit to the block's and back.
-  float bound[NC], state_unit[NC], up[NC], ratio[NC], to_state[NC];
+  // Of a column: its norm's bound and the unit of S behind the block; the block's unit, inverse; the ratios from the
+  // unit of S before the block to the block's and to that behind it, and from the block's to that.
+  float bound[NC], state_unit[NC], up[NC], ratio[NC], carry[NC], to_state[NC];
   float last_unit[NC];                         // of S as it is between blocks
   Walk k_at, t_at;
   bool bad = false;
@@ -577,7 +577,8 @@ struct Scan {
 
   // Units of a block, by column, from the bound before it (one more block is opened behind the last, which sees what
   // that one's decay says): everything in the block is below bound + 64 max|beta v|,
-  // updates below three times that.  Between blocks S has a unit by its bound alone, which follows strong decays.
+  // updates below three times that.  Between blocks S has a unit by its bound alone, which follows strong decays: to 2^-100 of
+  // the block's, so that the ratios stay in range whatever the decay.  The updates go into S in that unit.
   __device__ __forceinline__ void open_block(int b) {
     const float decay = lds.decay[b % kRing][lane];
 #pragma unroll
@@ -593,8 +594,9 @@ struct Scan {
         lds.units[b & 1][1][nc * 16 + c] = now * (a.scale / kTri);
       }
       bound[nc] = __builtin_fmaf(decay, bound[nc], more) * 1.00001f;
-      unit(bound[nc], state_up, state_unit[nc]);
+      unit(__builtin_fmaxf(bound[nc], 0x1p-100f * most), state_up, state_unit[nc]);
       to_state[nc] = now * state_up;
+      carry[nc] = was * state_up;
     }
   }
 
@@ -686,7 +688,8 @@ struct Scan {
       for (int r = 0; r < 4; ++r) u[r] = __builtin_fmaf(ul[r], 1.0f / kPart, u[r]) * (1.0f / kTri);
       const float d[4] = {d4.x, d4.y, d4.z, d4.w};
       half4_t uh, uw, oh, ow;
-      split4(f32x4_t{u[0] * d[0], u[1] * d[1], u[2] * d[2], u[3] * d[3]}, uh, uw, one);
+      const float to = to_state[nc];
+      split4(f32x4_t{u[0] * (d[0] * to), u[1] * (d[1] * to), u[2] * (d[2] * to), u[3] * (d[3] * to)}, uh, uw, one);
       *reinterpret_cast<half4_t*>(&lds.U[0][nc][c][16 * w + 4 * g]) = uh;
       *reinterpret_cast<half4_t*>(&lds.U[1][nc][c][16 * w + 4 * g]) = uw;
       split4(u, oh, ow, one);
@@ -708,16 +711,14 @@ struct Scan {
           kt[ks][i] = half8_t{p[0][0], p[0][1], p[0][2], p[0][3], p[1][0], p[1][1], p[1][2], p[1][3]};
         }
     }
-    float back[NC];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      back[nc] = to_state[nc];
       last_unit[nc] = state_unit[nc];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) S[i][nc] *= decay * ratio[nc];
+      for (int i = 0; i < 2; ++i) S[i][nc] *= decay * carry[nc];
     }
     lds_barrier();
-    // S <- decay S + K^T U in the block's unit, then in the state's
+    // S <- decay S + K^T U
     half8_t uh[2][NC], ul[2][NC];
     if (owner()) {
 #pragma unroll
@@ -746,7 +747,7 @@ struct Scan {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[i][nc][r] = __builtin_fmaf(low[i][r], 1.0f / kPart, S[i][nc][r]) * back[nc];
+          for (int r = 0; r < 4; ++r) S[i][nc][r] = __builtin_fmaf(low[i][r], 1.0f / kPart, S[i][nc][r]);
       }
     }
   }
