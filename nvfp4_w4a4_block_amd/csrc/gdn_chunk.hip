@@ -13,8 +13,12 @@
 // power of two per column that keeps them in range.  (With S, U and A in one part where they only reach the bf16 output the
 // outputs were off by 2^-11 of what the state holds, many steps of an output far below that.)
 // That scale rests on the contraction (finite values, g <= 0, 0 <= beta <= 2): a column's 2-norm stays below the
-// running sum B <- e^G B + sum |beta v|.  Where a block breaks that premise the scan gives up its slice with a flag, and
-// the token-by-token kernel, which runs behind it, takes the slice from the sequence's start.
+// running sum B <- e^G B + sum |beta v|.  A block's unit goes by the largest that its bound M can become in it, and leaves
+// 2^-48 M of an element: a token that writes far less than M, or a small state before a large write, would lose its bits to
+// what comes after it.  So where a token writes less than kRange M at most (its largest column of the slice) and the old state
+// has decayed below that by the block's end, or where a block breaks the premise, the scan gives up its slice with a flag, and
+// the token-by-token kernel, which runs behind it, takes the slice from the sequence's start.  (Tokens that write nothing,
+// padding for one, do not count: 2^-48 M is what their outputs are held to.)
 #include <type_traits>
 
 #include "gdn_chunk.h"
@@ -53,19 +57,18 @@ __device__ __forceinline__ half2_t to_half2(float a, float b) {
   return __builtin_convertvector((f32x2_t){a, b}, half2_t);
 }
 
-// The second of two parts, times kPart where it says so: it is no larger than the first one then, and as small values
-// keep their bits.
+// The second of two parts, times kPart: it is no larger than the first one then, and as small values keep their bits.
 constexpr float kPart = 0x1p11f;
 // T and A (at most 2) are multiplied by kTri: both parts of elements down to 2^-28 are normal numbers.
 constexpr float kTri = 0x1p14f;
 
-// Four values in two fp16 parts, x = hi + lo / part.  `one` is 1.0f where the compiler does not see it: x - (float)h is then
+// Four values in two fp16 parts, x = hi + lo / kPart.  `one` is 1.0f where the compiler does not see it: x - (float)h is then
 // one mixed multiply-add instead of a conversion and a difference.
-__device__ __forceinline__ void split4(const f32x4_t x, half4_t& hi, half4_t& lo, float one, float part = kPart) {
+__device__ __forceinline__ void split4(const f32x4_t x, half4_t& hi, half4_t& lo, float one) {
   const half2_t a = to_half2(x[0], x[1]), b = to_half2(x[2], x[3]);
   hi = half4_t{a[0], a[1], b[0], b[1]};
-  const half2_t c = to_half2(part * __builtin_fmaf((float)a[0], -one, x[0]), part * __builtin_fmaf((float)a[1], -one, x[1]));
-  const half2_t d = to_half2(part * __builtin_fmaf((float)b[0], -one, x[2]), part * __builtin_fmaf((float)b[1], -one, x[3]));
+  const half2_t c = to_half2(kPart * __builtin_fmaf((float)a[0], -one, x[0]), kPart * __builtin_fmaf((float)a[1], -one, x[1]));
+  const half2_t d = to_half2(kPart * __builtin_fmaf((float)b[0], -one, x[2]), kPart * __builtin_fmaf((float)b[1], -one, x[3]));
   lo = half4_t{c[0], c[1], d[0], d[1]};
 }
 __device__ __forceinline__ float hidden_one() {
@@ -102,6 +105,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, moved<0x141>(v));
   if (LANES == 16) v = max(v, moved<0x140>(v));
   return v;
+}
+
+// Smallest of a wavefront's values, in lane 63.
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+  v = min(v, moved<0xB1>(v));
+  v = min(v, moved<0x4E>(v));
+  v = min(v, moved<0x141>(v));
+  v = min(v, moved<0x140>(v));
+  v = min(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x142, 0xA, 0xF, false));     // rows 0, 2 to 1, 3
+  return min(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x143, 0xC, 0xF, false));  // lane 31 to rows 2, 3
 }
 
 // 8 elements of a row of q or k as fp16, the row (DK / 8 neighbouring lanes) scaled by a power of two `sc` to a largest
@@ -427,6 +440,10 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
 
 constexpr int kScanThreads = 512;
 
+// Range of what a block's tokens write: 2^-48 M is 2^-20 of the smallest then.  Beside values of order 1 (M about 200) that
+// takes a token's strength, in all columns, below 10^-6.
+constexpr float kRange = 0x1p-28f;
+
 // What a wavefront of the solving half needs of one block in registers, and one of the output half.
 struct SolveStage {
   half8_t k[4], t_hi[2], t_lo[2];  // k: 32 channels of all 64 tokens
@@ -477,6 +494,7 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
 template <int DK, int NC>
 struct Scan {
   static constexpr int KS = DK / 32;
+  static constexpr uint32_t kNone = 0x7F800000u;         // a token that writes nothing: infinity
   struct Lds {
     f32x4_t X[KS][4][NC][64];                  // K S of a wavefront's channels, 16 tokens each
     half8_t S[2][NC][KS][64];                  // the state in two parts, as an operand
@@ -489,6 +507,7 @@ struct Scan {
     float decay[kRing][64];                    // of the whole block, copies; NaN where it is out of the scale's premise
     float norm[KS][NC * 16];
     uint32_t top[3][NC * 16];                  // largest |beta v| of a block, as bits
+    float least[3][4];                         // 16 tokens each: the smallest of their largest |beta v|, zeros aside
     float units[2][2][NC * 16];                // for the output half: ratio, and the block's unit times the scale
   };
 
@@ -529,11 +548,11 @@ struct Scan {
     return (token * 4 + part) ^ (odd * 18);
   }
 
-  // Four values of two results' rows as one operand, in two parts of one unit: both go into one sum.
+  // Four values of two results' rows as one operand, in two parts.
   __device__ __forceinline__ void operand(const f32x4_t& x, const f32x4_t& y, half8_t& hi, half8_t& lo) const {
     half4_t a0, b0, a1, b1;
-    split4(x, a0, b0, one, 1.0f);
-    split4(y, a1, b1, one, 1.0f);
+    split4(x, a0, b0, one);
+    split4(y, a1, b1, one);
     hi = half8_t{a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
     lo = half8_t{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
   }
@@ -580,12 +599,13 @@ struct Scan {
   // updates below three times that.  Between blocks S has a unit by its bound alone, which follows strong decays: to 2^-100 of
   // the block's, so that the ratios stay in range whatever the decay.  The updates go into S in that unit.
   __device__ __forceinline__ void open_block(int b) {
-    const float decay = lds.decay[b % kRing][lane];
+    const float decay = lds.decay[b % kRing][lane], *tokens = lds.least[b % 3];
+    const float least = __builtin_fminf(__builtin_fminf(tokens[0], tokens[1]), __builtin_fminf(tokens[2], tokens[3]));
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       const float more = 64.0f * __uint_as_float(lds.top[b % 3][nc * 16 + c]);
       const float most = bound[nc] + more, was = state_unit[nc];
-      bad |= !(most < 0x1p100f);
+      bad |= !(most < 0x1p100f) || __builtin_fmaxf(least, decay * bound[nc]) < kRange * most;
       float now, state_up;
       unit(most, up[nc], now);
       ratio[nc] = was * up[nc];
@@ -623,8 +643,9 @@ struct Scan {
         operand(S[0][nc], S[1][nc], hi, lo);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], hi, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+        // K / kPart is as good as K beside the second part: its elements are off by 2^-14 of a row's largest at most
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j], lo, x[j]);
+        for (int j = 0; j < 4; ++j) x[j] = mfma(s.k[j] * (_Float16)(1.0f / kPart), lo, x[j]);
         lds.S[0][nc][w][lane] = hi;
         lds.S[1][nc][w][lane] = lo;
 #pragma unroll
@@ -858,14 +879,20 @@ struct Scan {
     f_at.next(more);
   }
 
-  // The largest |beta v| of 16 tokens, by column, for the block's units: read, then written.
+  // The largest |beta v| of 16 tokens, by column, for the block's units, and the tokens' smallest: read, then written.
   struct TopRows {
     float4 beta;
     uint32_t v[NC][4];
+    float beta_of;                             // of token lane / 4, a quarter of whose values follows
+    uint32_t row[2 * NC];
   };
   __device__ __forceinline__ void read_top(TopRows& t, int block) {
     const int slot = block % kRing, row = 16 * (w - 4) + 4 * g;
     t.beta = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]);
+    const int token = 16 * (w - 4) + (lane >> 2);
+    t.beta_of = lds.rows[slot][0][token];
+#pragma unroll
+    for (int i = 0; i < 2 * NC; ++i) t.row[i] = reinterpret_cast<const uint32_t*>(&lds.V[slot][token][(lane & 3) * 4 * NC])[i];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -880,6 +907,16 @@ struct Scan {
       for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(b[r] * __uint_as_float(t.v[nc][r] << 16)) & 0x7FFFFFFFu);
       atomicMax(&lds.top[block % 3][nc * 16 + c], m);
     }
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t two = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2 * NC; ++i) two = __builtin_elementwise_max(two, __builtin_bit_cast(u16x2_t, t.row[i] & 0x7FFF7FFFu));
+    uint32_t most = max(two[0], two[1]);
+    most = max(most, moved<0xB1>(most));       // of the token's four lanes
+    most = max(most, moved<0x4E>(most));
+    const float m = t.beta_of * __uint_as_float(most << 16);
+    const uint32_t least = wave_min(m > 0.0f ? __float_as_uint(m) : kNone);
+    if (lane == 63) lds.least[block % 3][w - 4] = __uint_as_float(least);
   }
 
   // A U and the stores of a block, its Q S in y.
@@ -947,11 +984,15 @@ struct Scan {
     here();
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      y[nc] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4_t low = {0.0f, 0.0f, 0.0f, 0.0f};
+      y[nc] = low;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(state[0][nc][ks], s.q[ks], y[nc]);
+      for (int ks = 0; ks < KS; ++ks) {
+        y[nc] = mfma(state[0][nc][ks], s.q[ks], y[nc]);
+        low = mfma(state[1][nc][ks], s.q[ks], low);
+      }
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) y[nc] = mfma(state[1][nc][ks], s.q[ks], y[nc]);
+      for (int r = 0; r < 4; ++r) y[nc][r] = __builtin_fmaf(low[r], 1.0f / kPart, y[nc][r]);
       const float4 ratio = *reinterpret_cast<const float4*>(&lds.units[b & 1][0][nc * 16 + 4 * g]);
       scale[nc] = *reinterpret_cast<const float4*>(&lds.units[b & 1][1][nc * 16 + 4 * g]);
       y[nc][0] *= e * ratio.x;

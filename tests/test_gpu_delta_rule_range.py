@@ -1,0 +1,71 @@
+"""Values of one block that lie far apart: a token has no influence on those before it, however large it is, and what
+follows a reset is exact, however large the state was."""
+import pytest
+import torch
+
+from tests.delta_range_helpers import exact_rule
+from tests.gdn_helpers import Seqs, assert_within, delta_inputs
+from tests.test_gpu_delta_rule import run
+
+pytestmark = pytest.mark.gpu
+
+SIZES = [8, 16, 22, 30, 40, 60, 88]
+
+
+def check(b, q, k, v, g, beta, state):
+    out, states = run(b, q, k, v, g, beta, state)
+    o, o_tol, s, s_tol = exact_rule(b, q, k, v, g, beta, state)
+    assert_within(out, o, o_tol, "out")
+    assert_within(states, s, s_tol, "states")
+    return out
+
+
+@pytest.mark.parametrize("n,at", [(16, 9), (17, 9), (100, 50), (100, 70), (200, 63), (200, 128)])
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("columns", ["all", "one"])
+def test_a_large_token(n, at, size, columns):
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=35)
+    v = v.float()
+    rows = [at, n + at]
+    if columns == "all":
+        v[rows] *= 2.0 ** size
+    else:
+        v[rows, 1, 5] *= 2.0 ** size
+    check(b, q, k, v.bfloat16(), g, beta, state)
+
+
+@pytest.mark.parametrize("n,at", [(16, 9), (17, 9), (100, 50), (100, 70), (200, 63), (200, 128)])
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("decay", ["reset", "steep"])
+def test_a_large_state_that_is_forgotten(n, at, size, decay):
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=37)
+    state = state * 2.0 ** size
+    if decay == "reset":
+        g[[at, n + at]] = -1e4
+    else:
+        g[at:at + 6], g[n + at:n + at + 6] = -0.12 * size, -0.12 * size          # e^-0.72 size = 2^-1.04 size
+    check(b, q, k, v, g, beta, state)
+
+
+@pytest.mark.parametrize("n", [60, 100, 260])
+@pytest.mark.parametrize("strong", [False, True])
+def test_tokens_of_zeros(n, strong):
+    # padding in front, within and behind: rows of zeros write nothing, whatever decays
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=39, strong=strong)
+    q, k, v = q.clone(), k.clone(), v.clone()
+    for lo, hi in ((0, 20), (30, 33), (40, 45), (n - 10, n), (n, n + 25)):
+        q[lo:hi], k[lo:hi], v[lo:hi] = 0.0, 0.0, 0.0
+    out = check(b, q, k, v, g, beta, state)
+    assert (out[:20] == 0).all() and (out[n:n + 25] == 0).all()
+
+
+@pytest.mark.parametrize("n", [17, 100])
+@pytest.mark.parametrize("size", [16, 24, 40])
+def test_strengths_near_none(n, size):
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=41)
+    beta[::3] = 2.0 ** -size
+    check(b, q, k, v, g, beta, state)
