@@ -37,15 +37,17 @@ __device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[N]) {
 }
 
 // x <- x / sqrt(x.x + 1e-6), a lane holding R of the row's values.  Ahead of the products with the state, so that
-// those stay in range; a row whose squares do not is scaled down first (1e-6 is nothing beside it).
+// those stay in range; a row whose squares do not is scaled by 2^-80 first, which makes 1e-6 less than 2^-179: nothing
+// beside a scaled sum of 2^-60 and more.
 template <int R>
 __device__ __forceinline__ void unit_row(float (&x)[R]) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < R; ++i) s = __builtin_fmaf(x[i], x[i], s);
   s = rows_sum(s);
+  float eps = 1e-6f;
   if (!(s < 0x1p100f)) {
-    s = 0.0f;
+    s = eps = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       x[i] *= 0x1p-80f;
@@ -53,7 +55,7 @@ __device__ __forceinline__ void unit_row(float (&x)[R]) {
     }
     s = rows_sum(s);
   }
-  const float r = 1.0f / __builtin_sqrtf(s + 1e-6f);
+  const float r = 1.0f / __builtin_sqrtf(s + eps);
 #pragma unroll
   for (int i = 0; i < R; ++i) x[i] *= r;
 }
