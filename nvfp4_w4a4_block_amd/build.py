@@ -53,11 +53,12 @@ def _stderr(res: subprocess.CompletedProcess) -> str:
 
 
 def check_m0(asm: str) -> int:
-    """The GEMM's direct-to-LDS copies set M0 from inline assembly, which cannot tell the
-    compiler that M0 changes.  Check on the generated gfx950 assembly that every M0 write is one
-    of those copies (immediately followed by its global_load_lds), that nothing else touches M0
-    and that every global_load_lds follows its own M0 write.  Returns the number of copies;
-    raises RuntimeError otherwise."""
+    """The direct-to-LDS copies set M0 from inline assembly, which cannot tell the compiler that
+    M0 changes, and which it does not search for hazards.  Check on generated gfx950 assembly that
+    every M0 write is one of those copies (followed by the wait state that a load to LDS needs
+    behind it, and its global_load_lds), that nothing else touches M0 and that every
+    global_load_lds follows its own M0 write.  Returns the number of copies; raises RuntimeError
+    otherwise."""
     import re
     code = [l.strip() for l in asm.splitlines()]
     code = [l for l in code if l and not l.startswith((";", "."))]
@@ -67,11 +68,11 @@ def check_m0(asm: str) -> int:
             continue
         if not re.fullmatch(r"s_mov_b32 m0, (s\d+|vcc_lo|vcc_hi)", l):
             raise RuntimeError(f"M0 used outside the LDS copies: {l}")
-        if i + 1 >= len(code) or not code[i + 1].startswith("global_load_lds_dword"):
-            raise RuntimeError(f"M0 write not followed by its copy: {l}")
+        if i + 2 >= len(code) or code[i + 1] != "s_nop 0" or not code[i + 2].startswith("global_load_lds_dword"):
+            raise RuntimeError(f"M0 write not followed by its wait state and copy: {l}")
         writes += 1
     loads = [i for i, l in enumerate(code) if l.startswith("global_load_lds")]
-    if not writes or any(not code[i - 1].startswith("s_mov_b32 m0,") for i in loads):
+    if not writes or any(not code[i - 2].startswith("s_mov_b32 m0,") for i in loads):
         raise RuntimeError("a global_load_lds does not follow its own M0 write")
     return writes
 

@@ -460,16 +460,17 @@ static_assert(kAhead == 6, "the first blocks' order and counts in out_block");
 // Copies 16 B (4 B) a lane from memory to LDS, lane l's to dst + 16 l (4 l): base + off, base and dst (an LDS address) the
 // same for all lanes.  From inline assembly, so that the compiler does not make every later LDS read wait for it; the copies write
 // no registers, and the kernel orders them itself: they are issued behind a barrier that follows every read of what
-// they overwrite, waited for by count and published with a barrier.  Nothing else in this file uses M0, which the build
-// checks on the generated assembly.
+// they overwrite, waited for by count and published with a barrier.  The s_nop is the wait state that a scalar write of M0
+// needs before a load to LDS; the compiler inserts none inside inline assembly.  Nothing else in this file uses M0.  The
+// build checks both on the generated assembly.
 typedef __attribute__((address_space(3))) void lds_void_t;
 __device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, uint32_t dst) {
   const uint32_t to = __builtin_amdgcn_readfirstlane(dst);
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
 }
 __device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, uint32_t dst) {
   const uint32_t to = __builtin_amdgcn_readfirstlane(dst);
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
 }
 // s_waitcnt immediate that waits for at most n outstanding vector memory operations.
 constexpr int vmcnt_imm(int n) { return (n & 15) | 0x0F70 | ((n >> 4) << 14); }

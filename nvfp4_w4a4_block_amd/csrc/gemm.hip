@@ -225,17 +225,19 @@ __device__ __forceinline__ int slot_swizzle(int row) { return (row ^ (row >> 3))
 // registers; the K loop orders it explicitly: a stage's copies are waited for (vmcnt(0)) and
 // published with a barrier before any wavefront reads that stage, and they are issued only
 // after a barrier that follows every read of the buffer they overwrite.  lds_dst must be the
-// same for every lane.  M0 cannot be named as clobbered (the compiler reserves it); nothing
-// else in this file's kernels uses M0, which a CPU test checks on the generated assembly.
+// same for every lane.  The s_nop is the wait state that a scalar write of M0 needs before a load
+// to LDS; the compiler inserts none inside inline assembly.  M0 cannot be named as clobbered (the
+// compiler reserves it); nothing else in this file's kernels uses M0.  The build checks both on the
+// generated assembly.
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* base, uint32_t off, const uint8_t* lds_dst) {
   const uint32_t dst = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t*)lds_dst);
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory");
 }
 
 // The same with 4 B per lane (lane l lands at lds_dst + 4 l: 256 B per wavefront).
 __device__ __forceinline__ void copy4_to_lds(const uint8_t* base, uint32_t off, const uint8_t* lds_dst) {
   const uint32_t dst = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void_t*)lds_dst);
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(dst) : "memory");
 }
 
 // Enqueue the copy of K step kt of both operands straight into LDS (no registers): each
