@@ -233,8 +233,7 @@ def build(verbose: bool = False) -> str:
         with open(s) as f:
             text = f.read()
         check_m0(text)
-        if s == listings[0]:
-            check_lds_refills(text)
+        check_lds_refills(text)
     for lib, o in ((LIB, objs), (CALIB_LIB, calib_objs)):
         tmp = lib + ".tmp"
         res = _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *o, "-o", tmp], verbose)

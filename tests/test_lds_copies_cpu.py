@@ -44,3 +44,11 @@ def test_check_wants_the_wait_state():
                 good + "s_add_u32 s0, m0, 1\n", good.replace("s4", "0x100"), "s_mov_b32 m0, s4\ns_nop 0\n", "s_nop 0\n"):
         with pytest.raises(RuntimeError):
             b.check_m0(bad)
+
+
+def test_copies_wait_for_reads_in_every_listing(listings):
+    for name, asm in listings.items():
+        found = b.check_lds_refills(asm)
+        assert found, name
+        if name == "gdn_chunk.hip":
+            assert len(found) == 4 and not any(found.values()), found
