@@ -77,20 +77,11 @@ def check_m0(asm: str) -> int:
     return writes
 
 
-def lds_reads_in_flight_at_copies(asm: str) -> dict:
-    """For each kernel of a gfx950 assembly listing that issues direct-to-LDS copies
-    (global_load_lds): the largest number of LDS reads that may still be in flight when such a
-    copy is issued, over every path through the kernel's branches.  A copy lands in LDS
-    asynchronously, so a read of the bytes it overwrites must be complete before it is issued.
-
-    Model: LDS instructions complete in issue order; scalar memory loads also count in lgkmcnt
-    but complete in any order, so `s_waitcnt lgkmcnt(N)` is taken to retire them first (the
-    case that leaves the most LDS reads in flight) and then the oldest LDS operations until at
-    most N remain.  Only the newest 64 operations are tracked: a wait keeps at most its
-    newest 15 (the counter is 4 bits wide), so older ones never change a result.  Returns
-    {kernel symbol: count}."""
+def _kernel_blocks(asm: str, having: str) -> dict:
+    """The kernels of a gfx950 assembly listing with an instruction (or mark) that starts with
+    `having`: {symbol: (basic blocks, lists of lines; the successors of block i, a function)}.
+    Comments are dropped but for marks, `; ring: N ...`, which become lines `ring_mark N`."""
     import re
-    result = {}
     funcs, cur = [], None
     for raw in asm.splitlines():
         m = re.match(r"^([A-Za-z_][\w.$]*):", raw)
@@ -103,11 +94,13 @@ def lds_reads_in_flight_at_copies(asm: str) -> dict:
         if raw.startswith(".Lfunc_end"):
             cur = None
             continue
-        line = raw.split(";")[0].strip()
+        mark = re.match(r"\s*; ring: (\d+)\b", raw)
+        line = f"ring_mark {mark.group(1)}" if mark else raw.split(";")[0].strip()
         if line:
             cur[1].append(line)
+    result = {}
     for name, lines in funcs:
-        if not any(l.startswith("global_load_lds") for l in lines):
+        if not any(l.startswith(having) for l in lines):
             continue
         # basic blocks: a label starts one, a branch or s_endpgm ends one
         blocks, labels, blk = [], {}, []
@@ -127,10 +120,11 @@ def lds_reads_in_flight_at_copies(asm: str) -> dict:
                 blk = []
         if blk:
             blocks.append(blk)
+
         # successors of block i: a branch target (a label maps to the block that follows it)
         # and, unless the block ends in an unconditional branch or the end of the program, the
         # next block
-        def succ(i):
+        def succ(i, name=name, blocks=blocks, labels=labels):
             last = blocks[i][-1] if blocks[i] else ""
             op = last.split()[0] if last else ""
             out = []
@@ -147,6 +141,25 @@ def lds_reads_in_flight_at_copies(asm: str) -> dict:
                 out.append(i + 1)
             return [t for t in out if t < len(blocks)]
 
+        result[name] = (blocks, succ)
+    return result
+
+
+def lds_reads_in_flight_at_copies(asm: str) -> dict:
+    """For each kernel of a gfx950 assembly listing that issues direct-to-LDS copies
+    (global_load_lds): the largest number of LDS reads that may still be in flight when such a
+    copy is issued, over every path through the kernel's branches.  A copy lands in LDS
+    asynchronously, so a read of the bytes it overwrites must be complete before it is issued.
+
+    Model: LDS instructions complete in issue order; scalar memory loads also count in lgkmcnt
+    but complete in any order, so `s_waitcnt lgkmcnt(N)` is taken to retire them first (the
+    case that leaves the most LDS reads in flight) and then the oldest LDS operations until at
+    most N remain.  Only the newest 64 operations are tracked: a wait keeps at most its
+    newest 15 (the counter is 4 bits wide), so older ones never change a result.  Returns
+    {kernel symbol: count}."""
+    import re
+    result = {}
+    for name, (blocks, succ) in _kernel_blocks(asm, "global_load_lds").items():
         def step(q, l):
             op = l.split()[0]
             if op.startswith("ds_"):
@@ -182,6 +195,35 @@ def lds_reads_in_flight_at_copies(asm: str) -> dict:
                         raise RuntimeError(f"{name}: too many paths to follow")
                     work.append((t, q))
         result[name] = worst
+    return result
+
+
+def check_ring_marks(asm: str) -> dict:
+    """Kernels whose waits for direct-to-LDS copies count the loads and stores issued behind them
+    mark how many they count on: `; ring: N ...` says that at least N loads and stores (copies
+    aside) follow before the next mark.  Check that on every path of the generated gfx950
+    assembly; returns {kernel symbol: number of marks}, raises RuntimeError otherwise."""
+    result = {}
+    for name, (blocks, succ) in _kernel_blocks(asm, "ring_mark").items():
+        marks = [(i, j) for i, blk in enumerate(blocks) for j, l in enumerate(blk) if l.startswith("ring_mark")]
+        for i, j in marks:
+            want = int(blocks[i][j].split()[1])
+            fewest, work = {}, [(i, j + 1, 0)]           # by block: operations since the mark at its entry
+            while work:
+                at, first, n = work.pop()
+                for l in blocks[at][first:]:
+                    if l.startswith("ring_mark") or l.startswith("s_endpgm"):
+                        if n < want:
+                            raise RuntimeError(f"{name}: {n} loads and stores behind a mark of {want}")
+                        break
+                    n += l.startswith(("global_", "buffer_", "flat_")) and not l.startswith("global_load_lds")
+                    n = min(n, want)
+                else:
+                    for t in succ(at):
+                        if n < fewest.get(t, want + 1):
+                            fewest[t] = n
+                            work.append((t, 0, n))
+        result[name] = len(marks)
     return result
 
 
@@ -234,6 +276,7 @@ def build(verbose: bool = False) -> str:
             text = f.read()
         check_m0(text)
         check_lds_refills(text)
+        check_ring_marks(text)
     for lib, o in ((LIB, objs), (CALIB_LIB, calib_objs)):
         tmp = lib + ".tmp"
         res = _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *o, "-o", tmp], verbose)

@@ -472,6 +472,13 @@ __device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, uin
   const uint32_t to = __builtin_amdgcn_readfirstlane(dst);
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "s"(to) : "memory");
 }
+// The waits for the copies count the loads and stores issued behind them, which the compiler could move or drop: at least N of
+// them stand between this place and the next one marked, on every path, or the build, which looks at the generated
+// assembly, fails.
+template <int N>
+__device__ __forceinline__ void ring_mark() {
+  asm volatile("; ring: %0 loads and stores" : : "n"(N) : "memory");
+}
 // s_waitcnt immediate that waits for at most n outstanding vector memory operations.
 constexpr int vmcnt_imm(int n) { return (n & 15) | 0x0F70 | ((n >> 4) << 14); }
 
@@ -948,12 +955,15 @@ struct Scan {
     o_at.p += o_at.step;
   }
 
+  // LAST: behind the loop over pairs of blocks.  No wait follows, and its loads, which nobody needs, may be dropped.
+  template <bool LAST = false>
   __device__ __forceinline__ void out_block(OutStage<KS>& s, int b, uint32_t lane_at) {
     // The copies begin with two blocks (all workgroups begin at once, and wait for the first) and go on by two a block,
     // 2 b + 2 and 2 b + 3, up to a lead of kAhead = 6.  Then this wavefront waits until its part of the next block's are
     // in, by what it has issued since at least; a block issues its copies, kLoads loads and a store.  For block 1 that is
     // kLoads loads and two copies, for 2 more; for 3 two blocks and four copies, for 4 to 8 more; from 9 on kAhead - 1
     // blocks and copies.
+    ring_mark<LAST ? 0 : kLoads + 1>();
     int turn = b;
     asm("" : "+s"(turn));                      // one loop for all of them
     if (turn < 4) {
@@ -1019,14 +1029,17 @@ struct Scan {
     v_at = Walk{reinterpret_cast<const char*>(a.v + rows.first * a.v_tok + head * a.v_head + c0), kTok * 2 * a.v_tok};
     o_at = Walk{reinterpret_cast<const char*>(a.out + rows.first * a.o_tok + head * a.o_head + c0), kTok * 2 * a.o_tok};
     copy_rows(0);
+    ring_mark<kLoads>();
     load_q(even, blocks > 1);
     load_a(even, blocks > 1);
+    ring_mark<0>();
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads));       // the first block's copies are in
     lds_barrier();
     TopRows top;
     read_top(top, 0);
     write_top(top, 0);
     copy_rows(1);
+    ring_mark<kLoads>();
     load_q(odd, blocks > 2);
     load_a(odd, blocks > 2);
     lds_barrier();
@@ -1035,7 +1048,8 @@ struct Scan {
       out_block(even, b, lane_at);
       out_block(odd, b + 1, lane_at);
     }
-    if (b < blocks) out_block(even, b, lane_at);
+    if (b < blocks) out_block<true>(even, b, lane_at);
+    ring_mark<0>();
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // no copy outlives the workgroup's LDS
   }
 };

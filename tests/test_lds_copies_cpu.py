@@ -52,3 +52,26 @@ def test_copies_wait_for_reads_in_every_listing(listings):
         assert found, name
         if name == "gdn_chunk.hip":
             assert len(found) == 4 and not any(found.values()), found
+
+
+def test_loads_and_stores_that_the_ring_counts_on_are_there(listings):
+    marks = b.check_ring_marks(listings["gdn_chunk.hip"])
+    # two in front of the loop's three copies of the block, two around the first wait, one behind
+    assert len(marks) == 4 and all("chunk_scan_kernel" in k and n >= 5 for k, n in marks.items()), marks
+    assert b.check_ring_marks(listings["gemm.hip"]) == {}
+
+
+def _kernel(body):
+    return "k:\n" + "\n".join("\t" + l if not l.startswith(".LBB") else l for l in body) + "\n.Lfunc_end0:\n"
+
+
+def test_ring_marks_count_the_shortest_path():
+    mark, load, store, copy = "; ring: 2 loads and stores", "global_load_dwordx4 v[0:3], v4, s[0:1]", "buffer_store_dwordx2 v[0:1], v2, s[0:3], 0 offen", "global_load_lds_dword v2, s[0:1]"
+    end = ["; ring: 0 loads and stores", "s_endpgm"]
+    assert b.check_ring_marks(_kernel([mark, load, store] + end)) == {"k": 2}
+    assert b.check_ring_marks(_kernel([mark, ".LBB0_1:", load, load, mark, store, load, "s_cbranch_scc1 .LBB0_1"] + end)) == {"k": 3}
+    for bad in ([mark, load] + end, [mark, load, copy] + end, [mark, "ds_read_b32 v0, v1", load] + end,
+                [mark, load, "s_cbranch_scc1 .LBB0_1", store, ".LBB0_1:"] + end,
+                [mark, load, load, ".LBB0_1:", mark, load, "s_cbranch_scc1 .LBB0_1", store] + end):
+        with pytest.raises(RuntimeError):
+            b.check_ring_marks(_kernel(bad))
