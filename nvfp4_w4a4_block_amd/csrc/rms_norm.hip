@@ -107,9 +107,10 @@ __device__ __forceinline__ uint4 fp8_16(const double (&y)[16], double f) {
 
 // z sigmoid(z) to about 2^-44.  e^-z = 2^n 2^f, |f| <= 1/2, n by adding 1.5 * 2^52, whose last bits are then n; 2^f by the
 // polynomial of degree 9 through its values at ten Chebyshev nodes (off by 2^-46); the quotient by a Newton step from the
-// hardware's estimate (2^-24 or better).
-__device__ __forceinline__ double silu(double z) {
-  const double t = (double)__builtin_amdgcn_fmed3f((float)z, -700.0f, 700.0f) * -1.4426950408889634074;
+// hardware's estimate (2^-24 or better).  Minus infinity gives what the formula does, -inf * 0: not a number.
+__device__ __forceinline__ double silu64(float gate) {
+  const double z = gate == -__builtin_inff() ? __builtin_nanf("") : gate;
+  const double t = (double)__builtin_amdgcn_fmed3f(gate, -700.0f, 700.0f) * -1.4426950408889634074;
   const double m = t + 0x1.8p52, f = t - (m - 0x1.8p52);
   double p = 1.0205905413765595e-07;
   p = __builtin_fma(p, f, 1.325964524488711e-06);
@@ -128,7 +129,7 @@ __device__ __forceinline__ double silu(double z) {
 
 // In fp32, by the hardware's exponential and reciprocal (a unit in the last place each); the exponential's argument is
 // rounded, so |z| 2^-24 relative.
-__device__ __forceinline__ float silu(float z) {
+__device__ __forceinline__ float silu32(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
 }
 
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
         for (int i = 0; i < 16; ++i) {
           const Real x = v[n][i];
           total += x * x;
-          y[i] = x * (Real)w[i] * silu((Real)z[i]);
+          y[i] = x * (Real)w[i] * (FORMAT == kNone ? (Real)silu32(z[i]) : (Real)silu64(z[i]));
         }
       }
       // a head's blocks lie in neighbouring lanes
