@@ -39,6 +39,9 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
     widen(reinterpret_cast<const uint4*>(p)[i], v + i * (16 / sizeof(T)), static_cast<const T*>(nullptr));
 }
 
+__device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float one(const float* p) { return *p; }
+
 __device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
   uint4* o = reinterpret_cast<uint4*>(p);
   o[0] = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
   float v[NB][16];
   double exact[FORMAT == kFp8 ? NB : 1][16];   // FP8: y is this times inv_of
   double inv_of[NB];
-  bool live[NB];
+  bool live[NB], again[NB];
   double sum = 0.0;
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
@@ -184,7 +187,14 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
       }
       // a head's blocks lie in neighbouring lanes
       for (int m = 1; m < a.head_blocks; m *= 2) total += __shfl_xor(total, m, 64);
-      const Real inv = (Real)1 / root(total / (Real)(a.head_blocks * 16) + (Real)a.eps);
+      const Real mean = total / (Real)(a.head_blocks * 16) + (Real)a.eps, inv = (Real)1 / root(mean);
+      if (FORMAT == kNone) {
+        // what fp32 does not hold: squares that overflow or vanish, products with the gate that overflow ahead of the norm
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = __builtin_fmaxf(most, __builtin_fabsf((float)y[i]));
+        again[n] = live[n] && (!(total < (Real)0x1p100) || mean < (Real)0x1p-40 || most > 0x1p100f);
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (FORMAT == kFp8)
@@ -223,6 +233,33 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
           v[n][i] = (float)(y * inv);
       }
       inv_of[n] = inv;
+    }
+  }
+  if (GATED && FORMAT == kNone) {
+    // such heads once more, in 64 bits and from memory, so that nothing is kept ready for it
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (__builtin_amdgcn_ballot_w64(again[n]) == 0) continue;
+      const int b = tid + n * threads, head = b / a.head_blocks, c = (b - head * a.head_blocks) * 16;
+      const XT* x = static_cast<const XT*>(a.x) + row * a.x_row + head * a.x_head + c;
+      const AT* z = static_cast<const AT*>(a.aux) + row * a.aux_row + head * a.aux_head + c;
+      double squares = 0.0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const double v = live[n] ? one(x + i) : 0.0f;
+        squares = __builtin_fma(v, v, squares);
+      }
+      for (int m = 1; m < a.head_blocks; m *= 2) {
+        squares += __shfl_xor(squares, m, 64);
+        again[n] |= __shfl_xor((int)again[n], m, 64) != 0;
+      }
+      if (!again[n] || !live[n]) continue;
+      const double inv = 1.0 / __builtin_sqrt(squares / (double)(a.head_blocks * 16) + (double)a.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[n][i] = (float)((double)one(x + i) * (double)a.weight[c + i] * silu64(one(z + i)) * inv);
+        __builtin_amdgcn_sched_barrier(0);               // one after the other: few registers
+      }
     }
   }
   if (a.y) {
