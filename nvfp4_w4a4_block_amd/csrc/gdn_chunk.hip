@@ -232,9 +232,9 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
     }
     if (w == 0) {
       // lane t: the sum of the log2 decays up to token t, in 64 bits: differences of far sums keep their last bits.  Decays
-      // below 2^-1000 are as good as that one, and sums of it stay finite in fp32.
+      // below 2^-1000, to 0, are as good as that one, and sums of it stay finite in fp32.
       const float gt = lane < m ? g_load : 0.0f, beta = lane < m ? beta_load : 0.0f;
-      off = __builtin_amdgcn_ballot_w64(!(gt <= 0.0f && gt >= -3e38f) || !(beta >= 0.0f && beta <= 2.0f)) != 0;
+      off = __builtin_amdgcn_ballot_w64(!(gt <= 0.0f) || !(beta >= 0.0f && beta <= 2.0f)) != 0;
       sum = running_sum(__builtin_fmax((double)gt * 1.4426950408889634074, -1000.0));
       const float hi = (float)sum;
       decay_hi[half][lane] = hi;

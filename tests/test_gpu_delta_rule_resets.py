@@ -45,3 +45,15 @@ def test_a_bound_that_grew_over_blocks(nothing):
     assert_within(out, o, o_tol + 2.0 ** -26 * o.abs().amax(), "out")      # M grows by 64 |beta v| a block: 2^5 blocks more of it
     assert_within(states, s, s_tol + 2.0 ** -26 * s.abs().amax(), "states")
     assert (out[at + 5:at + 64] == 0).all()
+
+
+@pytest.mark.parametrize("n", [9, 100, 200])
+def test_a_decay_to_zero_is_any_other_reset(n):
+    # e^-inf = e^-1e4 = 0: the same bits, and no reason to leave the blocks
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=35)
+    g[5::17] = -1e4
+    out, states = run(b, q, k, v, g, beta, state)
+    g[5::17] = -float("inf")
+    again, states_again = run(b, q, k, v, g, beta, state)
+    assert torch.equal(out, again) and torch.equal(states, states_again)
