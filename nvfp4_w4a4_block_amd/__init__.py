@@ -908,7 +908,7 @@ def _rows_arg(t: torch.Tensor, name: str, dtypes: tuple, gpu: int, rows: int, co
     try:
         n, c = t.shape
         pitch, step = t.stride()
-        if n == rows and c == cols and (step == 1 or n == 0) and t.dtype in dtypes and t.get_device() == gpu:
+        if n == rows and c == cols and (step == 1 or c == 1 or n == 0) and t.dtype in dtypes and t.get_device() == gpu:
             return pitch
     except (AttributeError, TypeError, ValueError):
         raise ValueError(f"{name}: a tensor {_shape_text(rows, cols)}") from None
@@ -916,7 +916,7 @@ def _rows_arg(t: torch.Tensor, name: str, dtypes: tuple, gpu: int, rows: int, co
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {_shape_text(rows, cols)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(x) for x in dtypes)}")
-    if step != 1 and n > 0:
+    if step != 1 and c != 1 and n > 0:
         raise ValueError(f"{name}: rows must be contiguous")
     raise ValueError(f"{name}: on {t.device}, the other tensors are elsewhere")
 
