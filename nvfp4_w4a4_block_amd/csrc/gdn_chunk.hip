@@ -15,10 +15,10 @@
 // That scale rests on the contraction (finite values, g <= 0, 0 <= beta <= 2): a column's 2-norm stays below the
 // running sum B <- e^G B + sum |beta v|.  A block's unit goes by the largest that its bound M can become in it, and leaves
 // 2^-48 M of an element: a token that writes far less than M, or a small state before a large write, would lose its bits to
-// what comes after it.  So where a token writes less than kRange M at most (its largest column of the slice) and the old state
-// has decayed below that by the block's end, or where a block breaks the premise, the scan gives up its slice with a flag, and
-// the token-by-token kernel, which runs behind it, takes the slice from the sequence's start.  (Tokens that write nothing,
-// padding for one, do not count: 2^-48 M is what their outputs are held to.)
+// what comes after it.  So where a token writes less than kRange M at most (its largest column of the slice), and what was
+// there before, old state or the first token's write, has decayed below that by the block's end, or where a block breaks the
+// premise, the scan gives up its slice with a flag, and the token-by-token kernel, which runs behind it, takes the slice from the
+// sequence's start.  (Tokens that write nothing, padding for one, do not count: 2^-48 M is what their outputs are held to.)
 #include <type_traits>
 
 #include "gdn_chunk.h"
@@ -515,7 +515,7 @@ struct Scan {
     float decay[kRing][64];                    // of the whole block, copies; NaN where it is out of the scale's premise
     float norm[KS][NC * 16];
     uint32_t top[3][NC * 16];                  // largest |beta v| of a block, as bits
-    float least[3][4];                         // 16 tokens each: the smallest of their largest |beta v|, zeros aside
+    float least[3];                            // the smallest that a block's tokens write, zeros aside, or the first's rest
     float units[2][2][NC * 16];                // for the output half: ratio, and the block's unit times the scale
   };
 
@@ -607,8 +607,8 @@ struct Scan {
   // updates below three times that.  Between blocks S has a unit by its bound alone, which follows strong decays: to 2^-100 of
   // the block's, so that the ratios stay in range whatever the decay.  The updates go into S in that unit.
   __device__ __forceinline__ void open_block(int b) {
-    const float decay = lds.decay[b % kRing][lane], *tokens = lds.least[b % 3];
-    const float least = __builtin_fminf(__builtin_fminf(tokens[0], tokens[1]), __builtin_fminf(tokens[2], tokens[3]));
+    const float decay = lds.decay[b % kRing][lane];
+    const float least = lds.least[b % 3];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       const float more = 64.0f * __uint_as_float(lds.top[b % 3][nc * 16 + c]);
@@ -887,20 +887,14 @@ struct Scan {
     f_at.next(more);
   }
 
-  // The largest |beta v| of 16 tokens, by column, for the block's units, and the tokens' smallest: read, then written.
+  // The largest |beta v| of 16 tokens, by column, for the block's units: read, then written.
   struct TopRows {
     float4 beta;
     uint32_t v[NC][4];
-    float beta_of;                             // of token lane / 4, a quarter of whose values follows
-    uint32_t row[2 * NC];
   };
   __device__ __forceinline__ void read_top(TopRows& t, int block) {
     const int slot = block % kRing, row = 16 * (w - 4) + 4 * g;
     t.beta = *reinterpret_cast<const float4*>(&lds.rows[slot][0][row]);
-    const int token = 16 * (w - 4) + (lane >> 2);
-    t.beta_of = lds.rows[slot][0][token];
-#pragma unroll
-    for (int i = 0; i < 2 * NC; ++i) t.row[i] = reinterpret_cast<const uint32_t*>(&lds.V[slot][token][(lane & 3) * 4 * NC])[i];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -915,16 +909,29 @@ struct Scan {
       for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(b[r] * __uint_as_float(t.v[nc][r] << 16)) & 0x7FFFFFFFu);
       atomicMax(&lds.top[block % 3][nc * 16 + c], m);
     }
+  }
+
+  // For the check of a block's range, by one wavefront (by all four, a row to four lanes, the scan took 5 % longer): the least that
+  // its tokens write, zeros aside, or what is left of the first one's at the end, if that is more.  A lane has a token and takes
+  // the largest of four columns, which is hardly ever far below the whole row's; where it is 0 the row decides.
+  __device__ __forceinline__ void write_least(int block) {
     typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-    u16x2_t two = {0, 0};
+    const int slot = block % kRing;
+    const float beta = lds.rows[slot][0][lane], decay = lds.decay[slot][lane];
+    auto largest = [&](int part) {             // of four columns, as bits
+      const uint2 v = *reinterpret_cast<const uint2*>(&lds.V[slot][lane][4 * part]);
+      const u16x2_t two = __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, v.x & 0x7FFF7FFFu), __builtin_bit_cast(u16x2_t, v.y & 0x7FFF7FFFu));
+      return (uint32_t)max(two[0], two[1]);
+    };
+    uint32_t most = largest(0);
+    if (__builtin_amdgcn_ballot_w64(most == 0 && beta > 0.0f) != 0) {
 #pragma unroll
-    for (int i = 0; i < 2 * NC; ++i) two = __builtin_elementwise_max(two, __builtin_bit_cast(u16x2_t, t.row[i] & 0x7FFF7FFFu));
-    uint32_t most = max(two[0], two[1]);
-    most = max(most, moved<0xB1>(most));       // of the token's four lanes
-    most = max(most, moved<0x4E>(most));
-    const float m = t.beta_of * __uint_as_float(most << 16);
+      for (int part = 1; part < 4 * NC; ++part) most = max(most, largest(part));
+    }
+    const float m = beta * __uint_as_float(most << 16);
     const uint32_t least = wave_min(m > 0.0f ? __float_as_uint(m) : kNone);
-    if (lane == 63) lds.least[block % 3][w - 4] = __uint_as_float(least);
+    const float first = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m)));
+    if (lane == 63) lds.least[block % 3] = __builtin_fmaxf(__uint_as_float(least), decay * first);
   }
 
   // A U and the stores of a block, its Q S in y.
@@ -1013,6 +1020,7 @@ struct Scan {
     }
     lds_barrier();
     write_top(top, b + 1);
+    if (w == 4) write_least(b + 1);
     load_q(s, b + 3 < blocks);
     if (w == 7 && lane < NC * 16) lds.top[(b + 2) % 3][lane] = 0;
     lds_barrier();
@@ -1038,6 +1046,7 @@ struct Scan {
     TopRows top;
     read_top(top, 0);
     write_top(top, 0);
+    if (w == 4) write_least(0);
     copy_rows(1);
     ring_mark<kLoads>();
     load_q(odd, blocks > 2);

@@ -69,3 +69,27 @@ def test_strengths_near_none(n, size):
     _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=41)
     beta[::3] = 2.0 ** -size
     check(b, q, k, v, g, beta, state)
+
+
+@pytest.mark.parametrize("n", [100, 200])
+def test_closed_gates_beside_weak_decays_stay_in_blocks(n):
+    # strengths of 1e-9 behind the first token: nothing is lost, what was written before is still there.  That the blocks keep
+    # them shows in the states' last bits, which differ from the token-by-token kernel's
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=47)
+    g[:] = -2.0 ** -7
+    beta[1::2] = 1e-9
+    check(b, q, k, v, g, beta, state)
+    blocks, steps = (run(b, q, k, v, g, beta, state, max_q=m)[1][b.slots.long()] for m in (0, 1))
+    assert (blocks != steps).flatten(2).any(2).all()
+
+
+@pytest.mark.parametrize("n", [100, 200])
+def test_slices_out_of_range_are_the_step_kernels(n):
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, 2, 4, 128, 64, seed=49)
+    v = v.clone()
+    v[[40, n + 40], :, 32:] *= 2.0 ** 60
+    blocks, steps = (run(b, q, k, v, g, beta, state, max_q=m)[1][b.slots.long()] for m in (0, 1))
+    assert torch.equal(blocks[..., 32:], steps[..., 32:])
+    assert (blocks != steps)[..., :32].flatten(2).any(2).all()
