@@ -572,7 +572,8 @@ int nvfp4_add_rms_norm(int64_t rows, int64_t cols, const void* x, int x_dtype, i
 /*
  * Norm of each head vector times its output gate, the rows of all heads quantized for the next linear:
  *   y[t, h] = x[t, h] * w / sqrt(mean(x[t, h]^2) + eps) * z[t, h] * sigmoid(z[t, h])
- * in fp32, or with a quantized output in 64 bits, y rounded to fp32 once.
+ * in fp32 (heads whose squares or products that does not hold: in 64 bits), or with a quantized output in 64 bits, y
+ * rounded to fp32 once.  z = infinity gives infinity, z = -infinity NaN (-inf * 0).
  *   head_dim     a power of two, 16 to 1024; heads * head_dim at most 32768 (the cols of the outputs).
  *   x, z         NVFP4_BF16 or NVFP4_F32 each; weight device fp32 [head_dim]; eps >= 0.
  *   tokens >= 0 (0 is a no-op), at most 2^21 - 1.  The outputs must not overlap the inputs.
@@ -623,7 +624,8 @@ int nvfp4_gdn_conv(const nvfp4_seq_states* states, int64_t tokens, int64_t chann
  *   S <- e^g S;  u = beta (v - S^T k^);  S <- S + k^ u^T;  out = scale * S^T q^
  * with q and k of key head h / (v heads / k heads).  One call takes any mix of single tokens, chunks and
  * prompts.  A token has no influence on the tokens before it or on other sequences, whatever its values; a
- * NaN or infinity in it makes its head's state and outputs (in v: those columns) non-finite from it on.
+ * NaN or infinity in it makes its head's state and outputs (in v: those columns) non-finite from it on, but for
+ * g = -infinity, which is a reset (e^g = 0).
  *   states       fp32 [v heads, k_dim, v_dim] per slot, replaced by the state behind the last new token.
  *   q, k         bf16, equal head counts; v, out: bf16, a multiple of q's heads, token strides below 2^24; out must
  *                not overlap the inputs.
@@ -634,7 +636,12 @@ int nvfp4_gdn_conv(const nvfp4_seq_states* states, int64_t tokens, int64_t chann
  *                kernels.  Results do not depend on its truth beyond rounding, speed does.
  *   workspace    device, 16-byte aligned, nvfp4_gated_delta_rule_workspace_size() bytes for the same
  *                arguments; contents need no initialisation and are clobbered.
- * States, sums and norms are fp32.  Deterministic.
+ * States, sums and norms are held to 32 bits, whatever kernel a length goes to, and out is rounded to bf16 once.
+ * Deterministic.  Sequences of more than 16 new tokens go in blocks of 64 tokens.  Where a block has g > 0, beta outside
+ * [0, 2], or tokens whose writes beta v lie further than 2^-28 below the largest values it holds with nothing older left
+ * beside them, the slice of 16 or 32 columns goes token by token from the sequence's start instead: the same results to
+ * rounding, at some 1.5 us a token.  Tokens that write nothing (padding, say) do not count for this: their outputs, and a
+ * state that only decays, are held to 2^-33 of the largest values of the same 64 tokens.
  */
 int nvfp4_gated_delta_rule(const nvfp4_seq_states* states, int64_t tokens, int64_t max_q, int64_t k_dim, int64_t v_dim,
                            const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v, const float* g, const float* beta,
