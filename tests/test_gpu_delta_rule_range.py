@@ -93,3 +93,30 @@ def test_slices_out_of_range_are_the_step_kernels(n):
     blocks, steps = (run(b, q, k, v, g, beta, state, max_q=m)[1][b.slots.long()] for m in (0, 1))
     assert torch.equal(blocks[..., 32:], steps[..., 32:])
     assert (blocks != steps)[..., :32].flatten(2).any(2).all()
+
+
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv", [(2, 40, 128, 128), (3, 72, 64, 64), (1, 2, 64, 32)])
+@pytest.mark.parametrize("case", ["large token", "large column", "forgotten", "padding", "first columns zero", "large behind zeros", "reset"])
+def test_wide_slices_and_short_keys(Hk, Hv, Dk, Dv, case):
+    # more slices of 16 columns than compute units are taken 32 at a time
+    n = 150
+    b = Seqs([n, 40], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, Hk, Hv, Dk, Dv, seed=53)
+    q, k, v = q.clone(), k.clone(), v.clone()
+    if case == "large token":
+        v[[50, n + 20]] *= 2.0 ** 40
+    elif case == "large column":
+        v[[50, n + 20], :, 21] *= 2.0 ** 40
+    elif case == "forgotten":
+        state, g[[70, n + 9]] = state * 2.0 ** 40, -1e4
+    elif case == "padding":
+        for x in (q, k, v):
+            x[20:30], x[64:140], x[n:n + 5] = 0.0, 0.0, 0.0
+    elif case == "first columns zero":
+        v[::2, :, :4], v[1::2, :, 16:20] = 0.0, 0.0
+    elif case == "large behind zeros":         # the first four columns tell nothing of the large token's row
+        v[:, :, :5], v[:, :, 16:21] = 0.0, 0.0
+        v[[50, n + 20]] *= 2.0 ** 40
+    else:
+        state, g[[70, n + 9]], beta[64:] = state * 2.0 ** 60, -1e4, 0.0
+    check(b, q, k, v, g, beta, state)
