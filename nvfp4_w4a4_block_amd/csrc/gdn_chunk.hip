@@ -176,8 +176,8 @@ __device__ __forceinline__ float power2(float x) { return __builtin_amdgcn_exp2f
 // T, A and the row factors of one block for two value heads of one key head: eight wavefronts, four to a value head;
 // wavefront w of four has rows 16 w .. 16 w + 15.  K K^T and Q K^T are both halves' own work, a tenth of
 // what exchanging them would wait for.  Bound by its bytes (q, k in, fragments out) and the latency of the inverse: 8192
-// tokens of 16 and 32 heads of 128, 215 MB, 58 us (3.7 TB/s).  One workgroup that takes block after block with the next
-// one's rows on the way took 70.
+// tokens of 16 and 32 heads of 128, 240 MB, 59 us (4.1 TB/s).  One workgroup that takes block after block with the next
+// one's rows on the way took 70 where this form took 58, before A had a second part.
 constexpr int kPrepareThreads = 512;
 
 template <int DK>
@@ -497,8 +497,8 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
 //   of K S just as the last update left them.  K S over its channels for all tokens; barrier; the sum over the
 //   wavefronts for tokens 16 w .. 16 w + 15, R; barrier; U = T R; barrier; its rows' update.
 //   Output half: Q S of 16 tokens each while the others solve, A U and the stores while they are at the next block.
-// Bound by the chain through the barriers, 2500 cycles a block: 8192 tokens of 32 heads of 128 take 160 us with every
-// compute unit at work and as long with one head on the machine.
+// Bound by the chain through the barriers, 1.3 us or about 3000 cycles a block: 8192 tokens of 32 heads of 128 take 167 us
+// with every compute unit at work and as long with one head on the machine.
 template <int DK, int NC>
 struct Scan {
   static constexpr int KS = DK / 32;
@@ -1104,9 +1104,9 @@ int launch_dk(const DeltaArgs& a, const ChunkWork& ws, int64_t max_q, hipStream_
   if (prepare * kPrepareThreads > (int64_t)UINT32_MAX) return NVFP4_ERR_UNSUPPORTED;
   chunk_prepare_kernel<DK><<<(unsigned)prepare, kPrepareThreads, 0, stream>>>(a, ws);
   if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-  // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.2 us
-  // with 16 columns and 1.9 us with 32 (one sequence of 8192 tokens, 256 slices of 16: 160 against 240 us; eight of
-  // 1023, 2048 slices: 186 against 142).  As many sequences as the tokens give of the longest.
+  // Slices of 16 columns while one round of workgroups holds them all, else of 32: a block of the scan takes 1.3 us
+  // with 16 columns and 2.1 us with 32 (whole calls, one sequence of 8192 tokens, 256 slices of 16: 228 against 324 us; eight
+  // of 1023, 2048 slices: 252 against 212).  As many sequences as the tokens give of the longest.
   const int64_t longest = max_q > a.s.tokens ? a.s.tokens : max_q > kTok ? max_q : kTok;
   const int64_t seqs = (a.s.tokens + longest - 1) / longest;
   const int64_t slices = (seqs < a.s.num_seqs ? seqs : a.s.num_seqs) * a.v_heads * (a.v_dim / 16);

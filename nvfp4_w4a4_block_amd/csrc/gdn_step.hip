@@ -127,9 +127,9 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(DeltaArgs a, int s
 }  // namespace
 
 // Sequences of at most this many new tokens go token by token, the whole call where the longest is known to be no longer.
-// A token's step is 1.4 us where the states fill the machine once, a block about the same for one token as for 64.  By
-// steps against in blocks, us, with 32 heads of 128 x 128: one sequence of 8 tokens 14 / 15, of 17 27 / 16; eight of 16
-// 30 / 34, of 24 42 / 34; 64 of 16 142 / 175, of 24 208 / 179.
+// A token's step is 1.4 us where the states fill the machine once, a block about the same for one token as for 64.  Calls by
+// steps against in blocks, us, with 32 heads of 128 x 128: one sequence of 8 tokens 15 / 21, of 12 21 / 21, of 17 27 / 21;
+// eight of 16 34 / 37, of 20 41 / 37; 64 of 16 153 / 218, of 24 217 / 221.
 constexpr int kShort = 16;
 
 size_t gated_delta_rule_workspace_bytes(int64_t tokens, int64_t max_q, int64_t num_seqs, int64_t k_heads, int64_t v_heads,
