@@ -339,10 +339,10 @@ __global__ __launch_bounds__(kPrepareThreads, 4) void chunk_prepare_kernel(Delta
     // the diagonal block and the rows of A are this wavefront's own: no barrier between them and their use
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
-    half8_t* a_out = reinterpret_cast<half8_t*>(ws.a) + 2 * ((int64_t)block * a.v_heads + head) * kTriFrags * 64;
+    half8_t* a_out = reinterpret_cast<half8_t*>(ws.a) + 2 * ((int64_t)block * a.v_heads + head) * kTriFrags * 64 + lane;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
-      if (ks <= (w >> 1)) (a_out + 2 * tri_frag(w, ks) * 64)[threadIdx.x & 63] = *reinterpret_cast<const half8_t*>(&At[16 * w + c][ks * 32 + g * 8]);
+      if (ks <= (w >> 1)) a_out[2 * tri_frag(w, ks) * 64] = *reinterpret_cast<const half8_t*>(&At[16 * w + c][ks * 32 + g * 8]);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     // they take the first ones' place
@@ -920,7 +920,8 @@ struct Scan {
     const float beta = lds.rows[slot][0][lane], decay = lds.decay[slot][lane];
     auto largest = [&](int part) {             // of four columns, as bits
       const uint2 v = *reinterpret_cast<const uint2*>(&lds.V[slot][lane][4 * part]);
-      const u16x2_t two = __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, v.x & 0x7FFF7FFFu), __builtin_bit_cast(u16x2_t, v.y & 0x7FFF7FFFu));
+      const u16x2_t two = __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, v.x & 0x7FFF7FFFu),
+                                                    __builtin_bit_cast(u16x2_t, v.y & 0x7FFF7FFFu));
       return (uint32_t)max(two[0], two[1]);
     };
     uint32_t most = largest(0);

@@ -7,17 +7,17 @@
 //
 // HBM-bound: every element is read once and written once (calls on inputs in turn: 4096 x 5120 bf16 with residual to NVFP4,
 // 138 MB, 31 us, 4.4 TB/s; gated, 8192 x 4096 to bf16, 201 MB, 37 us, 5.4 TB/s; 30 us on the same inputs every time, which
-// partly stay in the 256 MB cache).  A workgroup takes one row and keeps it in registers, a
-// thread 16 consecutive elements (an NVFP4 block) at a time, so that the statistics, the row's maximum and the
-// encoding need one pass over memory.  Rows of at most 64 blocks share workgroups, as many to a wavefront as it holds.
+// partly stay in the 256 MB cache).  A workgroup takes one row and keeps it in registers, a thread 16 consecutive elements
+// (an NVFP4 block) at a time, so that the statistics, the row's maximum and the encoding need one pass over memory.  Rows
+// of at most 64 blocks share workgroups, as many to a wavefront as it holds.
 //
 // Arithmetic: in 64 bits from the stored r' (x and z) to y: codes of values next to a rounding border do not depend on the
 // order of a sum.  The NVFP4 bytes are the quantizer's of fl32(y), the FP8 bytes the values nearest to y / scale, with one
 // rounding and, per row, max|y| / 448 before its own to fp32 (quotients of fl32(y) in fp32 put one byte in about three
-// million on a border's other side; 2049 x 4096 fp32: 12 us, 11 that way).  gated_rms_norm without a quantized output works in fp32, which hides its
-// exponential behind the loads, but for heads that fp32 does not hold (8192 tokens of 32 heads of 128, inputs in turn, bf16 output:
-// 37 us; on the same inputs 30, 58 in 64 bits; NVFP4 output, in 64 bits: 57 us, FP8 62 us, bound by their thousand
-// instructions, half of them of 64 bits, for 16 elements).
+// million on a border's other side; 2049 x 4096 fp32: 12 us, 11 that way).  gated_rms_norm without a quantized output works
+// in fp32, which hides its exponential behind the loads, but for heads that fp32 does not hold (8192 tokens of 32 heads of
+// 128, inputs in turn, bf16 output: 37 us; on the same inputs 30, 58 in 64 bits; NVFP4 output, in 64 bits: 57 us, FP8
+// 62 us, bound by their thousand instructions, half of them of 64 bits, for 16 elements).
 #include <type_traits>
 
 #include "fp8_device.h"

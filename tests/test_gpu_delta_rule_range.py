@@ -120,3 +120,18 @@ def test_wide_slices_and_short_keys(Hk, Hv, Dk, Dv, case):
     else:
         state, g[[70, n + 9]], beta[64:] = state * 2.0 ** 60, -1e4, 0.0
     check(b, q, k, v, g, beta, state)
+
+
+@pytest.mark.parametrize("n", [9, 100])
+@pytest.mark.parametrize("size", [40, 80, 100, 110, 116])
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv", [(2, 4, 128, 64), (2, 40, 128, 128)])
+def test_small_values_are_large_ones_scaled(n, size, Hk, Hv, Dk, Dv):
+    # the rule is linear in v and the state, and a power of two changes no bits but where numbers end: two outputs are apart by
+    # the two roundings to bf16 (2^-8 each), 32-bit arithmetic (2^-15 of the largest) and bf16's smallest step, states by that alone
+    b = Seqs([n, n], [4, 0])
+    _, q, k, v, g, beta, state = delta_inputs(b, Hk, Hv, Dk, Dv, seed=55)
+    out, states = (x.double().cpu() for x in run(b, q, k, v, g, beta, state))
+    small, small_states = (x.double().cpu() for x in run(b, q, k, (v.float() * 2.0 ** -size).bfloat16(), g, beta, state * 2.0 ** -size))
+    f = 2.0 ** -size
+    assert_within(small, out * f, 2.0 ** -7 * out.abs() * f + 2.0 ** -15 * out.abs().amax() * f + 2.0 ** -133)
+    assert_within(small_states, states * f, 2.0 ** -18 * states.abs().amax() * f + 2.0 ** -148)
