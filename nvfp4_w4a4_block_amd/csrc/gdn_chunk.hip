@@ -565,9 +565,10 @@ struct Scan {
     lo = half8_t{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
   }
 
-  // The power of two that takes x < 2^100 below 2^13, and its inverse.
+  // The power of two that takes x < 2^100 below 2^13, and its inverse: 2^-107 at least, so that it is a normal number times the
+  // outputs' scale and 1 / kTri, too, and no output's error is above 2^-140 for that.
   __device__ __forceinline__ static void unit(float x, float& up, float& down) {
-    const uint32_t e = max(min(__float_as_uint(x) >> 23, 226u), 20u);
+    const uint32_t e = max(min(__float_as_uint(x) >> 23, 226u), 32u);
     up = __uint_as_float((266u - e) << 23);
     down = __uint_as_float((e - 12u) << 23);
   }
